@@ -321,8 +321,7 @@ def _plain_plan(s):
         outs["mask"] = torch.where((t < cu[-1])[:, None], mask, 0)
     positions = torch.where(t < cu[-1], ctx[row] + depth, -1)
     head = s["head"] + torch.where(fits, need, 0).sum(dtype=torch.int32)
-    zero = torch.zeros_like(head)
-    counts = torch.cat([cu[-1:], head, (~fits).sum(dtype=torch.int32)[None], zero])
+    counts = torch.cat([cu[-1:], head, (~fits).sum(dtype=torch.int32)[None]])
     return {"table": table, "cu": cu, "slots": slots, "positions": positions, "counts": counts} | outs
 
 
@@ -453,7 +452,7 @@ def _exact_plan(s):
             if ok:
                 slots[start + i] = table[b, (c + i) // block] * block + (c + i) % block
     outs = {"table": table.astype(np.int32), "cu": np.array(cu, np.int32), "slots": slots.astype(np.int32),
-            "positions": positions.astype(np.int32), "counts": np.array([cu[-1], head, refused, 0], np.int32)}
+            "positions": positions.astype(np.int32), "counts": np.array([cu[-1], head, refused], np.int32)}
     return outs | ({"mask": mask.view(np.int64)} if parents is not None else {})
 
 
