@@ -26,7 +26,11 @@ STATUS = {0: "DGT_OK", -1: "DGT_E_ARG", -2: "DGT_E_SHAPE", -3: "DGT_E_ALPHABET",
 EXPORTS = ["dgt_version", "dgt_status_string", "dgt_compress_bound", "dgt_compress_layer",
            "dgt_layer_info", "dgt_decode_tiles", "dgt_gemm_workspace",
            "dgt_fused_decode_gemm", "dgt_dense_workspace", "dgt_dense_gemm",
-           "dgt_noalloc_scratch_bytes", "dgt_fused_decode_gemm_noalloc"]
+           "dgt_noalloc_scratch_bytes", "dgt_fused_decode_gemm_noalloc",
+           "dgt_page_plan", "dgt_kv_store", "dgt_tree_attention_workspace", "dgt_tree_attention",
+           "dgt_lora_workspace", "dgt_lora_add"]
+# element types of the serving operators
+DGT_ELT_BF16, DGT_ELT_F16, DGT_ELT_F32 = 1, 2, 3
 
 
 class DgtError(RuntimeError):
@@ -91,6 +95,24 @@ def lib():
         L.dgt_dense_gemm.restype = ctypes.c_int
         L.dgt_dense_gemm.argtypes = [u32, u32, u32, u32, vp, vp, u32, vp, ctypes.c_float, vp,
                                      vp, sz, vp]
+        i64, u64 = ctypes.c_int64, ctypes.c_uint64
+        L.dgt_page_plan.restype = ctypes.c_int
+        L.dgt_page_plan.argtypes = [vp, vp, u32, vp, u32, vp, vp, u32, u32, u32, u32, vp, u32, vp,
+                                    vp, vp, vp, vp, vp]
+        L.dgt_kv_store.restype = ctypes.c_int
+        L.dgt_kv_store.argtypes = [vp, vp, u32, i64, i64, i64, i64, vp, u32, u32, u32, u32, vp, vp,
+                                   u32, u32, vp]
+        L.dgt_tree_attention_workspace.restype = sz
+        L.dgt_tree_attention_workspace.argtypes = [u32, u32, u32, u32, u32]
+        L.dgt_tree_attention.restype = ctypes.c_int
+        L.dgt_tree_attention.argtypes = [u32, vp, u64, u64, vp, vp, u32, u32, vp, u32, vp, vp, u32,
+                                         u32, u32, u32, u32, vp, u32, ctypes.c_float, vp, u64, u64,
+                                         vp, sz, vp]
+        L.dgt_lora_workspace.restype = sz
+        L.dgt_lora_workspace.argtypes = [u32, u32, u32, u32, u32]
+        L.dgt_lora_add.restype = ctypes.c_int
+        L.dgt_lora_add.argtypes = [vp, u64, vp, u64, vp, vp, vp, u32, vp, vp, u32, u32, u32, u32,
+                                   u32, vp, u64, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -334,3 +356,245 @@ def dgt_dense_gemm(fmt, w, x, tile_n=128, scales=None, w_scale=1.0, y=None, ws=N
                                 float(w_scale), _ptr(y), _ptr(ws), ws.numel(),
                                 _stream(stream)), "dgt_dense_gemm")
     return y
+
+
+# --------------------------------------------------------- serving operators
+# Their smallest calls take a few microseconds on the GPU, so the checks below
+# are single comparisons while all is well and only then spell out what is not.
+def _check_array(t, name, dtype, shape, device):
+    """t must be a contiguous tensor of `dtype` and exactly `shape` on `device`."""
+    if not (t is not None and getattr(t, "dtype", None) is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        _check_tensor(t, name, shape, (str(dtype),), device)
+
+
+def _check_rows(t, name, dtypes, shape, device):
+    """t must be a tensor of one of `dtypes` and exactly `shape` on `device` whose last
+    dimension is contiguous; the other strides are free."""
+    if t is not None and getattr(t, "dtype", None) in dtypes and t.shape == shape \
+            and t.device == device and (t.stride(-1) == 1 or shape[-1] <= 1):
+        return
+    _need(t is not None, "%s is required" % name)
+    _need(hasattr(t, "data_ptr"), "%s must be a tensor" % name)
+    _need(t.dtype in dtypes, "%s has dtype %s, expected one of %s"
+          % (name, t.dtype, ", ".join(str(d) for d in dtypes)))
+    _need(t.shape == shape, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    _need(t.stride(-1) == 1, "%s must be contiguous in its last dimension" % name)
+    _need(t.device == device, "%s is on %s, expected %s" % (name, t.device, device))
+
+
+def _dims(t, name, count):
+    _need(hasattr(t, "data_ptr") and t.dim() == count, "%s must be a %d-D tensor" % (name, count))
+    return t.shape
+
+
+def _made_on(stream, make):
+    """Tensors made inside a call belong to the stream the call runs on, so their memory
+    is not handed on while that stream still uses it."""
+    import torch
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _call(name, device, stream, *args):
+    """One library call on `stream` (default: the device's current stream), with
+    `device` as the current device."""
+    import torch
+    fn = getattr(lib(), name)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            code = fn(*args, _stream(stream))
+    else:
+        code = fn(*args, _stream(stream))
+    if code:
+        raise DgtError(code, name)
+
+
+class PagePlan:
+    """What dgt_page_plan returns, on the device: cu int32[requests + 1], slots and
+    positions int32[tokens], counts int32[3] (rows needed, the free list's new head,
+    requests refused) and, for trees, mask int64[tokens, mask_words] (else None)."""
+
+    __slots__ = ("cu", "slots", "positions", "counts", "mask")
+
+    def __init__(self, cu, slots, positions, counts, mask=None):
+        self.cu, self.slots, self.positions, self.counts, self.mask = cu, slots, positions, counts, mask
+
+    @classmethod
+    def empty(cls, requests, tokens, mask_words=0, device="cuda"):
+        import torch
+        def i32(n):
+            return torch.empty(n, dtype=torch.int32, device=device)
+        mask = torch.empty((tokens, mask_words), dtype=torch.int64, device=device) if mask_words else None
+        return cls(i32(requests + 1), i32(tokens), i32(tokens), i32(3), mask)
+
+
+def dgt_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, block_size, num_blocks,
+                  tokens, parents=None, mask_words=0, out=None, stream=None):
+    """Offsets, slots, positions and tree masks of one step, and the pages it takes from
+    the free list (written into block_table).  parents: int32[tokens] for drafted trees,
+    with mask_words 64-bit words a token (default: one); None for chains.  out: a PagePlan
+    to write into.  out.counts[1:2] is the next step's free_head."""
+    import torch
+    i32, dev = torch.int32, ctx_lens.device
+    (requests,) = _dims(ctx_lens, "ctx_lens", 1)
+    (free,) = _dims(free_blocks, "free_blocks", 1)
+    width = _dims(block_table, "block_table", 2)[1]
+    tokens, words = int(tokens), int(mask_words)
+    if parents is not None:
+        words = words or 1
+    _check_array(ctx_lens, "ctx_lens", i32, (requests,), dev)
+    _check_array(new_lens, "new_lens", i32, (requests,), dev)
+    _check_array(free_blocks, "free_blocks", i32, (free,), dev)
+    _check_array(free_head, "free_head", i32, (1,), dev)
+    _check_array(block_table, "block_table", i32, (requests, width), dev)
+    _need(tokens >= 0 and words >= 0, "tokens and mask_words must not be negative")
+    if parents is not None:
+        _check_array(parents, "parents", i32, (tokens,), dev)
+    else:
+        _need(words == 0, "mask_words needs parents")
+    if out is not None:
+        _check_array(out.cu, "out.cu", i32, (requests + 1,), dev)
+        _check_array(out.slots, "out.slots", i32, (tokens,), dev)
+        _check_array(out.positions, "out.positions", i32, (tokens,), dev)
+        _check_array(out.counts, "out.counts", i32, (3,), dev)
+        if words:
+            _check_array(out.mask, "out.mask", torch.int64, (tokens, words), dev)
+    _check_gpu(dev)
+    if out is None:
+        out = _made_on(stream, lambda: PagePlan.empty(requests, tokens, words, dev))
+    # (a step of no tokens still has parents, if only by name)
+    up = None if parents is None else parents.data_ptr() or out.counts.data_ptr()
+    _call("dgt_page_plan", dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), requests,
+          free_blocks.data_ptr(), free, free_head.data_ptr(), block_table.data_ptr(), width,
+          block_size, num_blocks, tokens, up, words, out.cu.data_ptr(), out.slots.data_ptr(),
+          out.positions.data_ptr(), out.mask.data_ptr() if words else None, out.counts.data_ptr())
+    return out
+
+
+def _elements(t):
+    import torch
+    return {torch.bfloat16: DGT_ELT_BF16, torch.float16: DGT_ELT_F16, torch.float32: DGT_ELT_F32}.get(t.dtype)
+
+
+def _check_caches(k_cache, v_cache):
+    """Shape (blocks, heads, block, dim) of the key pages; the value pages are the same,
+    transposed."""
+    import torch
+    blocks, heads, block, dim = _dims(k_cache, "k_cache", 4)
+    dtype = k_cache.dtype
+    _need(dtype is torch.bfloat16 or dtype is torch.float16,
+          "k_cache has dtype %s, expected torch.bfloat16 or torch.float16" % dtype)
+    _check_array(k_cache, "k_cache", dtype, (blocks, heads, block, dim), k_cache.device)
+    _check_array(v_cache, "v_cache", dtype, (blocks, heads, dim, block), k_cache.device)
+    return blocks, heads, block, dim
+
+
+def dgt_kv_store(k, v, slots, k_cache, v_cache, stream=None):
+    """Write k, v [tokens, heads, dim] (the caches' dtype or float32, any row and head
+    strides) into the pages at `slots`; slots outside the pool are skipped."""
+    import torch
+    blocks, heads, block, dim = _check_caches(k_cache, v_cache)
+    dev = k_cache.device
+    tokens = _dims(k, "k", 3)[0]
+    dtypes = (torch.float32, k_cache.dtype)
+    _check_rows(k, "k", dtypes, (tokens, heads, dim), dev)
+    _check_rows(v, "v", (k.dtype,), (tokens, heads, dim), dev)
+    _check_array(slots, "slots", torch.int32, (tokens,), dev)
+    _check_gpu(dev)
+    _call("dgt_kv_store", dev, stream, k.data_ptr(), v.data_ptr(), _elements(k), k.stride(0),
+          k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(), tokens, heads, dim,
+          _elements(k_cache), k_cache.data_ptr(), v_cache.data_ptr(), blocks, block)
+
+
+def dgt_tree_attention_workspace(q_shape, kv_heads, requests) -> int:
+    """Bytes of workspace for queries of shape [tokens, heads, dim]."""
+    tokens, heads, dim = q_shape
+    n = lib().dgt_tree_attention_workspace(tokens, heads, kv_heads, dim, requests)
+    if n == 0:
+        raise DgtError(-2, "dgt_tree_attention_workspace")
+    return n
+
+
+def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None, scale=None,
+                       out=None, ws=None, stream=None):
+    """Attention of the new tokens q [tokens, heads, dim] over each request's cached tokens
+    and over those of its new tokens (already stored) that `mask` (dgt_page_plan) lets a
+    token see; without a mask each sees the ones before it and itself.  scale defaults to
+    dim ** -0.5.  Rows past cu[-1] of `out` are not written."""
+    import torch
+    blocks, kv_heads, block, dim = _check_caches(k_cache, v_cache)
+    dev = k_cache.device
+    tokens, heads, _ = _dims(q, "q", 3)
+    requests, width = _dims(block_table, "block_table", 2)
+    _check_rows(q, "q", (k_cache.dtype,), (tokens, heads, dim), dev)
+    _need(heads % max(kv_heads, 1) == 0, "q has %d heads, not a multiple of the cache's %d" % (heads, kv_heads))
+    _check_array(block_table, "block_table", torch.int32, (requests, width), dev)
+    _check_array(ctx_lens, "ctx_lens", torch.int32, (requests,), dev)
+    _check_array(cu, "cu", torch.int32, (requests + 1,), dev)
+    words = 0
+    if mask is not None:
+        words = _dims(mask, "mask", 2)[1]
+        _need(words > 0, "mask needs at least one word a token")
+        _check_array(mask, "mask", torch.int64, (tokens, words), dev)
+    if out is not None:
+        _check_rows(out, "out", (q.dtype,), (tokens, heads, dim), dev)
+    if ws is not None:
+        _check_array(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    _check_gpu(dev)
+    if out is None:
+        out = _made_on(stream, lambda: torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev))
+    if ws is None:
+        nbytes = dgt_tree_attention_workspace(q.shape, kv_heads, requests)
+        ws = _made_on(stream, lambda: alloc_workspace(nbytes, dev))
+    _call("dgt_tree_attention", dev, stream, _elements(q), q.data_ptr(), q.stride(0), q.stride(1),
+          k_cache.data_ptr(), v_cache.data_ptr(), blocks, block, block_table.data_ptr(), width,
+          ctx_lens.data_ptr(), cu.data_ptr(), requests, tokens, heads, kv_heads, dim,
+          mask.data_ptr() if words and tokens else None, words if tokens else 0,
+          dim ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1),
+          ws.data_ptr(), ws.numel())
+    return out
+
+
+def dgt_lora_workspace(tokens, requests, n, k, rank) -> int:
+    nbytes = lib().dgt_lora_workspace(tokens, requests, n, k, rank)
+    if nbytes == 0:
+        raise DgtError(-2, "dgt_lora_workspace")
+    return nbytes
+
+
+def dgt_lora_add(y, x, a, b, scaling, adapters, cu, out=None, ws=None, stream=None):
+    """out[t] = y[t] + scaling[i] * (x[t] a[i]^T) b[i]^T, i = adapters[request of t] (rows of
+    requests with an id outside the adapters: out[t] = y[t]).  x bf16 [tokens, k],
+    a bf16 [count, rank, k], b bf16 [count, n, rank], y float32 [tokens, n].  out defaults
+    to y (in place)."""
+    import torch
+    dev = y.device
+    tokens, n = _dims(y, "y", 2)
+    k = _dims(x, "x", 2)[1]
+    count, rank, _ = _dims(a, "a", 3)
+    (requests,) = _dims(adapters, "adapters", 1)
+    f32, bf16 = torch.float32, torch.bfloat16
+    _check_rows(y, "y", (f32,), (tokens, n), dev)
+    _check_rows(x, "x", (bf16,), (tokens, k), dev)
+    _check_array(a, "a", bf16, (count, rank, k), dev)
+    _check_array(b, "b", bf16, (count, n, rank), dev)
+    _check_array(scaling, "scaling", f32, (count,), dev)
+    _check_array(adapters, "adapters", torch.int32, (requests,), dev)
+    _check_array(cu, "cu", torch.int32, (requests + 1,), dev)
+    if out is None:
+        out = y
+    else:
+        _check_rows(out, "out", (f32,), (tokens, n), dev)
+    if ws is not None:
+        _check_array(ws, "ws", torch.uint8, (ws.numel(),), dev)
+    _check_gpu(dev)
+    if ws is None:
+        nbytes = dgt_lora_workspace(tokens, requests, n, k, rank)
+        ws = _made_on(stream, lambda: torch.empty(nbytes, dtype=torch.uint8, device=dev))
+    _call("dgt_lora_add", dev, stream, y.data_ptr(), y.stride(0), x.data_ptr(), x.stride(0),
+          a.data_ptr(), b.data_ptr(), scaling.data_ptr(), count, adapters.data_ptr(), cu.data_ptr(),
+          requests, tokens, n, k, rank, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel())
+    return out

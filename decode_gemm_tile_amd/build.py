@@ -22,6 +22,8 @@ HIP_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-result",
 ]
+# sources of one object each: the decode-GEMM entry points and the serving operators
+SOURCES = ("dgt_api", "dgt_pages", "dgt_tree_attn", "dgt_lora")
 FORMATS = {"int8": 1, "int4": 2, "fp8": 3, "bf16": 4, "int4p": 5, "bf16e": 6, "bf16p": 7,
            "bf16w": 8}
 
@@ -67,9 +69,10 @@ def build(verbose: bool = False, jobs: int = None, incremental: bool = False) ->
         steps.append([hipcc] + HIP_FLAGS + [f"-DDGT_FMT={val}", "-c",
                                             os.path.join(CSRC, "dgt_fmt.hip"), "-o", obj])
         objs.append(obj)
-    api_obj = os.path.join(BUILD, "dgt_api.o")
-    steps.append([hipcc] + HIP_FLAGS + ["-c", os.path.join(CSRC, "dgt_api.hip"), "-o", api_obj])
-    objs.append(api_obj)
+    for name in SOURCES:
+        obj = os.path.join(BUILD, f"{name}.o")
+        steps.append([hipcc] + HIP_FLAGS + ["-c", os.path.join(CSRC, f"{name}.hip"), "-o", obj])
+        objs.append(obj)
     if incremental:
         steps = [c for c in steps if _stale(c[-1], c[-3])]
     with cf.ThreadPoolExecutor(jobs) as ex:

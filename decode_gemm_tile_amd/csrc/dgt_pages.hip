@@ -1,0 +1,316 @@
+// Page plan of a serving step and the store of new keys and values into the
+// paged cache.
+#include "dgt_serve.h"
+
+#include <algorithm>
+
+namespace dgt {
+namespace serve {
+namespace {
+
+// ------------------------------------------------------------------ page plan
+// Two exclusive sums over the requests (their new tokens, and the pages they
+// still need) and then one independent computation per new token.  The sums are
+// a few microseconds of latency and no work, so every workgroup forms them for
+// itself in LDS and goes on to its own tokens: one launch, no hand-off.
+struct PlanArgs {
+  const int32_t *ctx, *fresh_tokens, *free_list, *free_head, *parents;
+  int32_t *table, *cu, *slots, *positions, *counts;
+  uint64_t* mask;
+  uint32_t requests, free_len, width, log_block, blocks, tokens, words;
+};
+
+constexpr uint32_t kPlanThreads = 256;
+
+struct Request {
+  uint32_t ctx, have;  // tokens and pages in the cache
+  uint32_t need;       // pages to take from the free list
+  bool wide;           // the table has a column for every page
+};
+
+__device__ __forceinline__ Request plan_request(const PlanArgs& p, uint32_t b) {
+  Request r;
+  r.ctx = (uint32_t)max(p.ctx[b], 0);
+  const uint32_t n = (uint32_t)max(p.fresh_tokens[b], 0);
+  const uint32_t round = (1u << p.log_block) - 1;
+  r.have = (r.ctx + round) >> p.log_block;  // both below 2^31: no carry out of 32 bits
+  const uint32_t after = (uint32_t)(((uint64_t)r.ctx + n + round) >> p.log_block);
+  r.wide = after <= p.width;
+  r.need = r.wide ? after - r.have : 0u;
+  return r;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void k_page_plan(PlanArgs p) {
+  extern __shared__ uint32_t lds[];
+  uint32_t* s_cu = lds;                        // [requests + 1] token offsets
+  uint32_t* s_end = lds + p.requests + 1;      // [requests] pages needed up to and with b
+  __shared__ uint32_t s_tok[kPlanThreads / 64], s_page[kPlanThreads / 64], s_out[2];
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  // Sums stop growing one past what fits, so that no input overflows them:
+  // min(a + b, cap) over non-negative numbers is associative.
+  const uint32_t tok_cap = p.tokens + 1, page_cap = p.free_len + 1;
+  uint32_t tok_base = 0, page_base = 0;
+  for (uint32_t b0 = 0; b0 < p.requests; b0 += kPlanThreads) {
+    const uint32_t b = b0 + t;
+    uint32_t tok = 0, page = 0;
+    if (b < p.requests) {
+      tok = min((uint32_t)max(p.fresh_tokens[b], 0), tok_cap);
+      page = min(plan_request(p, b).need, page_cap);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t to = __shfl_up(tok, d, 64), po = __shfl_up(page, d, 64);
+      if (lane >= (uint32_t)d) {
+        tok = min(tok + to, tok_cap);
+        page = min(page + po, page_cap);
+      }
+    }
+    if (lane == 63) {
+      s_tok[wave] = tok;
+      s_page[wave] = page;
+    }
+    __syncthreads();
+    uint32_t tb = tok_base, pb = page_base;
+    for (uint32_t w = 0; w < kPlanThreads / 64; ++w) {
+      if (w == wave) {
+        tok = min(tok + tb, tok_cap);
+        page = min(page + pb, page_cap);
+      }
+      tb = min(tb + s_tok[w], tok_cap);
+      pb = min(pb + s_page[w], page_cap);
+    }
+    tok_base = tb;
+    page_base = pb;
+    if (b < p.requests) {
+      s_cu[b + 1] = tok;
+      s_end[b] = page;
+    }
+    __syncthreads();  // s_tok and s_page are rewritten by the next round
+  }
+  if (t == 0) s_cu[0] = 0;
+  if (t < 2) s_out[t] = 0;
+  __syncthreads();
+
+  const uint32_t head = (uint32_t)max(*p.free_head, 0);
+  const uint32_t left = head < p.free_len ? p.free_len - head : 0u;
+  // b keeps its tokens if its pages have columns, its rows exist and, where it
+  // needs pages, the list still holds them.
+  auto fits = [&](uint32_t b, const Request& r) {
+    return r.wide && s_cu[b + 1] <= p.tokens && (r.need == 0 || s_end[b] <= left);
+  };
+  if (blockIdx.x == 0) {
+    uint32_t refused = 0, taken = 0;
+    for (uint32_t b = t; b < p.requests; b += kPlanThreads) {
+      const Request r = plan_request(p, b);
+      const bool ok = fits(b, r);
+      if (!ok) refused += 1;
+      if (ok && r.need) taken = max(taken, s_end[b]);
+    }
+    if (refused) atomicAdd(&s_out[0], refused);  // whole numbers: any order gives the same
+    if (taken) atomicMax(&s_out[1], taken);
+    for (uint32_t b = t; b <= p.requests; b += kPlanThreads)
+      p.cu[b] = (int32_t)min(s_cu[b], p.tokens);
+    __syncthreads();
+    if (t == 0) {
+      p.counts[0] = (int32_t)s_cu[p.requests];
+      p.counts[1] = (int32_t)(head + s_out[1]);
+      p.counts[2] = (int32_t)s_out[0];
+    }
+  }
+
+  const uint32_t total = min(s_cu[p.requests], p.tokens), block = 1u << p.log_block;
+  for (uint64_t t64 = (uint64_t)blockIdx.x * kPlanThreads + t; t64 < p.tokens;
+       t64 += (uint64_t)gridDim.x * kPlanThreads) {
+    const uint32_t tok = (uint32_t)t64;
+    uint64_t* row = p.mask ? p.mask + (uint64_t)tok * p.words : nullptr;
+    int32_t slot = -1, position = -1;
+    uint32_t lowest = p.words;  // mask words from here on are written
+    if (tok < total) {
+      // the last request whose first row is at or before tok
+      uint32_t lo = 0, hi = p.requests;  // s_cu[lo] <= tok < s_cu[hi]
+      while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        if (s_cu[mid] <= tok) lo = mid; else hi = mid;
+      }
+      const uint32_t b = lo, at = tok - s_cu[b];
+      const Request r = plan_request(p, b);
+      const uint32_t pos = r.ctx + at;
+      bool sound = true;
+      uint32_t depth = at;
+      if (p.parents) {
+        // Walk to the root.  Parents lie before their children, so the walk ends
+        // and meets mask words from the last to the first.
+        const int32_t* par = p.parents + s_cu[b];
+        depth = 0;
+        sound = at < p.words * 64u;
+        int32_t node = (int32_t)at;
+        uint64_t bits = 0;
+        uint32_t word = at >> 6;
+        lowest = sound ? word + 1 : p.words;
+        if (row) for (uint32_t w = lowest; w < p.words; ++w) row[w] = 0;
+        while (sound) {
+          if ((uint32_t)node >> 6 != word) {
+            row[word] = bits;
+            lowest = word;
+            bits = 0;
+            while (--word > (uint32_t)node >> 6) row[lowest = word] = 0;
+          }
+          bits |= 1ull << (node & 63);
+          const int32_t up = par[node];
+          if (up == -1) break;
+          sound = up >= 0 && up < node;
+          node = up;
+          ++depth;
+        }
+        if (sound) {
+          row[word] = bits;
+          lowest = word;
+        } else {
+          lowest = p.words;  // a bad link: the row sees nothing
+        }
+      }
+      if (sound) position = (int32_t)(r.ctx + depth);
+      if (fits(b, r)) {
+        const uint32_t page = pos >> p.log_block;
+        uint32_t id;
+        if (page >= r.have) {
+          id = (uint32_t)p.free_list[head + s_end[b] - r.need + (page - r.have)];
+          if ((pos & (block - 1)) == 0) p.table[(uint64_t)b * p.width + page] = (int32_t)id;
+        } else {
+          id = (uint32_t)p.table[(uint64_t)b * p.width + page];
+        }
+        if (sound && id < p.blocks) slot = (int32_t)((id << p.log_block) + (pos & (block - 1)));
+      }
+    }
+    p.slots[tok] = slot;
+    p.positions[tok] = position;
+    if (row) for (uint32_t w = 0; w < lowest; ++w) row[w] = 0;
+  }
+}
+
+// ---------------------------------------------------------------- cache store
+// Key rows are copied into their page as they are; value rows go in transposed,
+// one element per value row of the page.
+struct StoreArgs {
+  const void *k, *v;
+  const int32_t* slots;
+  void *kc, *vc;
+  int64_t k_row, k_head, v_row, v_head;  // element strides of k and v
+  uint32_t tokens, heads, dim, log_block, blocks;
+};
+
+template <typename E, typename S>
+__device__ __forceinline__ uint16_t to_cache(S v) {
+  if constexpr (sizeof(S) == 2) return __builtin_bit_cast(uint16_t, v);
+  else return (uint16_t)E::pack2(v, 0.f);
+}
+
+template <typename E, typename S>
+__global__ __launch_bounds__(256) void k_kv_store(StoreArgs a) {
+  const uint32_t tok = blockIdx.x;
+  const uint32_t slot = (uint32_t)a.slots[tok];
+  if (slot >= a.blocks << a.log_block) return;
+  const uint32_t block = 1u << a.log_block, page = slot >> a.log_block, cell = slot & (block - 1);
+  const S* k = static_cast<const S*>(a.k) + (int64_t)tok * a.k_row;
+  const S* v = static_cast<const S*>(a.v) + (int64_t)tok * a.v_row;
+  for (uint32_t i = threadIdx.x; i < a.heads * a.dim; i += blockDim.x) {
+    const uint32_t h = i / a.dim, d = i % a.dim;
+    const uint64_t base = ((uint64_t)page * a.heads + h) * block * a.dim;
+    static_cast<uint16_t*>(a.kc)[base + (uint64_t)cell * a.dim + d] =
+        to_cache<E, S>(k[(int64_t)h * a.k_head + d]);
+    static_cast<uint16_t*>(a.vc)[base + (uint64_t)d * block + cell] =
+        to_cache<E, S>(v[(int64_t)h * a.v_head + d]);
+  }
+}
+
+}  // namespace
+}  // namespace serve
+}  // namespace dgt
+
+using namespace dgt::serve;
+
+extern "C" {
+
+int dgt_page_plan(const int32_t* d_ctx, const int32_t* d_new, uint32_t requests,
+                  const int32_t* d_free, uint32_t free_len, const int32_t* d_free_head,
+                  int32_t* d_table, uint32_t width, uint32_t block, uint32_t blocks,
+                  uint32_t tokens, const int32_t* d_parents, uint32_t mask_words, int32_t* d_cu,
+                  int32_t* d_slots, int32_t* d_positions, uint64_t* d_mask, int32_t* d_counts,
+                  void* stream) {
+  if (!block_ok(block) || !pool_ok(blocks, block)) return DGT_E_SHAPE;
+  if (requests > kMaxRequests || tokens > (1u << 28) || free_len > (1u << 30) ||
+      (uint64_t)width * block > 0x7FFFFFFFull || mask_words > 1024)
+    return DGT_E_SHAPE;
+  if (!d_cu || !d_counts || !d_free_head || (free_len && !d_free)) return DGT_E_ARG;
+  if (requests && (!d_ctx || !d_new || (width && !d_table))) return DGT_E_ARG;
+  if (tokens && (!d_slots || !d_positions)) return DGT_E_ARG;
+  // a tree comes with its masks and masks with their tree
+  if ((mask_words != 0) != (d_parents != nullptr) || (mask_words && tokens && !d_mask)) return DGT_E_ARG;
+  PlanArgs p;
+  p.ctx = d_ctx;
+  p.fresh_tokens = d_new;
+  p.free_list = d_free;
+  p.free_head = d_free_head;
+  p.parents = d_parents;
+  p.table = d_table;
+  p.cu = d_cu;
+  p.slots = d_slots;
+  p.positions = d_positions;
+  p.counts = d_counts;
+  p.mask = mask_words ? d_mask : nullptr;
+  p.requests = requests;
+  p.free_len = free_len;
+  p.width = width;
+  p.log_block = (uint32_t)__builtin_ctz(block);
+  p.blocks = blocks;
+  p.tokens = tokens;
+  p.words = mask_words;
+  const uint32_t lds = (2 * requests + 1) * 4;
+  if (lds > 64 * 1024 &&
+      hipFuncSetAttribute(reinterpret_cast<const void*>(k_page_plan),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+    return DGT_E_HIP;
+  const uint32_t grid = std::min(std::max((tokens + kPlanThreads - 1) / kPlanThreads, 1u), 4 * kCUs);
+  hipLaunchKernelGGL(k_page_plan, dim3(grid), dim3(kPlanThreads), lds,
+                     static_cast<hipStream_t>(stream), p);
+  return launched();
+}
+
+int dgt_kv_store(const void* d_k, const void* d_v, uint32_t source, int64_t k_row, int64_t k_head,
+                 int64_t v_row, int64_t v_head, const int32_t* d_slots, uint32_t tokens,
+                 uint32_t heads, uint32_t dim, uint32_t cache, void* d_k_cache, void* d_v_cache,
+                 uint32_t blocks, uint32_t block, void* stream) {
+  if (!block_ok(block) || !pool_ok(blocks, block) || heads == 0 || dim == 0 || dim % 8 ||
+      dim > 1024 || heads > 65535 || tokens > (1u << 28))
+    return DGT_E_SHAPE;
+  if (cache != DGT_ELT_BF16 && cache != DGT_ELT_F16) return DGT_E_UNSUPPORTED;
+  if (source != DGT_ELT_F32 && source != cache) return DGT_E_UNSUPPORTED;
+  if (tokens == 0 || blocks == 0) return DGT_OK;
+  if (!d_k || !d_v || !d_slots || !d_k_cache || !d_v_cache) return DGT_E_ARG;
+  if (!aligned(d_k_cache, 16) || !aligned(d_v_cache, 16)) return DGT_E_ARG;
+  StoreArgs a;
+  a.k = d_k;
+  a.v = d_v;
+  a.slots = d_slots;
+  a.kc = d_k_cache;
+  a.vc = d_v_cache;
+  a.k_row = k_row;
+  a.k_head = k_head;
+  a.v_row = v_row;
+  a.v_head = v_head;
+  a.tokens = tokens;
+  a.heads = heads;
+  a.dim = dim;
+  a.log_block = (uint32_t)__builtin_ctz(block);
+  a.blocks = blocks;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(tokens), dim3(256), 0, st, a);
+    return launched();
+  };
+  if (cache == DGT_ELT_BF16)
+    return source == DGT_ELT_F32 ? run(k_kv_store<Bf16, float>) : run(k_kv_store<Bf16, uint16_t>);
+  return source == DGT_ELT_F32 ? run(k_kv_store<F16, float>) : run(k_kv_store<F16, uint16_t>);
+}
+
+}  // extern "C"

@@ -230,6 +230,124 @@ int dgt_dense_gemm(uint32_t fmt, uint32_t n, uint32_t k, uint32_t tile_n, const 
                    const uint16_t* d_x, uint32_t m, const uint16_t* d_scales, float w_scale,
                    float* d_y, void* d_ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------ serving operators
+ * What stands beside the compressed projections when a batch of requests is
+ * served and drafted tokens are verified: the page plan of a step, the store of
+ * new keys and values into a paged cache, attention over that cache, and
+ * low-rank adapters.
+ *
+ * Shared conventions.  Request b holds ctx[b] tokens in the cache and brings
+ * new[b] tokens to the step; the new tokens of all requests lie one after
+ * another in `tokens` rows, request b in rows cu[b] .. cu[b+1] - 1 (cu starts
+ * at 0 and never falls).  The cache is a pool of `blocks` pages of `block`
+ * tokens (a power of two, 8..1024):
+ *   keys   [blocks, kv_heads, block, dim]
+ *   values [blocks, kv_heads, dim, block]   (each page transposed)
+ * A slot is page * block + place in the page (blocks * block < 2^31).  A block
+ * table [requests, width] names each request's pages; token p of a request is
+ * in page table[b, p / block].  At most 16384 requests a call.
+ * Lengths, offsets, tables, slots and ids are device data that the host does
+ * not see: the kernels hold every access inside the buffers whatever they hold
+ * (lengths are cut to the table, offsets to the rows, a page or adapter id out
+ * of range counts as absent). */
+
+/* Element types of cache and activations. */
+enum dgt_element {
+  DGT_ELT_BF16 = 1,
+  DGT_ELT_F16 = 2,
+  DGT_ELT_F32 = 3
+};
+
+/* Page plan of one step, in one launch.  All arrays are on the device.
+ *   d_ctx, d_new: int32[requests]; negative values count as 0.
+ *   d_free: int32[free_len] page ids that may be taken, from *d_free_head on.
+ *   d_table: int32[requests, width]; columns of pages taken now are written.
+ *   d_parents: NULL (the new tokens of a request are a chain) or int32[tokens]:
+ *          parent of a drafted token, as an index within its request's new
+ *          tokens, below its own index; -1 hangs it off the cached context.
+ * Request b is refused if its pages would not fit `width`, its rows would not
+ * fit `tokens`, or the free list has too few pages for it and the requests
+ * before it; it then takes no page.
+ *   d_cu: int32[requests + 1], the exclusive sums of new, cut to `tokens`.
+ *   d_slots: int32[tokens], slot of each new token (token i of b is stored at
+ *          position ctx[b] + i); -1 for rows of no request or a refused one.
+ *   d_positions: int32[tokens]: ctx[b] + i, or ctx[b] + depth in the tree; -1
+ *          for rows of no request.
+ *   d_mask (with d_parents, else NULL and mask_words 0): uint64[tokens,
+ *          mask_words]: bit j is set if j is the token itself or one of its
+ *          ancestors.  mask_words <= 1024.
+ *   d_counts: int32[3]: rows needed (tokens + 1 if more than `tokens`), the
+ *          free list's new head, requests refused.
+ * A token whose index does not fit the mask, or whose way to the root meets a
+ * parent that is not below its child, gets slot -1, position -1 and no bits.
+ * Errors: E_ARG, E_SHAPE, E_HIP. */
+int dgt_page_plan(const int32_t* d_ctx, const int32_t* d_new, uint32_t requests,
+                  const int32_t* d_free, uint32_t free_len, const int32_t* d_free_head,
+                  int32_t* d_table, uint32_t width, uint32_t block, uint32_t blocks,
+                  uint32_t tokens, const int32_t* d_parents, uint32_t mask_words, int32_t* d_cu,
+                  int32_t* d_slots, int32_t* d_positions, uint64_t* d_mask, int32_t* d_counts,
+                  void* stream);
+
+/* Write the new tokens' keys and values into their slots.
+ *   d_k, d_v: [tokens, heads, dim] of type `source` (a dgt_element), element
+ *          strides per row and head given, elements of a head contiguous.
+ *   cache: type of the pages, BF16 or F16; `source` is F32 (rounded to nearest
+ *          even) or the same type (copied bit for bit).
+ *   d_slots: int32[tokens]; slots outside the pool are skipped.  Two rows with
+ *          one slot leave it with either's values.
+ * dim is a multiple of 8, at most 1024.  Errors: E_ARG, E_SHAPE,
+ * E_UNSUPPORTED, E_HIP. */
+int dgt_kv_store(const void* d_k, const void* d_v, uint32_t source, int64_t k_row, int64_t k_head,
+                 int64_t v_row, int64_t v_head, const int32_t* d_slots, uint32_t tokens,
+                 uint32_t heads, uint32_t dim, uint32_t cache, void* d_k_cache, void* d_v_cache,
+                 uint32_t blocks, uint32_t block, void* stream);
+
+/* Attention of the new tokens over cached and new keys:
+ *   out[i, h] = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale * q[i, h] . k_j),
+ * j over the request's ctx[b] cached tokens and those of its new tokens
+ * (stored at positions ctx[b] .. ctx[b] + n - 1) that token i sees: j with bit
+ * set in its mask row, or without a mask every j <= i.  Query head h reads key
+ * head h / (heads / kv_heads).  A row that sees no key is zero; keys that a row
+ * does not see do not touch it, whatever their values.  Sums are fp32, weights
+ * are rounded to `type` for the product with the values.
+ *   type: BF16 or F16, of q, the pages and out.
+ *   d_q, d_out: [tokens, heads, dim] with element strides per row and head,
+ *          elements of a head contiguous; strides of q multiples of 8, of out
+ *          of 2; q 16-byte aligned.  Rows past cu[requests] are not written.
+ *   d_mask: uint64[tokens, mask_words] or NULL with mask_words 0.
+ *   scale > 0.  dim: a multiple of 8 up to 256.
+ *   d_ws: dgt_tree_attention_workspace(...) bytes, zero-filled before its first
+ *          use; every call leaves it ready for the next (on one stream).
+ * One launch; the order of all sums is fixed by the lengths and shapes.
+ * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED, E_HIP. */
+size_t dgt_tree_attention_workspace(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                                    uint32_t requests);
+int dgt_tree_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t q_head,
+                       const void* d_k_cache, const void* d_v_cache, uint32_t blocks, uint32_t block,
+                       const int32_t* d_table, uint32_t width, const int32_t* d_ctx, const int32_t* d_cu,
+                       uint32_t requests, uint32_t tokens, uint32_t heads, uint32_t kv_heads,
+                       uint32_t dim, const uint64_t* d_mask, uint32_t mask_words, float scale,
+                       void* d_out, uint64_t out_row, uint64_t out_head, void* d_ws, size_t ws_bytes,
+                       void* stream);
+
+/* Low-rank adapters: out[t] = y[t] + scaling[a] * (x[t] A_a^T) B_a^T for the
+ * adapter a = ids[b] of row t's request (cu as above); rows of a request whose
+ * id is outside 0..adapters-1, or of no request, get out[t] = y[t].
+ *   d_x: bf16 [tokens, k]; d_a: bf16 [adapters, rank, k]; d_b: bf16 [adapters,
+ *          n, rank]; d_scaling: float[adapters]; d_y, d_out: fp32 [tokens, n];
+ *          x_row, y_row, out_row are element strides of the rows.
+ *   d_out may be d_y (then rows without an adapter are not touched); otherwise
+ *          they do not overlap.
+ * k is a multiple of 8, rank a multiple of 8 up to 256; x_row a multiple of 8; x, a, b 16-byte
+ * aligned.  All sums are fp32 and of a fixed order.  d_ws: dgt_lora_workspace
+ * bytes, any contents.  Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_HIP. */
+size_t dgt_lora_workspace(uint32_t tokens, uint32_t requests, uint32_t n, uint32_t k, uint32_t rank);
+int dgt_lora_add(const float* d_y, uint64_t y_row, const uint16_t* d_x, uint64_t x_row,
+                 const uint16_t* d_a, const uint16_t* d_b, const float* d_scaling, uint32_t adapters,
+                 const int32_t* d_ids, const int32_t* d_cu, uint32_t requests, uint32_t tokens,
+                 uint32_t n, uint32_t k, uint32_t rank, float* d_out, uint64_t out_row, void* d_ws,
+                 size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
