@@ -46,29 +46,39 @@ struct Shape {  // of one request
   uint32_t first, count, ctx, keys, tiles, chunks;
 };
 
-template <int RT>
+template <int ROWS>
 __device__ __forceinline__ Shape request_shape(const AttnArgs& a, uint32_t b) {
   Shape s;
   request_rows(a.cu, b, a.tokens, &s.first, &s.count);
   const uint32_t room = a.width << a.log_block;
   s.ctx = min((uint32_t)max(a.ctx[b], 0), room);
   s.keys = min(s.ctx + s.count, room);
-  s.tiles = (s.count * a.group + 16 * RT - 1) / (16 * RT);
+  s.tiles = (s.count * a.group + ROWS - 1) / ROWS;
   s.chunks = max((s.keys + kUnitKeys - 1) / kUnitKeys, 1u);
   return s;
 }
 
-template <int RT>
+template <int ROWS>
 __device__ __forceinline__ uint64_t request_units(const AttnArgs& a, uint32_t b) {
-  const Shape s = request_shape<RT>(a, b);
+  const Shape s = request_shape<ROWS>(a, b);
   return (uint64_t)s.tiles * s.chunks * a.heads;
 }
 
-__device__ __forceinline__ void agent_store(float* p, float v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Parts pass between workgroups that may sit on different dies, so they are
+// written through and read past the caches that the dies do not share (the sc1
+// bit of a buffer access, as agent-scope atomics have it, but 16 bytes a lane).
+constexpr int kAgent = 16;
+__device__ __forceinline__ void part_store(__amdgpu_buffer_rsrc_t r, uint32_t at, floatx4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at * 4, 0, kAgent);
 }
-__device__ __forceinline__ float agent_load(const float* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void part_store(__amdgpu_buffer_rsrc_t r, uint32_t at, float v) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at * 4, 0, kAgent);
+}
+__device__ __forceinline__ floatx4 part_load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, at * 4, 0, kAgent));
+}
+__device__ __forceinline__ float part_load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at * 4, 0, kAgent));
 }
 
 // What token `tok` of the request may see of the 8 keys from position kv on, one
@@ -89,23 +99,21 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Shape& s,
   return bits & ((1u << real) - 1);
 }
 
-template <class E, int DP, int RT, bool PAD>
-__global__ __launch_bounds__(256) void k_tree_attention(AttnArgs a) {
-  constexpr int KS = DP / 32, DT = DP / 16, ROWS = 16 * RT;
-  constexpr uint32_t kPart = ROWS * (DP + 2);  // floats of a part: m, l, o
-  __shared__ float s_o[ROWS][DP + 4];
-  __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
-  __shared__ uint64_t s_sum[256];
-  __shared__ uint32_t s_b, s_last;
-  __shared__ uint64_t s_base;
-  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, g = lane >> 4, l16 = lane & 15;
-  const uint32_t wg = blockIdx.x, grid = gridDim.x;
+// A workgroup's run of units [u, end), and the request that holds unit u.
+struct Run {
+  uint64_t u, end, base, units;  // base: the request's first unit
+  uint32_t wgs, b;
+};
 
-  // ------------------------------------------------ this workgroup's run of units
+// Deals the batch's units to the workgroups.  Every workgroup adds up the lengths
+// for itself, which costs less than a launch; false: nothing is left for this one.
+template <int ROWS>
+__device__ __forceinline__ bool find_run(const AttnArgs& a, uint64_t* s_sum, Run* out) {
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const uint32_t per = (a.requests + 255) / 256;
   const uint32_t b_lo = min(t * per, a.requests), b_hi = min(b_lo + per, a.requests);
   uint64_t mine = 0;
-  for (uint32_t b = b_lo; b < b_hi; ++b) mine += request_units<RT>(a, b);
+  for (uint32_t b = b_lo; b < b_hi; ++b) mine += request_units<ROWS>(a, b);
   uint64_t scan = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -119,70 +127,228 @@ __global__ __launch_bounds__(256) void k_tree_attention(AttnArgs a) {
     if (w < wave) scan += s_sum[w];
     units += s_sum[w];
   }
-  if (units == 0) return;
+  if (units == 0) return false;
   const uint64_t most = (units + kMinUnits - 1) / kMinUnits;
-  const uint32_t wgs = (uint32_t)min((uint64_t)grid, most);
-  if (wg >= wgs) return;
-  const uint64_t u_end = units * (wg + 1) / wgs;
-  uint64_t u = units * wg / wgs;
+  const uint32_t wgs = (uint32_t)min((uint64_t)gridDim.x, most);
+  if (blockIdx.x >= wgs) return false;
+  const uint64_t u = units * blockIdx.x / wgs;
   const uint64_t before = scan - mine;
   if (before <= u && u < scan) {  // one thread holds the run's first unit
     uint64_t base = before;
     uint32_t b = b_lo;
     for (;; ++b) {
-      const uint64_t n = request_units<RT>(a, b);
+      const uint64_t n = request_units<ROWS>(a, b);
       if (u < base + n) break;
       base += n;
     }
-    s_b = b;
-    s_base = base;
+    s_sum[4] = b;
+    s_sum[5] = base;
   }
   __syncthreads();
-  uint32_t b = __builtin_amdgcn_readfirstlane(s_b);
-  uint64_t base = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(s_base >> 32)) << 32 |
-                  __builtin_amdgcn_readfirstlane((uint32_t)s_base);
-  Shape sh = request_shape<RT>(a, b);
+  out->u = u;
+  out->end = units * (blockIdx.x + 1) / wgs;
+  out->units = units;
+  out->wgs = wgs;
+  out->b = __builtin_amdgcn_readfirstlane((uint32_t)s_sum[4]);
+  out->base = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(s_sum[5] >> 32)) << 32 |
+              __builtin_amdgcn_readfirstlane((uint32_t)s_sum[5]);
+  return true;
+}
 
-  while (u < u_end) {
-    while (u >= base + (uint64_t)sh.tiles * sh.chunks * a.heads) {  // on to the next request
-      base += (uint64_t)sh.tiles * sh.chunks * a.heads;
-      sh = request_shape<RT>(a, ++b);
-    }
-    const uint32_t in = (uint32_t)(u - base), item = in / sh.chunks, c0 = in % sh.chunks;
-    const uint32_t head = item / sh.tiles, tile = item % sh.tiles;
-    const uint64_t item0 = u - c0;  // the item's first unit
-    const uint32_t c1 = (uint32_t)min((uint64_t)sh.chunks, u_end - item0);
-    const uint32_t rows = sh.count * a.group, row0 = tile * ROWS;
+// The part of one (request, key head, tile of rows) that the run covers.
+struct Item {
+  uint32_t head, row0, rows;  // rows: of the request and head
+  uint32_t c0, c1;            // chunks of its keys
+  uint64_t first;             // unit of chunk 0
+  bool whole;
+};
 
-    // queries, the product's second operand; rows past the end read the last one
-    u32x4 q[RT][KS];
-    uint32_t tok[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const uint32_t r = min(row0 + 16 * i + l16, rows - 1);
-      tok[i] = r / a.group;
-      const uint16_t* p = a.q + (uint64_t)(sh.first + tok[i]) * a.q_row +
-                          (uint64_t)(head * a.group + r % a.group) * a.q_head;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint32_t d = 32 * s + 8 * g;
-        q[i][s] = (!PAD || d < a.dim) ? *reinterpret_cast<const u32x4*>(p + d) : u32x4{};
-      }
-    }
-    floatx4 o[RT][DT];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[i][d] = floatx4{};
-    }
+template <int ROWS>
+__device__ __forceinline__ Item next_item(const AttnArgs& a, Run* run, Shape* sh) {
+  while (run->u >= run->base + (uint64_t)sh->tiles * sh->chunks * a.heads) {
+    run->base += (uint64_t)sh->tiles * sh->chunks * a.heads;
+    *sh = request_shape<ROWS>(a, ++run->b);
+  }
+  const uint32_t in = (uint32_t)(run->u - run->base), item = in / sh->chunks;
+  Item it;
+  it.c0 = in % sh->chunks;
+  it.head = item / sh->tiles;
+  it.row0 = item % sh->tiles * ROWS;
+  it.rows = sh->count * a.group;
+  it.first = run->u - it.c0;
+  it.c1 = (uint32_t)min((uint64_t)sh->chunks, run->end - it.first);
+  it.whole = it.c0 == 0 && it.c1 == sh->chunks;
+  run->u = it.first + it.c1;
+  return it;
+}
 
-    const int32_t* pages = a.table + (uint64_t)b * a.width;
-    const uint32_t in_page = (1u << a.log_block) - 1;
-    const uint64_t page_len = (uint64_t)a.dim << a.log_block;  // elements of a head's page
-    for (uint32_t c = c0; c < c1; ++c) {
+__device__ __forceinline__ uint16_t* out_at(const AttnArgs& a, const Shape& sh, const Item& it, uint32_t r) {
+  const uint32_t row = it.row0 + r, tok = row / a.group, head = it.head * a.group + row % a.group;
+  return a.out + (uint64_t)(sh.first + tok) * a.out_row + (uint64_t)head * a.out_head;
+}
+
+// 1 / the sum of weights; 0 where the row saw nothing (a NaN stays one).
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
+// Where the parts of an item lie: its workgroups are owner(first unit) ..
+// owner(last unit); each has room for two, one item that it ends or crosses and
+// one that it begins.  A part is m[ROWS], l[ROWS] and the outputs, in floats.
+template <int ROWS, int DP>
+struct Parts {
+  static constexpr uint32_t kFloats = ROWS * (DP + 2);
+  uint32_t w0, w1;
+  __amdgpu_buffer_rsrc_t at;
+  __device__ __forceinline__ Parts(const AttnArgs& a, const Run& run, const Item& it, uint32_t chunks) {
+    auto owner = [&](uint64_t x) {  // the last w with floor(units * w / wgs) <= x
+      return (uint32_t)(((x + 1) * run.wgs - 1) / run.units);
+    };
+    w0 = owner(it.first);
+    w1 = owner(it.first + chunks - 1);
+    // raw 32-bit data; accesses are checked against the length
+    at = __builtin_amdgcn_make_buffer_rsrc(a.parts, 0, gridDim.x * 2 * kFloats * 4, 0x00027000);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t w) const { return (2 * w + (w == w0)) * kFloats; }
+
+  // Counts this workgroup's part in; true for the item's last.  Waiting for the
+  // stores before counting orders them without the cache writeback of a fence.
+  __device__ __forceinline__ bool last(const AttnArgs& a, uint32_t* s_last) const {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const uint32_t old = __hip_atomic_fetch_add(a.counters + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      *s_last = old == w1 - w0;
+      if (old == w1 - w0)  // ready for the next call
+        __hip_atomic_store(a.counters + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    return *s_last != 0;
+  }
+
+  // Joins row r of the parts in the order of the keys: N pieces of four outputs at
+  // at0, at0 + step, ..., within a part.  Returns the sum of weights.
+  template <int N>
+  __device__ __forceinline__ float join(uint32_t r, uint32_t at0, uint32_t step, floatx4 (&o)[N], float scale) const {
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = floatx4{};
+    for (uint32_t w = w0; w <= w1; ++w) {
+      const uint32_t p = of(w);
+      const float mw = part_load(at, p + r), lw = part_load(at, p + ROWS + r);
+      floatx4 ow[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) ow[i] = part_load4(at, p + 2 * ROWS + at0 + i * step);
+      const float now = fmaxf(m, mw), ref = now == -INFINITY ? 0.f : now;
+      const float f = __builtin_amdgcn_exp2f((m - ref) * scale), fw = __builtin_amdgcn_exp2f((mw - ref) * scale);
+      m = now;
+      l = fmaf(lw, fw, l * f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = o[i] * f + ow[i] * fw;
+    }
+    return l;
+  }
+};
+
+template <class E>
+__device__ __forceinline__ void write4(uint16_t* p, floatx4 v, float inv) {
+  *reinterpret_cast<uint32_t*>(p) = E::pack2(v[0] * inv, v[1] * inv);
+  *reinterpret_cast<uint32_t*>(p + 2) = E::pack2(v[2] * inv, v[3] * inv);
+}
+
+// Queries of 16 rows a lane group, the products' second operand; rows past the
+// end read the last one.
+template <int RT, int KS, bool PAD>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Shape& sh, const Item& it, uint32_t row,
+                                             u32x4 (&q)[RT][KS], uint32_t (&tok)[RT]) {
+  const uint32_t lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const uint32_t r = min(row + 16 * i + l16, it.rows - 1);
+    tok[i] = r / a.group;
+    const uint16_t* p = a.q + (uint64_t)(sh.first + tok[i]) * a.q_row +
+                        (uint64_t)(it.head * a.group + r % a.group) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t d = 32 * s + 8 * g;
+      q[i][s] = (!PAD || d < a.dim) ? *reinterpret_cast<const u32x4*>(p + d) : u32x4{};
+    }
+  }
+}
+
+// One step of the running softmax over the 4 N scores that a lane holds of its
+// row: s becomes the weights, m and l are updated; returns what the output so
+// far is multiplied by.  l counts this lane's keys only, the lanes of a row are
+// added at the end.
+template <int N>
+__device__ __forceinline__ float softmax_step(floatx4 (&s)[N], float& m, float& l, float scale) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int h = 0; h < N; ++h)
+    top = fmaxf(top, fmaxf(fmaxf(s[h][0], s[h][1]), fmaxf(s[h][2], s[h][3])));
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  const float now = fmaxf(m, top);
+  // a row that has seen nothing yet keeps -inf; its weights are exp2(-inf) = 0
+  const float ref = now == -INFINITY ? 0.f : now * scale;
+  const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(fmaf(m, scale, -ref));
+  m = now;
+  float sum = 0.f;
+#pragma unroll
+  for (int h = 0; h < N; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(s[h][e], scale, -ref));
+      s[h][e] = p;
+      sum += p;
+    }
+  l = fmaf(l, keep, sum);
+  return keep;
+}
+
+// The weights are rounded to the cache's type, as the matrix instruction takes
+// them; the sum that divides them is of the unrounded ones.
+template <class E>
+__device__ __forceinline__ u32x4 weights(const floatx4& s0, const floatx4& s1) {
+  return u32x4{E::pack2(s0[0], s0[1]), E::pack2(s0[2], s0[3]), E::pack2(s1[0], s1[1]), E::pack2(s1[2], s1[3])};
+}
+
+// Keeps what is computed from v inside the loop it stands in: the rare paths'
+// addresses would otherwise be formed ahead of all loops and hold registers there.
+__device__ __forceinline__ void keep_here(uint32_t& v) { asm volatile("" : "+v"(v)); }
+
+// Pages of the keys at hand, kept in LDS: table entries of up to kPageRoom pages.
+constexpr uint32_t kPageRoom = 1024;
+
+// ----------------------------------------------------------- 16 rows and fewer
+// Each wave streams its own 32 keys of a unit from memory straight into the
+// operands; the waves meet once an item.
+template <class E, int DP, bool PAD>
+__global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(AttnArgs a) {
+  constexpr int KS = DP / 32, DT = DP / 16, ROWS = 16;
+  __shared__ float s_o[ROWS][DP + 4];
+  __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
+  __shared__ uint64_t s_sum[6];
+  __shared__ uint32_t s_last;
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, g = lane >> 4, l16 = lane & 15;
+  Run run;
+  if (!find_run<ROWS>(a, s_sum, &run)) return;
+  Shape sh = request_shape<ROWS>(a, run.b);
+  const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
+  const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
+
+  const uint32_t v_step = 16u << a.log_block;  // 16 value rows
+
+  while (run.u < run.end) {
+    const Item it = next_item<ROWS>(a, &run, &sh);
+    u32x4 q[1][KS];
+    uint32_t tok[1];
+    load_queries<1, KS, PAD>(a, sh, it, it.row0, q, tok);
+    floatx4 o[DT];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = floatx4{};
+
+    const int32_t* pages = a.table + (uint64_t)run.b * a.width;
+    for (uint32_t c = it.c0; c < it.c1; ++c) {
       const uint32_t kb = c * kUnitKeys + wave * kTileKeys;
       if (kb >= sh.keys) break;
       // the lane's group of 8 keys for masks and values, and for its key rows
@@ -192,33 +358,28 @@ __global__ __launch_bounds__(256) void k_tree_attention(AttnArgs a) {
       const bool held = pv < a.blocks;
       pv = held ? pv : 0u;
       pk = pk < a.blocks ? pk : 0u;
-      const uint16_t* kp = a.kc + ((uint64_t)pk * a.heads + head) * page_len +
-                           (uint64_t)((kk & in_page) + (l16 & 3)) * a.dim;
-      const uint16_t* vp = a.vc + ((uint64_t)pv * a.heads + head) * page_len + (kv & in_page);
+      const uint16_t* kp = a.kc + ((uint64_t)pk * a.heads + it.head) * page_len +
+                           ((kk & in_page) + (l16 & 3)) * dim + 8 * g;
+      const uint16_t* vp = a.vc + ((uint64_t)pv * a.heads + it.head) * page_len + (l16 << a.log_block) + (kv & in_page);
 
-      floatx4 s[RT][2];
+      u32x4 kf[2][KS], vf[DT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) s[i][h] = floatx4{};
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
           const uint32_t d = 32 * x + 8 * g;
-          const u32x4 kf = (!PAD || d < a.dim)
-                               ? *reinterpret_cast<const u32x4*>(kp + (uint64_t)4 * h * a.dim + d)
-                               : u32x4{};
-#pragma unroll
-          for (int i = 0; i < RT; ++i) s[i][h] = E::mfma(kf, q[i][x], s[i][h]);
+          kf[h][x] = (!PAD || d < dim) ? *reinterpret_cast<const u32x4*>(kp + 4 * h * dim + 32 * x) : u32x4{};
         }
-      }
-      u32x4 vf[DT];
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const uint32_t row = 16 * d + l16;
-        vf[d] = (!PAD || row < a.dim)
-                    ? *reinterpret_cast<const u32x4*>(vp + ((uint64_t)row << a.log_block))
-                    : u32x4{};
+        vf[d] = (!PAD || row < dim) ? *reinterpret_cast<const u32x4*>(vp + d * v_step) : u32x4{};
       }
+      floatx4 s[2] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < KS; ++x) s[h] = E::mfma(kf[h][x], q[0][x], s[h]);
 
       // Past the cached keys, or where a page is missing, scores of unseen keys
       // become -inf and values of keys that do not exist become zero (0 * NaN
@@ -226,62 +387,30 @@ __global__ __launch_bounds__(256) void k_tree_attention(AttnArgs a) {
       const bool edge = __any(kb + kTileKeys > sh.ctx || !held);
       bool odd_values = false;
       if (edge) {
+        const uint32_t bits = held ? seen_bits(a, sh, tok[0], kv) : 0u;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const uint32_t bits = held ? seen_bits(a, sh, tok[i], kv) : 0u;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!((bits >> e) & 1)) s[i][e >> 2][e & 3] = -INFINITY;
-        }
+        for (int e = 0; e < 8; ++e)
+          if (!((bits >> e) & 1)) s[e >> 2][e & 3] = -INFINITY;
         const uint32_t real = !held || kv >= sh.keys ? 0u : min(sh.keys - kv, 8u);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t v = vf[d][w];
-            if (real <= 2u * w) v = 0u;
-            else if (real == 2u * w + 1) v &= 0xFFFFu;
+            v = real <= 2u * w ? 0u : real == 2u * w + 1 ? v & 0xFFFFu : v;
             vf[d][w] = v;
             odd_values |= !E::finite2(v);
           }
         odd_values = __any(odd_values);
       }
 
+      const float keep = softmax_step<2>(s, m, l, a.scale);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float top = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                          fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float now = fmaxf(m[i], top);
-        // a row that has seen nothing yet keeps -inf; its weights are exp2(-inf) = 0
-        const float ref = now == -INFINITY ? 0.f : now * a.scale;
-        const float keep = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] * a.scale - ref);
-        m[i] = now;
-        float sum = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(s[i][h][e], a.scale, -ref));
-            s[i][h][e] = p;
-            sum += p;
-          }
-        l[i] = fmaf(l[i], keep, sum);  // this lane's keys; the lanes are added at the end
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[i][d] *= keep;
-      }
-
+      for (int d = 0; d < DT; ++d) o[d] *= keep;
       if (!odd_values) {
-        // The weights are rounded to the cache's type, as the matrix instruction
-        // takes them; the sum that divides them is of the unrounded ones.
+        const u32x4 p = weights<E>(s[0], s[1]);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const u32x4 p = {E::pack2(s[i][0][0], s[i][0][1]), E::pack2(s[i][0][2], s[i][0][3]),
-                           E::pack2(s[i][1][0], s[i][1][1]), E::pack2(s[i][1][2], s[i][1][3])};
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[i][d] = E::mfma(vf[d], p, o[i][d]);
-        }
+        for (int d = 0; d < DT; ++d) o[d] = E::mfma(vf[d], p, o[d]);
       } else {
         // A drafted value is infinite or NaN: rows that do not see it must not
         // meet it, so keys of weight zero are left out one by one.
@@ -290,141 +419,363 @@ __global__ __launch_bounds__(256) void k_tree_attention(AttnArgs a) {
         for (uint32_t x = 0; x < real; ++x) {
           const uint32_t key = kb + x, page = (uint32_t)pages[key >> a.log_block];
           if (page >= a.blocks) continue;
-          const uint16_t* vx = a.vc + ((uint64_t)page * a.heads + head) * page_len + (key & in_page);
-          float p[RT];
+          const uint16_t* vx = a.vc + ((uint64_t)page * a.heads + it.head) * page_len + (key & in_page);
+          uint32_t g_now = g;
+          keep_here(g_now);
+          float p = s[0][0];
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            float v = s[i][0][0];
-#pragma unroll
-            for (uint32_t e = 1; e < 8; ++e) v = (x & 7) == e ? s[i][e >> 2][e & 3] : v;
-            p[i] = __shfl(v, (x >> 3) * 16 + l16, 64);
-          }
+          for (uint32_t e = 1; e < 8; ++e) p = (x & 7) == e ? s[e >> 2][e & 3] : p;
+          p = __shfl(p, (x >> 3) * 16 + l16, 64);
 #pragma unroll
           for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t row = 16 * d + 4 * g + j;
+              const uint32_t row = 16 * d + 4 * g_now + j;
               if (PAD && row >= a.dim) continue;
               const float v = E::up(vx[(uint64_t)row << a.log_block]);
-#pragma unroll
-              for (int i = 0; i < RT; ++i)
-                if (p[i] != 0.f) o[i][d][j] = fmaf(p[i], v, o[i][d][j]);
+              if (p != 0.f) o[d][j] = fmaf(p, v, o[d][j]);
             }
         }
       }
     }
 
-    // ------------------------------------------- the four waves' parts, added in order
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      l[i] += __shfl_xor(l[i], 16, 64);
-      l[i] += __shfl_xor(l[i], 32, 64);
-      if (g == 0) {
-        s_m[wave][16 * i + l16] = m[i];
-        s_l[wave][16 * i + l16] = l[i];
-      }
+    // the four waves' parts, added in order
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (g == 0) {
+      s_m[wave][l16] = m;
+      s_l[wave][l16] = l;
     }
     __syncthreads();
-    float top[RT], total[RT];
+    const float top = fmaxf(fmaxf(s_m[0][l16], s_m[1][l16]), fmaxf(s_m[2][l16], s_m[3][l16]));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const uint32_t r = 16 * i + l16;
-      top[i] = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
-      const float ref = top[i] == -INFINITY ? 0.f : top[i];
-      total[i] = 0.f;
-#pragma unroll
-      for (uint32_t w = 0; w < kWaves; ++w)
-        total[i] += s_l[w][r] * __builtin_amdgcn_exp2f((s_m[w][r] - ref) * a.scale);
-      const float f = __builtin_amdgcn_exp2f((m[i] - ref) * a.scale);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[i][d] *= f;
-    }
+    for (uint32_t w = 0; w < kWaves; ++w)
+      total += s_l[w][l16] * __builtin_amdgcn_exp2f((s_m[w][l16] - ref) * a.scale);
+    const float f = __builtin_amdgcn_exp2f((m - ref) * a.scale);
     for (uint32_t w = 0; w < kWaves; ++w) {
       if (w == wave) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            floatx4* p = reinterpret_cast<floatx4*>(&s_o[16 * i + l16][16 * d + 4 * g]);
-            if (w == 0) *p = o[i][d];
-            else *p += o[i][d];
-          }
+        for (int d = 0; d < DT; ++d) {
+          floatx4* p = reinterpret_cast<floatx4*>(&s_o[l16][16 * d + 4 * g]);
+          if (w == 0) *p = o[d] * f;
+          else *p += o[d] * f;
+        }
       }
       __syncthreads();
     }
-    const uint32_t live = min(rows - row0, (uint32_t)ROWS);
-    auto write = [&](uint32_t r, uint32_t d, float v0, float v1) {
-      const uint32_t row = row0 + r, tk = row / a.group, hd = head * a.group + row % a.group;
-      *reinterpret_cast<uint32_t*>(a.out + (uint64_t)(sh.first + tk) * a.out_row + (uint64_t)hd * a.out_head + d) =
-          E::pack2(v0, v1);
-    };
     if (wave == 0 && g == 0) {  // the joined statistics, for the threads that write
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        s_m[0][16 * i + l16] = top[i];
-        s_l[0][16 * i + l16] = total[i];
-      }
+      s_m[0][l16] = top;
+      s_l[0][l16] = total;
     }
     __syncthreads();
-    const bool whole = c0 == 0 && c1 == sh.chunks;
-    if (whole) {
-      for (uint32_t i = t; i < live * (DP / 2); i += 256) {
-        const uint32_t r = i / (DP / 2), d = 2 * (i % (DP / 2));
-        if (PAD && d >= a.dim) continue;
-        const float inv = s_l[0][r] > 0.f || s_l[0][r] != s_l[0][r] ? 1.f / s_l[0][r] : 0.f;
-        write(r, d, s_o[r][d] * inv, s_o[r][d + 1] * inv);
+    const uint32_t live = min(it.rows - it.row0, (uint32_t)ROWS);
+    constexpr uint32_t kFours = DP / 4;  // of a row
+    if (it.whole) {
+      for (uint32_t i = t; i < live * kFours; i += 256) {
+        const uint32_t r = i / kFours, d = 4 * (i % kFours);
+        if (!PAD || d < dim)
+          write4<E>(out_at(a, sh, it, r) + d, *reinterpret_cast<floatx4*>(&s_o[r][d]), inverse(s_l[0][r]));
       }
     } else {
-      // first and last workgroup of the item, from the runs' bounds
-      const uint64_t end = item0 + sh.chunks - 1;
-      auto owner = [&](uint64_t x) {
-        uint32_t w = (uint32_t)(((x + 1) * wgs - 1) / units);  // the last w with units * w / wgs <= x
-        return w;
-      };
-      const uint32_t w0 = owner(item0), w1 = owner(end);
-      auto part_of = [&](uint32_t w) { return a.parts + ((uint64_t)2 * w + (w == w0)) * kPart; };
-      float* part = part_of(wg);
-      for (uint32_t i = t; i < live; i += 256) {
-        agent_store(part + i, s_m[0][i]);
-        agent_store(part + ROWS + i, s_l[0][i]);
+      const Parts<ROWS, DP> parts(a, run, it, sh.chunks);
+      const uint32_t mine = parts.of(blockIdx.x);
+      if (t < live) {
+        part_store(parts.at, mine + t, s_m[0][t]);
+        part_store(parts.at, mine + ROWS + t, s_l[0][t]);
       }
-      for (uint32_t i = t; i < live * DP; i += 256)
-        agent_store(part + 2 * ROWS + i, s_o[i / DP][i % DP]);
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (t == 0) {
-        const uint32_t old = __hip_atomic_fetch_add(a.counters + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = old == w1 - w0;
-      }
-      __syncthreads();
-      if (s_last) {
-        if (t == 0) __hip_atomic_store(a.counters + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        for (uint32_t i = t; i < live * (DP / 2); i += 256) {
-          const uint32_t r = i / (DP / 2), d = 2 * (i % (DP / 2));
-          if (PAD && d >= a.dim) continue;
-          float mm = -INFINITY;
-          for (uint32_t w = w0; w <= w1; ++w) mm = fmaxf(mm, agent_load(part_of(w) + r));
-          const float ref = mm == -INFINITY ? 0.f : mm;
-          float ll = 0.f, v0 = 0.f, v1 = 0.f;
-          for (uint32_t w = w0; w <= w1; ++w) {
-            const float* p = part_of(w);
-            const float f = __builtin_amdgcn_exp2f((agent_load(p + r) - ref) * a.scale);
-            ll = fmaf(agent_load(p + ROWS + r), f, ll);
-            v0 = fmaf(agent_load(p + 2 * ROWS + r * DP + d), f, v0);
-            v1 = fmaf(agent_load(p + 2 * ROWS + r * DP + d + 1), f, v1);
-          }
-          const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-          write(r, d, v0 * inv, v1 * inv);
+      for (uint32_t i = t; i < live * kFours; i += 256)
+        part_store(parts.at, mine + 2 * ROWS + 4 * i, *reinterpret_cast<floatx4*>(&s_o[i / kFours][4 * (i % kFours)]));
+      if (parts.last(a, &s_last)) {
+        for (uint32_t i = t; i < live * kFours; i += 256) {
+          const uint32_t r = i / kFours, d = 4 * (i % kFours);
+          floatx4 sum[1];
+          const float all = parts.join(r, 4 * i, 0, sum, a.scale);
+          if (!PAD || d < dim) write4<E>(out_at(a, sh, it, r) + d, sum[0], inverse(all));
         }
       }
     }
     __syncthreads();  // the LDS is reused by the next item
-    u = item0 + c1;
+  }
+}
+
+// -------------------------------------------------------------- more than 16 rows
+// The waves take 16 RT rows each and share tiles of keys and values in LDS, two
+// buffers deep: the next tile is loaded into registers while this one is
+// multiplied.  16-byte pieces of a row are permuted by its number so that the
+// lanes of an operand read fall on different banks.
+template <int DP>
+struct Tile {
+  static constexpr uint32_t kKeys = DP == 256 ? 32 : 64;
+  static constexpr uint32_t kKPieces = DP / 8, kVPieces = kKeys / 8;  // of a row
+  static constexpr uint32_t kPieces = kKeys * kKPieces;               // of a buffer, keys or values
+  static constexpr uint32_t kEach = kPieces / 256;                    // a thread
+  static constexpr uint32_t kBytes = 2 * 2 * kPieces * 16 + kPageRoom * 4;
+  // rows of one operand read are r .. r + 3 and r + 8 .. r + 11 for keys, consecutive for values
+  static __device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t piece) {
+    return row * kKPieces + (piece ^ ((row & 3) | ((row >> 1) & 4)));
+  }
+  static __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
+    return row * kVPieces + (piece ^ (row & (kVPieces - 1)));
+  }
+};
+
+template <class E, int DP, int RT, bool PAD>
+__global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
+  using T = Tile<DP>;
+  constexpr int KS = DP / 32, DT = DP / 16, ROWS = 64 * RT, NS = T::kKeys / 16;
+  extern __shared__ u32x4 lds[];
+  u32x4* s_k = lds;                       // [2][kPieces]
+  u32x4* s_v = lds + 2 * T::kPieces;      // [2][kPieces]
+  uint32_t* s_page = reinterpret_cast<uint32_t*>(lds + 4 * T::kPieces);
+  __shared__ uint64_t s_sum[6];
+  __shared__ uint32_t s_last;
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, g = lane >> 4, l16 = lane & 15;
+  Run run;
+  if (!find_run<ROWS>(a, s_sum, &run)) return;
+  Shape sh = request_shape<ROWS>(a, run.b);
+  const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
+  const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
+  // pieces of a page's value row that lie in one tile, as a power of two
+  const uint32_t log_vp = min(a.log_block, (uint32_t)__builtin_ctz(T::kKeys)) - 3;
+
+  // Piece x of a tile of values in the order of memory: page by page, value row by
+  // row; which of the row's pieces it is.
+  const uint32_t log_part = log_vp + (uint32_t)__builtin_ctz(DP);
+  auto value_piece = [&](uint32_t x) { return (x >> log_part << log_vp) + (x & ((1u << log_vp) - 1)); };
+
+  while (run.u < run.end) {
+    const Item it = next_item<ROWS>(a, &run, &sh);
+    const uint32_t row_w = it.row0 + wave * 16 * RT;  // the wave's first row
+    const bool works = row_w < it.rows;
+    u32x4 q[RT][KS];
+    uint32_t tok[RT];
+    load_queries<RT, KS, PAD>(a, sh, it, row_w, q, tok);
+    floatx4 o[RT][DT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[i][d] = floatx4{};
+    }
+    const int32_t* pages = a.table + (uint64_t)run.b * a.width;
+    const uint32_t k_end = min(it.c1 * kUnitKeys, sh.keys);
+
+    // in pieces of as many pages as the LDS has room for; a piece ends on a page's end
+    for (uint32_t seg = it.c0 * kUnitKeys, seg_end; seg < k_end; seg = seg_end) {
+      const uint32_t page0 = seg >> a.log_block;
+      seg_end = min(k_end, (page0 + kPageRoom) << a.log_block);
+      const uint32_t n_pages = ((seg_end - 1) >> a.log_block) - page0 + 1;
+      for (uint32_t i = t; i < n_pages; i += 256) s_page[i] = (uint32_t)pages[page0 + i];
+      __syncthreads();
+
+      u32x4 rk[T::kEach], rv[T::kEach];
+      bool odd = false;
+      auto load = [&](uint32_t kb) {
+        odd = false;
+#pragma unroll
+        for (uint32_t j = 0; j < T::kEach; ++j) {
+          const uint32_t x = t + 256 * j, key = kb + x / T::kKPieces, d = 8 * (t % T::kKPieces);
+          rk[j] = u32x4{};
+          if (key < seg_end && (!PAD || d < dim)) {
+            const uint32_t page = s_page[(key >> a.log_block) - page0];
+            if (page < a.blocks)
+              rk[j] = *reinterpret_cast<const u32x4*>(a.kc + ((uint64_t)page * a.heads + it.head) * page_len +
+                                                      ((key & in_page) * dim + d));
+          }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < T::kEach; ++j) {
+          const uint32_t x = t + 256 * j, y = x & ((DP << log_vp) - 1), row = y >> log_vp;
+          const uint32_t key = kb + 8 * value_piece(x);
+          rv[j] = u32x4{};
+          if (key < seg_end && (!PAD || row < dim)) {
+            const uint32_t page = s_page[(key >> a.log_block) - page0];
+            if (page < a.blocks)
+              rv[j] = *reinterpret_cast<const u32x4*>(a.vc + ((uint64_t)page * a.heads + it.head) * page_len +
+                                                      ((row << a.log_block) + (key & in_page)));
+          }
+        }
+      };
+      // Values of keys that do not exist become zero, and a drafted value that is
+      // not finite is noted: a weight of zero times it is not zero.
+      auto store = [&](uint32_t kb, uint32_t buf) {
+        const bool edge = kb + T::kKeys > sh.ctx;
+#pragma unroll
+        for (uint32_t j = 0; j < T::kEach; ++j) {
+          const uint32_t x = t + 256 * j;
+          s_k[buf * T::kPieces + T::k_at(x / T::kKPieces, x % T::kKPieces)] = rk[j];
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < T::kEach; ++j) {
+          const uint32_t x = t + 256 * j, row = (x & ((DP << log_vp) - 1)) >> log_vp;
+          const uint32_t piece = value_piece(x), key = kb + 8 * piece;
+          if (edge) {
+            const uint32_t real = key < sh.keys ? min(sh.keys - key, 8u) : 0u;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              uint32_t v = rv[j][w];
+              v = real <= 2u * w ? 0u : real == 2u * w + 1 ? v & 0xFFFFu : v;
+              rv[j][w] = v;
+              odd |= !E::finite2(v);
+            }
+          }
+          s_v[buf * T::kPieces + T::v_at(row, piece)] = rv[j];
+        }
+        // true where any thread noted one
+        if (edge) odd = __syncthreads_or(odd);
+        else __syncthreads();
+      };
+
+      load(seg);
+      store(seg, 0);
+      uint32_t buf = 0;
+      for (uint32_t kb = seg; kb < seg_end; kb += T::kKeys, buf ^= 1) {
+        const bool more = kb + T::kKeys < seg_end, odd_now = odd;
+        if (more) load(kb + T::kKeys);
+        if (works) {
+          const u32x4* bk = s_k + buf * T::kPieces;
+          const u32x4* bv = s_v + buf * T::kPieces;
+          floatx4 s[RT][NS];
+#pragma unroll
+          for (int h = 0; h < NS; ++h) {
+            const uint32_t row = 32 * (h >> 1) + 8 * (l16 >> 2) + 4 * (h & 1) + (l16 & 3);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) s[i][h] = floatx4{};
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+              const u32x4 kf = bk[T::k_at(row, 4 * x + g)];
+#pragma unroll
+              for (int i = 0; i < RT; ++i) s[i][h] = E::mfma(kf, q[i][x], s[i][h]);
+            }
+          }
+          // scores of unseen keys become -inf: past the cached keys, and on missing pages
+          bool missing[NS / 2];
+          bool edge = kb + T::kKeys > sh.ctx;
+#pragma unroll
+          for (int h = 0; h < NS / 2; ++h) {
+            const uint32_t kv = kb + 32 * h + 8 * g;
+            missing[h] = kv < seg_end && s_page[(kv >> a.log_block) - page0] >= a.blocks;
+            edge |= missing[h];
+          }
+          if (__any(edge)) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+              for (int h = 0; h < NS / 2; ++h) {
+                const uint32_t bits = missing[h] ? 0u : seen_bits(a, sh, tok[i], kb + 32 * h + 8 * g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (!((bits >> e) & 1)) s[i][2 * h + (e >> 2)][e & 3] = -INFINITY;
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            const float keep = softmax_step<NS>(s[i], m[i], l[i], a.scale);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[i][d] *= keep;
+          }
+          if (!odd_now) {
+#pragma unroll
+            for (int h = 0; h < NS / 2; ++h) {
+              u32x4 p[RT];
+#pragma unroll
+              for (int i = 0; i < RT; ++i) p[i] = weights<E>(s[i][2 * h], s[i][2 * h + 1]);
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                const u32x4 vf = bv[T::v_at(16 * d + l16, 4 * h + g)];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) o[i][d] = E::mfma(vf, p[i], o[i][d]);
+              }
+            }
+          } else {
+            // key by key, leaving out those of weight zero
+            const uint16_t* values = reinterpret_cast<const uint16_t*>(bv);
+#pragma unroll 1
+            for (uint32_t x = 0; x < T::kKeys; ++x) {
+              uint32_t g_now = g;
+              keep_here(g_now);
+              float p[RT];
+#pragma unroll
+              for (int i = 0; i < RT; ++i) {
+                p[i] = 0.f;
+#pragma unroll
+                for (uint32_t e = 0; e < 2 * NS * 2; ++e)
+                  p[i] = (x >> 5) * 8 + (x & 7) == e ? s[i][e >> 2][e & 3] : p[i];
+                p[i] = __shfl(p[i], ((x >> 3) & 3) * 16 + l16, 64);
+              }
+#pragma unroll
+              for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float v = E::up(values[T::v_at(16 * d + 4 * g_now + j, x >> 3) * 8 + (x & 7)]);
+#pragma unroll
+                  for (int i = 0; i < RT; ++i)
+                    if (p[i] != 0.f) o[i][d][j] = fmaf(p[i], v, o[i][d][j]);
+                }
+            }
+          }
+        }
+        if (more) store(kb + T::kKeys, buf ^ 1);
+      }
+      __syncthreads();  // the buffers and the pages are refilled
+    }
+
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      l[i] += __shfl_xor(l[i], 16, 64);
+      l[i] += __shfl_xor(l[i], 32, 64);
+    }
+    bool write = it.whole;
+    if (!it.whole) {
+      // outputs lie in the order of the lanes that hold them
+      const Parts<ROWS, DP> parts(a, run, it, sh.chunks);
+      const uint32_t mine = parts.of(blockIdx.x), at0 = 4 * (wave * RT * DT * 64 + lane);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t r = wave * 16 * RT + 16 * i + l16;
+        if (it.row0 + r < it.rows) {
+          if (g == 0) {
+            part_store(parts.at, mine + r, m[i]);
+            part_store(parts.at, mine + ROWS + r, l[i]);
+          }
+#pragma unroll
+          for (int d = 0; d < DT; ++d) part_store(parts.at, mine + 2 * ROWS + at0 + (i * DT + d) * 256, o[i][d]);
+        }
+      }
+      write = parts.last(a, &s_last);
+      if (write) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const uint32_t r = wave * 16 * RT + 16 * i + l16;
+          if (it.row0 + r < it.rows) l[i] = parts.join(r, at0 + i * DT * 256, 256, o[i], a.scale);
+        }
+      }
+    }
+    if (write) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const uint32_t r = wave * 16 * RT + 16 * i + l16;
+        if (it.row0 + r < it.rows) {
+          const float inv = inverse(l[i]);
+          uint16_t* p = out_at(a, sh, it, r);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const uint32_t at = 16 * d + 4 * g;
+            if (!PAD || at < dim) write4<E>(p + at, o[i][d], inv);
+          }
+        }
+      }
+    }
+    __syncthreads();  // s_last is reused
   }
 }
 
 struct AttnPlan {
-  uint32_t dp, rt, grid;
+  uint32_t dp, rt, grid;  // rt: 0 the narrow kernel, else 16-row tiles a wave of the wide one
   size_t part_off, ws_bytes;
 };
 
@@ -433,10 +784,10 @@ AttnPlan plan_attention(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint
   p.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   // rows of a request and key head, on the average
   const uint64_t rows = (uint64_t)tokens * (heads / kv_heads) / std::max(requests, 1u);
-  p.rt = rows <= 16 ? 1 : rows <= 32 || p.dp == 256 ? 2 : 4;
-  p.grid = kCUs * (p.rt == 1 ? 4 : p.rt == 2 ? 2 : 1);
+  p.rt = rows <= 16 ? 0 : rows <= 64 || p.dp == 256 ? 1 : 2;
+  p.grid = kCUs * (p.rt == 0 ? 3 : 2);
   p.part_off = ((size_t)p.grid * 4 + 255) / 256 * 256;
-  p.ws_bytes = p.part_off + (size_t)p.grid * 2 * (16 * p.rt) * (p.dp + 2) * 4;
+  p.ws_bytes = p.part_off + (size_t)p.grid * 2 * (p.rt ? 64 * p.rt : 16) * (p.dp + 2) * 4;
   return p;
 }
 
@@ -446,26 +797,37 @@ bool attn_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t 
          (uint64_t)tokens * heads <= (1u << 30);
 }
 
+template <class E, int DP, int RT, bool PAD>
+int launch_attention(const AttnArgs& a, uint32_t grid, hipStream_t st) {
+  if constexpr (RT == 0) {
+    hipLaunchKernelGGL((k_attention_narrow<E, DP, PAD>), dim3(grid), dim3(256), 0, st, a);
+  } else {
+    const auto kernel = k_attention_wide<E, DP, RT, PAD>;
+    if (Tile<DP>::kBytes > 64 * 1024 &&
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)Tile<DP>::kBytes) != hipSuccess)
+      return DGT_E_HIP;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), Tile<DP>::kBytes, st, a);
+  }
+  return launched();
+}
+
 template <class E, int DP, int RT>
 int launch_attention(const AttnArgs& a, uint32_t grid, hipStream_t st) {
-  if (a.dim == DP)
-    hipLaunchKernelGGL((k_tree_attention<E, DP, RT, false>), dim3(grid), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_tree_attention<E, DP, RT, true>), dim3(grid), dim3(256), 0, st, a);
-  return launched();
+  return a.dim == DP ? launch_attention<E, DP, RT, false>(a, grid, st) : launch_attention<E, DP, RT, true>(a, grid, st);
 }
 
 template <class E>
 int launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
   switch (p.dp * 8 + p.rt) {
+    case 64 * 8 + 0: return launch_attention<E, 64, 0>(a, p.grid, st);
     case 64 * 8 + 1: return launch_attention<E, 64, 1>(a, p.grid, st);
     case 64 * 8 + 2: return launch_attention<E, 64, 2>(a, p.grid, st);
-    case 64 * 8 + 4: return launch_attention<E, 64, 4>(a, p.grid, st);
+    case 128 * 8 + 0: return launch_attention<E, 128, 0>(a, p.grid, st);
     case 128 * 8 + 1: return launch_attention<E, 128, 1>(a, p.grid, st);
     case 128 * 8 + 2: return launch_attention<E, 128, 2>(a, p.grid, st);
-    case 128 * 8 + 4: return launch_attention<E, 128, 4>(a, p.grid, st);
+    case 256 * 8 + 0: return launch_attention<E, 256, 0>(a, p.grid, st);
     case 256 * 8 + 1: return launch_attention<E, 256, 1>(a, p.grid, st);
-    case 256 * 8 + 2: return launch_attention<E, 256, 2>(a, p.grid, st);
   }
   return DGT_E_UNSUPPORTED;
 }
