@@ -359,27 +359,24 @@ def dgt_dense_gemm(fmt, w, x, tile_n=128, scales=None, w_scale=1.0, y=None, ws=N
 
 
 # --------------------------------------------------------- serving operators
-# Their smallest calls take a few microseconds on the GPU, so the checks below
-# are single comparisons while all is well and only then spell out what is not.
+# Their smallest calls take a few microseconds on the GPU, and what the host does
+# before the launch is the larger part of them.  So each function first tests
+# everything in one expression; only where that fails are the checks made one by one,
+# to say which argument is wrong and how.
 def _check_array(t, name, dtype, shape, device):
     """t must be a contiguous tensor of `dtype` and exactly `shape` on `device`."""
-    if not (t is not None and getattr(t, "dtype", None) is dtype and t.shape == shape
-            and t.is_contiguous() and t.device == device):
-        _check_tensor(t, name, shape, (str(dtype),), device)
+    _check_tensor(t, name, shape, (str(dtype),), device)
 
 
 def _check_rows(t, name, dtypes, shape, device):
     """t must be a tensor of one of `dtypes` and exactly `shape` on `device` whose last
     dimension is contiguous; the other strides are free."""
-    if t is not None and getattr(t, "dtype", None) in dtypes and t.shape == shape \
-            and t.device == device and (t.stride(-1) == 1 or shape[-1] <= 1):
-        return
     _need(t is not None, "%s is required" % name)
     _need(hasattr(t, "data_ptr"), "%s must be a tensor" % name)
     _need(t.dtype in dtypes, "%s has dtype %s, expected one of %s"
           % (name, t.dtype, ", ".join(str(d) for d in dtypes)))
     _need(t.shape == shape, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    _need(t.stride(-1) == 1, "%s must be contiguous in its last dimension" % name)
+    _need(t.stride(-1) == 1 or shape[-1] <= 1, "%s must be contiguous in its last dimension" % name)
     _need(t.device == device, "%s is on %s, expected %s" % (name, t.device, device))
 
 
@@ -402,12 +399,17 @@ def _call(name, device, stream, *args):
     """One library call on `stream` (default: the device's current stream), with
     `device` as the current device."""
     import torch
-    fn = getattr(lib(), name)
-    if device.index is not None and device.index != torch.cuda.current_device():
+    index = device.index
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:  # the current stream's handle, without an object around it
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    fn = getattr(_lib or lib(), name)
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            code = fn(*args, _stream(stream))
+            code = fn(*args, handle)
     else:
-        code = fn(*args, _stream(stream))
+        code = fn(*args, handle)
     if code:
         raise DgtError(code, name)
 
@@ -431,20 +433,12 @@ class PagePlan:
         return cls(i32(requests + 1), i32(tokens), i32(tokens), i32(3), mask)
 
 
-def dgt_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, block_size, num_blocks,
-                  tokens, parents=None, mask_words=0, out=None, stream=None):
-    """Offsets, slots, positions and tree masks of one step, and the pages it takes from
-    the free list (written into block_table).  parents: int32[tokens] for drafted trees,
-    with mask_words 64-bit words a token (default: one); None for chains.  out: a PagePlan
-    to write into.  out.counts[1:2] is the next step's free_head."""
+def _check_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, tokens, parents, words, out):
     import torch
     i32, dev = torch.int32, ctx_lens.device
     (requests,) = _dims(ctx_lens, "ctx_lens", 1)
     (free,) = _dims(free_blocks, "free_blocks", 1)
     width = _dims(block_table, "block_table", 2)[1]
-    tokens, words = int(tokens), int(mask_words)
-    if parents is not None:
-        words = words or 1
     _check_array(ctx_lens, "ctx_lens", i32, (requests,), dev)
     _check_array(new_lens, "new_lens", i32, (requests,), dev)
     _check_array(free_blocks, "free_blocks", i32, (free,), dev)
@@ -463,20 +457,67 @@ def dgt_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, block
         if words:
             _check_array(out.mask, "out.mask", torch.int64, (tokens, words), dev)
     _check_gpu(dev)
+
+
+def dgt_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, block_size, num_blocks,
+                  tokens, parents=None, mask_words=0, out=None, stream=None):
+    """Offsets, slots, positions and tree masks of one step, and the pages it takes from
+    the free list (written into block_table).  parents: int32[tokens] for drafted trees,
+    with mask_words 64-bit words a token (default: one); None for chains.  out: a PagePlan
+    to write into.  out.counts[1:2] is the next step's free_head."""
+    import torch
+    i32, words = torch.int32, mask_words
+    if parents is not None and words == 0:
+        words = 1
+    _need(hasattr(ctx_lens, "data_ptr"), "ctx_lens must be a 1-D tensor")
+    dev, shape = ctx_lens.device, ctx_lens.shape
+    try:
+        good = (dev.type == "cuda" and ctx_lens.dtype is i32 and ctx_lens.is_contiguous() and len(shape) == 1
+                and new_lens.dtype is i32 and new_lens.shape == shape and new_lens.is_contiguous()
+                and new_lens.device == dev
+                and free_blocks.dtype is i32 and free_blocks.dim() == 1 and free_blocks.is_contiguous()
+                and free_blocks.device == dev
+                and free_head.dtype is i32 and free_head.shape == (1,) and free_head.device == dev
+                and block_table.dtype is i32 and block_table.dim() == 2 and block_table.shape[0] == shape[0]
+                and block_table.is_contiguous() and block_table.device == dev and tokens >= 0
+                and (words == 0 if parents is None else words > 0 and parents.dtype is i32
+                     and parents.shape == (tokens,) and parents.is_contiguous() and parents.device == dev))
+        if good and out is not None:
+            cu, slots, positions, counts, mask = out.cu, out.slots, out.positions, out.counts, out.mask
+            good = (cu.dtype is i32 and cu.shape == (shape[0] + 1,) and cu.is_contiguous() and cu.device == dev
+                    and slots.dtype is i32 and slots.shape == (tokens,) and slots.is_contiguous()
+                    and slots.device == dev
+                    and positions.dtype is i32 and positions.shape == (tokens,) and positions.is_contiguous()
+                    and positions.device == dev
+                    and counts.dtype is i32 and counts.shape == (3,) and counts.is_contiguous()
+                    and counts.device == dev
+                    and (words == 0 or mask.dtype is torch.int64 and mask.shape == (tokens, words)
+                         and mask.is_contiguous() and mask.device == dev))
+    except AttributeError:
+        good = False
+    if not good:
+        _check_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, tokens, parents, words, out)
     if out is None:
-        out = _made_on(stream, lambda: PagePlan.empty(requests, tokens, words, dev))
+        out = _made_on(stream, lambda: PagePlan.empty(shape[0], tokens, words, dev))
     # (a step of no tokens still has parents, if only by name)
     up = None if parents is None else parents.data_ptr() or out.counts.data_ptr()
-    _call("dgt_page_plan", dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), requests,
-          free_blocks.data_ptr(), free, free_head.data_ptr(), block_table.data_ptr(), width,
-          block_size, num_blocks, tokens, up, words, out.cu.data_ptr(), out.slots.data_ptr(),
-          out.positions.data_ptr(), out.mask.data_ptr() if words else None, out.counts.data_ptr())
+    _call("dgt_page_plan", dev, stream, ctx_lens.data_ptr(), new_lens.data_ptr(), shape[0],
+          free_blocks.data_ptr(), free_blocks.shape[0], free_head.data_ptr(), block_table.data_ptr(),
+          block_table.shape[1], block_size, num_blocks, tokens, up, words, out.cu.data_ptr(),
+          out.slots.data_ptr(), out.positions.data_ptr(), out.mask.data_ptr() if words else None,
+          out.counts.data_ptr())
     return out
 
 
-def _elements(t):
-    import torch
-    return {torch.bfloat16: DGT_ELT_BF16, torch.float16: DGT_ELT_F16, torch.float32: DGT_ELT_F32}.get(t.dtype)
+_ELEMENTS = {}
+
+
+def _elements():
+    """The library's number of each torch dtype that the operators take."""
+    if not _ELEMENTS:
+        import torch
+        _ELEMENTS.update({torch.bfloat16: DGT_ELT_BF16, torch.float16: DGT_ELT_F16, torch.float32: DGT_ELT_F32})
+    return _ELEMENTS
 
 
 def _check_caches(k_cache, v_cache):
@@ -492,21 +533,42 @@ def _check_caches(k_cache, v_cache):
     return blocks, heads, block, dim
 
 
-def dgt_kv_store(k, v, slots, k_cache, v_cache, stream=None):
-    """Write k, v [tokens, heads, dim] (the caches' dtype or float32, any row and head
-    strides) into the pages at `slots`; slots outside the pool are skipped."""
+def _check_kv_store(k, v, slots, k_cache, v_cache):
     import torch
     blocks, heads, block, dim = _check_caches(k_cache, v_cache)
     dev = k_cache.device
     tokens = _dims(k, "k", 3)[0]
-    dtypes = (torch.float32, k_cache.dtype)
-    _check_rows(k, "k", dtypes, (tokens, heads, dim), dev)
+    _check_rows(k, "k", (torch.float32, k_cache.dtype), (tokens, heads, dim), dev)
     _check_rows(v, "v", (k.dtype,), (tokens, heads, dim), dev)
     _check_array(slots, "slots", torch.int32, (tokens,), dev)
     _check_gpu(dev)
-    _call("dgt_kv_store", dev, stream, k.data_ptr(), v.data_ptr(), _elements(k), k.stride(0),
-          k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(), tokens, heads, dim,
-          _elements(k_cache), k_cache.data_ptr(), v_cache.data_ptr(), blocks, block)
+
+
+def dgt_kv_store(k, v, slots, k_cache, v_cache, stream=None):
+    """Write k, v [tokens, heads, dim] (the caches' dtype or float32, any row and head
+    strides) into the pages at `slots`; slots outside the pool are skipped."""
+    import torch
+    elements = _elements()
+    try:
+        dev, dtype, source = k_cache.device, k_cache.dtype, k.dtype
+        blocks, heads, block, dim = k_cache.shape
+        tokens = k.shape[0]
+        (k_row, k_head, k_one), (v_row, v_head, v_one) = k.stride(), v.stride()
+        good = (dev.type == "cuda" and (dtype is torch.bfloat16 or dtype is torch.float16)
+                and k_cache.is_contiguous() and v_cache.dtype is dtype
+                and v_cache.shape == (blocks, heads, dim, block) and v_cache.is_contiguous()
+                and v_cache.device == dev and (source is dtype or source is torch.float32)
+                and k.shape == (tokens, heads, dim) and k.device == dev and k_one == 1
+                and v.dtype is source and v.shape == (tokens, heads, dim) and v.device == dev and v_one == 1
+                and slots.dtype is torch.int32 and slots.shape == (tokens,) and slots.is_contiguous()
+                and slots.device == dev)
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_kv_store(k, v, slots, k_cache, v_cache)
+    _call("dgt_kv_store", dev, stream, k.data_ptr(), v.data_ptr(), elements[source], k_row, k_head, v_row,
+          v_head, slots.data_ptr(), tokens, heads, dim, elements[dtype], k_cache.data_ptr(),
+          v_cache.data_ptr(), blocks, block)
 
 
 def dgt_tree_attention_workspace(q_shape, kv_heads, requests) -> int:
@@ -518,12 +580,7 @@ def dgt_tree_attention_workspace(q_shape, kv_heads, requests) -> int:
     return n
 
 
-def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None, scale=None,
-                       out=None, ws=None, stream=None):
-    """Attention of the new tokens q [tokens, heads, dim] over each request's cached tokens
-    and over those of its new tokens (already stored) that `mask` (dgt_page_plan) lets a
-    token see; without a mask each sees the ones before it and itself.  scale defaults to
-    dim ** -0.5.  Rows past cu[-1] of `out` are not written."""
+def _check_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask, out, ws):
     import torch
     blocks, kv_heads, block, dim = _check_caches(k_cache, v_cache)
     dev = k_cache.device
@@ -534,7 +591,6 @@ def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None
     _check_array(block_table, "block_table", torch.int32, (requests, width), dev)
     _check_array(ctx_lens, "ctx_lens", torch.int32, (requests,), dev)
     _check_array(cu, "cu", torch.int32, (requests + 1,), dev)
-    words = 0
     if mask is not None:
         words = _dims(mask, "mask", 2)[1]
         _need(words > 0, "mask needs at least one word a token")
@@ -542,18 +598,59 @@ def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None
     if out is not None:
         _check_rows(out, "out", (q.dtype,), (tokens, heads, dim), dev)
     if ws is not None:
-        _check_array(ws, "ws", torch.uint8, (ws.numel(),), dev)
+        _check_array(ws, "ws", torch.uint8, (None,), dev)
     _check_gpu(dev)
+
+
+def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None, scale=None,
+                       out=None, ws=None, stream=None):
+    """Attention of the new tokens q [tokens, heads, dim] over each request's cached tokens
+    and over those of its new tokens (already stored) that `mask` (dgt_page_plan) lets a
+    token see; without a mask each sees the ones before it and itself.  scale defaults to
+    dim ** -0.5.  Rows past cu[-1] of `out` are not written."""
+    import torch
+    i32, words = torch.int32, 0
+    try:
+        dev, dtype = k_cache.device, k_cache.dtype
+        blocks, kv_heads, block, dim = k_cache.shape
+        shape = tokens, heads, _ = q.shape
+        requests, width = block_table.shape
+        q_row, q_head, q_one = q.stride()
+        good = (dev.type == "cuda" and (dtype is torch.bfloat16 or dtype is torch.float16)
+                and k_cache.is_contiguous() and v_cache.dtype is dtype
+                and v_cache.shape == (blocks, kv_heads, dim, block) and v_cache.is_contiguous()
+                and v_cache.device == dev
+                and q.dtype is dtype and shape[2] == dim and q_one == 1 and q.device == dev
+                and kv_heads > 0 and heads % kv_heads == 0
+                and block_table.dtype is i32 and block_table.is_contiguous() and block_table.device == dev
+                and ctx_lens.dtype is i32 and ctx_lens.shape == (requests,) and ctx_lens.is_contiguous()
+                and ctx_lens.device == dev
+                and cu.dtype is i32 and cu.shape == (requests + 1,) and cu.is_contiguous() and cu.device == dev)
+        if mask is not None:
+            words = mask.shape[1]
+            good = (good and words > 0 and mask.dtype is torch.int64 and mask.shape == (tokens, words)
+                    and mask.is_contiguous() and mask.device == dev)
+        if out is not None:
+            good = good and out.dtype is dtype and out.shape == shape and out.stride(2) == 1 and out.device == dev
+        if ws is not None:
+            good = good and ws.dtype is torch.uint8 and ws.dim() == 1 and ws.is_contiguous() and ws.device == dev
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask, out, ws)
     if out is None:
-        out = _made_on(stream, lambda: torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev))
+        out = _made_on(stream, lambda: torch.empty(shape, dtype=dtype, device=dev))
+        out_row, out_head = heads * dim, dim
+    else:
+        out_row, out_head, _ = out.stride()
     if ws is None:
-        nbytes = dgt_tree_attention_workspace(q.shape, kv_heads, requests)
+        nbytes = dgt_tree_attention_workspace(shape, kv_heads, requests)
         ws = _made_on(stream, lambda: alloc_workspace(nbytes, dev))
-    _call("dgt_tree_attention", dev, stream, _elements(q), q.data_ptr(), q.stride(0), q.stride(1),
+    _call("dgt_tree_attention", dev, stream, _elements()[dtype], q.data_ptr(), q_row, q_head,
           k_cache.data_ptr(), v_cache.data_ptr(), blocks, block, block_table.data_ptr(), width,
           ctx_lens.data_ptr(), cu.data_ptr(), requests, tokens, heads, kv_heads, dim,
           mask.data_ptr() if words and tokens else None, words if tokens else 0,
-          dim ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1),
+          dim ** -0.5 if scale is None else scale, out.data_ptr(), out_row, out_head,
           ws.data_ptr(), ws.numel())
     return out
 
@@ -565,18 +662,14 @@ def dgt_lora_workspace(tokens, requests, n, k, rank) -> int:
     return nbytes
 
 
-def dgt_lora_add(y, x, a, b, scaling, adapters, cu, out=None, ws=None, stream=None):
-    """out[t] = y[t] + scaling[i] * (x[t] a[i]^T) b[i]^T, i = adapters[request of t] (rows of
-    requests with an id outside the adapters: out[t] = y[t]).  x bf16 [tokens, k],
-    a bf16 [count, rank, k], b bf16 [count, n, rank], y float32 [tokens, n].  out defaults
-    to y (in place)."""
+def _check_lora_add(y, x, a, b, scaling, adapters, cu, out, ws):
     import torch
-    dev = y.device
+    f32, bf16 = torch.float32, torch.bfloat16
     tokens, n = _dims(y, "y", 2)
+    dev = y.device
     k = _dims(x, "x", 2)[1]
     count, rank, _ = _dims(a, "a", 3)
     (requests,) = _dims(adapters, "adapters", 1)
-    f32, bf16 = torch.float32, torch.bfloat16
     _check_rows(y, "y", (f32,), (tokens, n), dev)
     _check_rows(x, "x", (bf16,), (tokens, k), dev)
     _check_array(a, "a", bf16, (count, rank, k), dev)
@@ -584,17 +677,50 @@ def dgt_lora_add(y, x, a, b, scaling, adapters, cu, out=None, ws=None, stream=No
     _check_array(scaling, "scaling", f32, (count,), dev)
     _check_array(adapters, "adapters", torch.int32, (requests,), dev)
     _check_array(cu, "cu", torch.int32, (requests + 1,), dev)
-    if out is None:
-        out = y
-    else:
+    if out is not None:
         _check_rows(out, "out", (f32,), (tokens, n), dev)
     if ws is not None:
-        _check_array(ws, "ws", torch.uint8, (ws.numel(),), dev)
+        _check_array(ws, "ws", torch.uint8, (None,), dev)
     _check_gpu(dev)
+
+
+def dgt_lora_add(y, x, a, b, scaling, adapters, cu, out=None, ws=None, stream=None):
+    """out[t] = y[t] + scaling[i] * (x[t] a[i]^T) b[i]^T, i = adapters[request of t] (rows of
+    requests with an id outside the adapters: out[t] = y[t]).  x bf16 [tokens, k],
+    a bf16 [count, rank, k], b bf16 [count, n, rank], y float32 [tokens, n].  out defaults
+    to y (in place)."""
+    import torch
+    f32, bf16, i32 = torch.float32, torch.bfloat16, torch.int32
+    try:
+        dev = y.device
+        shape = tokens, n = y.shape
+        k = x.shape[1]
+        count, rank, _ = a.shape
+        (requests,) = adapters.shape
+        (y_row, y_one), (x_row, x_one) = y.stride(), x.stride()
+        good = (dev.type == "cuda" and y.dtype is f32 and (y_one == 1 or n == 1)
+                and x.dtype is bf16 and x.shape == (tokens, k) and x_one == 1 and x.device == dev
+                and a.dtype is bf16 and a.shape == (count, rank, k) and a.is_contiguous() and a.device == dev
+                and b.dtype is bf16 and b.shape == (count, n, rank) and b.is_contiguous() and b.device == dev
+                and scaling.dtype is f32 and scaling.shape == (count,) and scaling.is_contiguous()
+                and scaling.device == dev
+                and adapters.dtype is i32 and adapters.is_contiguous() and adapters.device == dev
+                and cu.dtype is i32 and cu.shape == (requests + 1,) and cu.is_contiguous() and cu.device == dev)
+        if out is not None:
+            good = (good and out.dtype is f32 and out.shape == shape and (out.stride(1) == 1 or n == 1)
+                    and out.device == dev)
+        if ws is not None:
+            good = good and ws.dtype is torch.uint8 and ws.dim() == 1 and ws.is_contiguous() and ws.device == dev
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_lora_add(y, x, a, b, scaling, adapters, cu, out, ws)
+    if out is None:
+        out = y
     if ws is None:
         nbytes = dgt_lora_workspace(tokens, requests, n, k, rank)
         ws = _made_on(stream, lambda: torch.empty(nbytes, dtype=torch.uint8, device=dev))
-    _call("dgt_lora_add", dev, stream, y.data_ptr(), y.stride(0), x.data_ptr(), x.stride(0),
+    _call("dgt_lora_add", dev, stream, y.data_ptr(), y_row, x.data_ptr(), x_row,
           a.data_ptr(), b.data_ptr(), scaling.data_ptr(), count, adapters.data_ptr(), cu.data_ptr(),
           requests, tokens, n, k, rank, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel())
     return out
