@@ -96,7 +96,7 @@ inline bool power_of_two(uint32_t v) { return v && !(v & (v - 1)); }
 inline int launched() { return hipGetLastError() == hipSuccess ? DGT_OK : DGT_E_HIP; }
 
 // Page sizes that the operators take, and their bound on requests per call.
-constexpr uint32_t kMinBlock = 8, kMaxBlock = 1024, kMaxRequests = 16384;
+constexpr uint32_t kMinBlock = 8, kMaxBlock = 1024, kMaxRequests = 8192;
 inline bool block_ok(uint32_t block) {
   return power_of_two(block) && block >= kMinBlock && block <= kMaxBlock;
 }

@@ -21,12 +21,14 @@ namespace {
 // between waves passes through LDS, and a row's maximum and sum need two lane
 // exchanges.
 //
-// Work is cut into units of 128 keys (32 a wave) of one (request, key head, tile
-// of rows); the units of the whole batch are numbered in that order and dealt to
-// the workgroups in equal runs, whatever the lengths.  A run that holds only a
-// part of a tile's keys leaves maximum, sum and unscaled output in the
-// workspace, and the workgroup that comes last adds the parts up in the order of
-// the keys.
+// Work is cut into units of 128 keys of one (request, key head, tile of rows), and
+// the units of the whole batch are numbered and dealt to the workgroups in equal
+// runs, whatever the lengths.  The keys of a request fall into spans of a run's
+// length; units are numbered request, head, span, tile of rows, key.  So the
+// tiles of one span go to neighbouring workgroups, which read the same keys at the
+// same time, from the cache of the die they share.  A run that holds only a part of
+// a tile's keys leaves maximum, sum and unscaled output in the workspace, and the
+// workgroup that comes last adds the parts up in the order of the keys.
 struct AttnArgs {
   const uint16_t *q, *kc, *vc;
   const int32_t *table, *ctx, *cu;
@@ -41,6 +43,7 @@ struct AttnArgs {
 
 constexpr uint32_t kWaves = 4, kTileKeys = 32, kUnitKeys = kWaves * kTileKeys;
 constexpr uint32_t kMinUnits = 2;  // a workgroup's run is not cut below this
+constexpr uint32_t kDies = 8;
 
 struct Shape {  // of one request
   uint32_t first, count, ctx, keys, tiles, chunks;
@@ -58,11 +61,25 @@ __device__ __forceinline__ Shape request_shape(const AttnArgs& a, uint32_t b) {
   return s;
 }
 
+// (The host has made sure that the batch's units stay below 2^31.)
 template <int ROWS>
-__device__ __forceinline__ uint64_t request_units(const AttnArgs& a, uint32_t b) {
+__device__ __forceinline__ uint32_t request_units(const AttnArgs& a, uint32_t b) {
   const Shape s = request_shape<ROWS>(a, b);
-  return (uint64_t)s.tiles * s.chunks * a.heads;
+  return s.tiles * s.chunks * a.heads;
 }
+
+// n things dealt to `count` holders: the first n % count hold one more.
+struct Deal {
+  uint32_t n, count, each, more;
+  __device__ __forceinline__ Deal(uint32_t n, uint32_t count)
+      : n(n), count(count), each(n / count), more(n - each * count) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t i) const { return i * each + min(i, more); }
+  __device__ __forceinline__ uint32_t owner(uint32_t x) const {
+    const uint32_t longer = more * (each + 1);
+    return x < longer ? x / (each + 1) : more + (x - longer) / each;
+  }
+  __device__ __forceinline__ uint32_t most() const { return each + (more != 0); }
+};
 
 // Parts pass between workgroups that may sit on different dies, so they are
 // written through and read past the caches that the dies do not share (the sc1
@@ -101,84 +118,100 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnArgs& a, const Shape& s,
 
 // A workgroup's run of units [u, end), and the request that holds unit u.
 struct Run {
-  uint64_t u, end, base, units;  // base: the request's first unit
-  uint32_t wgs, b;
+  Deal deal;         // of the batch's units to the runs
+  uint32_t wg;       // this run's number
+  uint32_t u, end;
+  uint32_t b, base;  // the request and its first unit
 };
 
-// Deals the batch's units to the workgroups.  Every workgroup adds up the lengths
-// for itself, which costs less than a launch; false: nothing is left for this one.
+// Every workgroup adds up the lengths for itself, which costs less than a launch;
+// count 0: nothing is left for this one.
 template <int ROWS>
-__device__ __forceinline__ bool find_run(const AttnArgs& a, uint64_t* s_sum, Run* out) {
+__device__ __forceinline__ Run find_run(const AttnArgs& a, uint32_t* s_sum) {
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const uint32_t per = (a.requests + 255) / 256;
   const uint32_t b_lo = min(t * per, a.requests), b_hi = min(b_lo + per, a.requests);
-  uint64_t mine = 0;
+  uint32_t mine = 0;
   for (uint32_t b = b_lo; b < b_hi; ++b) mine += request_units<ROWS>(a, b);
-  uint64_t scan = mine;
+  uint32_t scan = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = __shfl_up((unsigned long long)scan, d, 64);
+    const uint32_t o = __shfl_up(scan, d, 64);
     if (lane >= (uint32_t)d) scan += o;
   }
   if (lane == 63) s_sum[wave] = scan;
   __syncthreads();
-  uint64_t units = 0;
+  uint32_t units = 0;
   for (uint32_t w = 0; w < 4; ++w) {
     if (w < wave) scan += s_sum[w];
     units += s_sum[w];
   }
-  if (units == 0) return false;
-  const uint64_t most = (units + kMinUnits - 1) / kMinUnits;
-  const uint32_t wgs = (uint32_t)min((uint64_t)gridDim.x, most);
-  if (blockIdx.x >= wgs) return false;
-  const uint64_t u = units * blockIdx.x / wgs;
-  const uint64_t before = scan - mine;
-  if (before <= u && u < scan) {  // one thread holds the run's first unit
-    uint64_t base = before;
-    uint32_t b = b_lo;
+  units = __builtin_amdgcn_readfirstlane(units);
+  Run run{Deal(units, min(gridDim.x, max((units + kMinUnits - 1) / kMinUnits, 1u))), 0, 0, 0, 0, 0};
+  // Workgroups go round the dies; neighbouring runs, which read the same keys for
+  // other rows, stay on one, so that its cache serves all but the first.
+  const uint32_t runs = run.deal.count, die = blockIdx.x % kDies, nth = blockIdx.x / kDies;
+  if (units == 0 || nth >= runs / kDies + (die < runs % kDies)) return run;
+  run.wg = die * (runs / kDies) + min(die, runs % kDies) + nth;
+  run.u = run.deal.begin(run.wg);
+  run.end = run.deal.begin(run.wg + 1);
+  const uint32_t before = scan - mine;
+  if (before <= run.u && run.u < scan) {  // one thread holds the run's first unit
+    uint32_t base = before, b = b_lo;
     for (;; ++b) {
-      const uint64_t n = request_units<ROWS>(a, b);
-      if (u < base + n) break;
+      const uint32_t n = request_units<ROWS>(a, b);
+      if (run.u < base + n) break;
       base += n;
     }
     s_sum[4] = b;
     s_sum[5] = base;
   }
   __syncthreads();
-  out->u = u;
-  out->end = units * (blockIdx.x + 1) / wgs;
-  out->units = units;
-  out->wgs = wgs;
-  out->b = __builtin_amdgcn_readfirstlane((uint32_t)s_sum[4]);
-  out->base = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(s_sum[5] >> 32)) << 32 |
-              __builtin_amdgcn_readfirstlane((uint32_t)s_sum[5]);
-  return true;
+  run.b = __builtin_amdgcn_readfirstlane(s_sum[4]);
+  run.base = __builtin_amdgcn_readfirstlane(s_sum[5]);
+  return run;
 }
 
-// The part of one (request, key head, tile of rows) that the run covers.
+// The request's chunks in spans as long as the longest run, so that runs side by
+// side are at the same key; the last one is from half to one and a half as long.
+struct Spans {
+  uint32_t chunks, len, count;
+  __device__ __forceinline__ Spans(const Run& run, const Shape& sh)
+      : chunks(sh.chunks), len(run.deal.most()), count(max((chunks + len / 2) / len, 1u)) {}
+  __device__ __forceinline__ uint32_t begin(uint32_t i) const { return i < count ? i * len : chunks; }
+  __device__ __forceinline__ uint32_t owner(uint32_t chunk) const { return min(chunk / len, count - 1); }
+};
+
+// What the run covers of one (request, key head, span, tile of rows).
 struct Item {
-  uint32_t head, row0, rows;  // rows: of the request and head
-  uint32_t c0, c1;            // chunks of its keys
-  uint64_t first;             // unit of chunk 0
+  uint32_t head, tile, row0, rows;  // rows: of the request and head
+  uint32_t c0, c1;                  // chunks of its keys
+  uint32_t base;                    // first unit of the head
+  uint32_t first;                   // unit of the span's first chunk for this tile
   bool whole;
 };
 
 template <int ROWS>
 __device__ __forceinline__ Item next_item(const AttnArgs& a, Run* run, Shape* sh) {
-  while (run->u >= run->base + (uint64_t)sh->tiles * sh->chunks * a.heads) {
-    run->base += (uint64_t)sh->tiles * sh->chunks * a.heads;
+  while (run->u - run->base >= sh->tiles * sh->chunks * a.heads) {
+    run->base += sh->tiles * sh->chunks * a.heads;
     *sh = request_shape<ROWS>(a, ++run->b);
   }
-  const uint32_t in = (uint32_t)(run->u - run->base), item = in / sh->chunks;
+  const Spans spans(*run, *sh);
+  const uint32_t in = run->u - run->base, per = sh->tiles * sh->chunks, left = in % per;
   Item it;
-  it.c0 = in % sh->chunks;
-  it.head = item / sh->tiles;
-  it.row0 = item % sh->tiles * ROWS;
+  it.head = in / per;
+  it.base = run->u - left;
+  const uint32_t span = spans.owner(left / sh->tiles), begin = spans.begin(span), len = spans.begin(span + 1) - begin;
+  const uint32_t within = left - sh->tiles * begin;
+  it.tile = within / len;
+  it.row0 = it.tile * ROWS;
   it.rows = sh->count * a.group;
-  it.first = run->u - it.c0;
-  it.c1 = (uint32_t)min((uint64_t)sh->chunks, run->end - it.first);
+  it.c0 = begin + within % len;
+  it.first = run->u - within % len;
+  it.c1 = min(begin + len, it.c0 + (run->end - run->u));
   it.whole = it.c0 == 0 && it.c1 == sh->chunks;
-  run->u = it.first + it.c1;
+  run->u += it.c1 - it.c0;
   return it;
 }
 
@@ -190,59 +223,114 @@ __device__ __forceinline__ uint16_t* out_at(const AttnArgs& a, const Shape& sh, 
 // 1 / the sum of weights; 0 where the row saw nothing (a NaN stays one).
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
-// Where the parts of an item lie: its workgroups are owner(first unit) ..
-// owner(last unit); each has room for two, one item that it ends or crosses and
-// one that it begins.  A part is m[ROWS], l[ROWS] and the outputs, in floats.
+// Where the parts of a tile of rows lie.  Each of its spans is held by the runs from
+// owner(span's first unit) to owner(its last); a run has room for three parts: one
+// of a span that began before it, and one of a span that begins in either half of it
+// (spans of a tile that is not whole are no shorter than half the longest run).  A part is m[ROWS], l[ROWS] and the
+// outputs, in floats.
+constexpr uint32_t kRoom = 3;
+
 template <int ROWS, int DP>
 struct Parts {
   static constexpr uint32_t kFloats = ROWS * (DP + 2);
-  uint32_t w0, w1;
+  const Deal runs;
+  const Spans spans;
+  uint32_t base;  // first unit of the head
+  uint32_t tiles, tile;
   __amdgpu_buffer_rsrc_t at;
-  __device__ __forceinline__ Parts(const AttnArgs& a, const Run& run, const Item& it, uint32_t chunks) {
-    auto owner = [&](uint64_t x) {  // the last w with floor(units * w / wgs) <= x
-      return (uint32_t)(((x + 1) * run.wgs - 1) / run.units);
-    };
-    w0 = owner(it.first);
-    w1 = owner(it.first + chunks - 1);
+  __device__ __forceinline__ Parts(const AttnArgs& a, const Run& run, const Item& it, const Shape& sh)
+      : runs(run.deal), spans(run, sh), base(it.base), tiles(sh.tiles), tile(it.tile) {
     // raw 32-bit data; accesses are checked against the length
-    at = __builtin_amdgcn_make_buffer_rsrc(a.parts, 0, gridDim.x * 2 * kFloats * 4, 0x00027000);
+    at = __builtin_amdgcn_make_buffer_rsrc(a.parts, 0, gridDim.x * kRoom * kFloats * 4, 0x00027000);
   }
-  __device__ __forceinline__ uint32_t of(uint32_t w) const { return (2 * w + (w == w0)) * kFloats; }
+  // number of the part that run w has of the span whose first unit is x
+  __device__ __forceinline__ uint32_t number(uint32_t w, uint32_t x) const {
+    const uint32_t begin = runs.begin(w);
+    return kRoom * w + (x < begin ? 0u : 1u + (x - begin) / ((runs.most() + 1) / 2));
+  }
+  __device__ __forceinline__ uint32_t first(uint32_t span) const {
+    const uint32_t b = spans.begin(span), e = spans.begin(span + 1);
+    return base + tiles * b + tile * (e - b);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t w, uint32_t x) const { return number(w, x) * kFloats; }
 
-  // Counts this workgroup's part in; true for the item's last.  Waiting for the
+  // The parts in the order of the keys: run w has one of span i.
+  struct Place {
+    uint32_t i, x, w, last;  // x: the span's first unit, last: its last run
+  };
+  __device__ __forceinline__ Place begin(uint32_t i) const {
+    const uint32_t x = first(i);
+    return Place{i, x, runs.owner(x), runs.owner(x + spans.begin(i + 1) - spans.begin(i) - 1)};
+  }
+  __device__ __forceinline__ void next(Place& p) const {
+    if (p.w < p.last) ++p.w;
+    else if (p.i + 1 < spans.count) p = begin(p.i + 1);
+    else p.i = spans.count;
+  }
+  __device__ __forceinline__ uint32_t count() const {
+    uint32_t n = 0;
+    for (uint32_t i = 0; i < spans.count; ++i) {
+      const Place p = begin(i);
+      n += p.last - p.w + 1;
+    }
+    return n;
+  }
+
+  // Counts this workgroup's part in; true for the tile's last.  Waiting for the
   // stores before counting orders them without the cache writeback of a fence.
   __device__ __forceinline__ bool last(const AttnArgs& a, uint32_t* s_last) const {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     if (threadIdx.x == 0) {
-      const uint32_t old = __hip_atomic_fetch_add(a.counters + w0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      *s_last = old == w1 - w0;
-      if (old == w1 - w0)  // ready for the next call
-        __hip_atomic_store(a.counters + w0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t others = count() - 1;
+      const uint32_t x = first(0);
+      uint32_t* counter = a.counters + number(runs.owner(x), x);
+      const uint32_t old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      *s_last = old == others;
+      if (old == others)  // ready for the next call
+        __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     return *s_last != 0;
   }
 
   // Joins row r of the parts in the order of the keys: N pieces of four outputs at
-  // at0, at0 + step, ..., within a part.  Returns the sum of weights.
+  // at0, at0 + step, ..., within a part.  Returns the sum of weights.  The parts come
+  // from other dies' memory, microseconds away, so four are asked for at a time.
   template <int N>
   __device__ __forceinline__ float join(uint32_t r, uint32_t at0, uint32_t step, floatx4 (&o)[N], float scale) const {
+    constexpr int kBatch = 4;
     float m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = floatx4{};
-    for (uint32_t w = w0; w <= w1; ++w) {
-      const uint32_t p = of(w);
-      const float mw = part_load(at, p + r), lw = part_load(at, p + ROWS + r);
-      floatx4 ow[N];
+    for (Place p = begin(0); p.i < spans.count;) {
+      float mw[kBatch], lw[kBatch];
+      floatx4 ow[kBatch][N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) ow[i] = part_load4(at, p + 2 * ROWS + at0 + i * step);
-      const float now = fmaxf(m, mw), ref = now == -INFINITY ? 0.f : now;
-      const float f = __builtin_amdgcn_exp2f((m - ref) * scale), fw = __builtin_amdgcn_exp2f((mw - ref) * scale);
-      m = now;
-      l = fmaf(lw, fw, l * f);
+      for (int k = 0; k < kBatch; ++k) {
+        mw[k] = -INFINITY;
+        lw[k] = 0.f;
+        if (p.i < spans.count) {
+          const uint32_t part = of(p.w, p.x);
+          mw[k] = part_load(at, part + r);
+          lw[k] = part_load(at, part + ROWS + r);
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = o[i] * f + ow[i] * fw;
+          for (int i = 0; i < N; ++i) ow[k][i] = part_load4(at, part + 2 * ROWS + at0 + i * step);
+          next(p);
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) ow[k][i] = floatx4{};
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float now = fmaxf(m, mw[k]), ref = now == -INFINITY ? 0.f : now;
+        const float f = __builtin_amdgcn_exp2f((m - ref) * scale), fw = __builtin_amdgcn_exp2f((mw[k] - ref) * scale);
+        m = now;
+        l = fmaf(lw[k], fw, l * f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = o[i] * f + ow[k][i] * fw;
+      }
     }
     return l;
   }
@@ -274,19 +362,35 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Shape& sh,
   }
 }
 
+// Maximum and sum over the four lanes that hold one row (lanes l, l + 16, l + 32,
+// l + 48): the swaps exchange half waves and neighbouring rows of 16 lanes.
+__device__ __forceinline__ float row_max(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(fmaxf(v, __uint_as_float(a[0])), __uint_as_float(a[1]));
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(fmaxf(v, __uint_as_float(a[0])), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
 // One step of the running softmax over the 4 N scores that a lane holds of its
 // row: s becomes the weights, m and l are updated; returns what the output so
 // far is multiplied by.  l counts this lane's keys only, the lanes of a row are
 // added at the end.
 template <int N>
 __device__ __forceinline__ float softmax_step(floatx4 (&s)[N], float& m, float& l, float scale) {
-  float top = -INFINITY;
+  // (a maximum of three is one instruction; of two it is two more, to settle NaNs)
+  float top = m;
 #pragma unroll
-  for (int h = 0; h < N; ++h)
-    top = fmaxf(top, fmaxf(fmaxf(s[h][0], s[h][1]), fmaxf(s[h][2], s[h][3])));
-  top = fmaxf(top, __shfl_xor(top, 16, 64));
-  top = fmaxf(top, __shfl_xor(top, 32, 64));
-  const float now = fmaxf(m, top);
+  for (int h = 0; h < N; ++h) {
+    top = fmaxf(fmaxf(top, s[h][0]), s[h][1]);
+    top = fmaxf(fmaxf(top, s[h][2]), s[h][3]);
+  }
+  const float now = row_max(top);
   // a row that has seen nothing yet keeps -inf; its weights are exp2(-inf) = 0
   const float ref = now == -INFINITY ? 0.f : now * scale;
   const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(fmaf(m, scale, -ref));
@@ -326,11 +430,11 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
   constexpr int KS = DP / 32, DT = DP / 16, ROWS = 16;
   __shared__ float s_o[ROWS][DP + 4];
   __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
-  __shared__ uint64_t s_sum[6];
+  __shared__ uint32_t s_sum[6];
   __shared__ uint32_t s_last;
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, g = lane >> 4, l16 = lane & 15;
-  Run run;
-  if (!find_run<ROWS>(a, s_sum, &run)) return;
+  Run run = find_run<ROWS>(a, s_sum);
+  if (run.u == run.end) return;
   Shape sh = request_shape<ROWS>(a, run.b);
   const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
   const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
@@ -405,8 +509,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
       }
 
       const float keep = softmax_step<2>(s, m, l, a.scale);
+      if (__any(keep != 1.f)) {  // a maximum moved: rare once some keys are seen
 #pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] *= keep;
+        for (int d = 0; d < DT; ++d) o[d] *= keep;
+      }
       if (!odd_values) {
         const u32x4 p = weights<E>(s[0], s[1]);
 #pragma unroll
@@ -440,8 +546,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
     }
 
     // the four waves' parts, added in order
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
+    l = row_sum(l);
     if (g == 0) {
       s_m[wave][l16] = m;
       s_l[wave][l16] = l;
@@ -479,8 +584,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
           write4<E>(out_at(a, sh, it, r) + d, *reinterpret_cast<floatx4*>(&s_o[r][d]), inverse(s_l[0][r]));
       }
     } else {
-      const Parts<ROWS, DP> parts(a, run, it, sh.chunks);
-      const uint32_t mine = parts.of(blockIdx.x);
+      const Parts<ROWS, DP> parts(a, run, it, sh);
+      const uint32_t mine = parts.of(run.wg, it.first);
       if (t < live) {
         part_store(parts.at, mine + t, s_m[0][t]);
         part_store(parts.at, mine + ROWS + t, s_l[0][t]);
@@ -529,11 +634,12 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
   u32x4* s_k = lds;                       // [2][kPieces]
   u32x4* s_v = lds + 2 * T::kPieces;      // [2][kPieces]
   uint32_t* s_page = reinterpret_cast<uint32_t*>(lds + 4 * T::kPieces);
-  __shared__ uint64_t s_sum[6];
+  __shared__ uint32_t s_sum[6];
   __shared__ uint32_t s_last;
-  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, g = lane >> 4, l16 = lane & 15;
-  Run run;
-  if (!find_run<ROWS>(a, s_sum, &run)) return;
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const uint32_t g = lane >> 4, l16 = lane & 15;
+  Run run = find_run<ROWS>(a, s_sum);
+  if (run.u == run.end) return;
   Shape sh = request_shape<ROWS>(a, run.b);
   const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
   const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
@@ -544,6 +650,11 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
   // row; which of the row's pieces it is.
   const uint32_t log_part = log_vp + (uint32_t)__builtin_ctz(DP);
   auto value_piece = [&](uint32_t x) { return (x >> log_part << log_vp) + (x & ((1u << log_vp) - 1)); };
+
+  // a lane's place within its wave's pieces of a load, and a page of all heads, in bytes
+  const uint32_t k_lane = 2 * ((lane / T::kKPieces) * dim + 8 * (lane % T::kKPieces));
+  const uint32_t v_lane = 2 * (((lane >> log_vp) << a.log_block) + 8 * (lane & ((1u << log_vp) - 1)));
+  const uint32_t page_bytes = (uint32_t)(2 * page_len) * a.heads;
 
   while (run.u < run.end) {
     const Item it = next_item<ROWS>(a, &run, &sh);
@@ -563,6 +674,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
     }
     const int32_t* pages = a.table + (uint64_t)run.b * a.width;
     const uint32_t k_end = min(it.c1 * kUnitKeys, sh.keys);
+    const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.kc + it.head * page_len);
+    const uint8_t* values = reinterpret_cast<const uint8_t*>(a.vc + it.head * page_len);
 
     // in pieces of as many pages as the LDS has room for; a piece ends on a page's end
     for (uint32_t seg = it.c0 * kUnitKeys, seg_end; seg < k_end; seg = seg_end) {
@@ -572,38 +685,46 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
       for (uint32_t i = t; i < n_pages; i += 256) s_page[i] = (uint32_t)pages[page0 + i];
       __syncthreads();
 
+      // Pages of a tile's groups of 8 keys, one a lane (repeating); ~0 where the group
+      // does not exist.  `absent` has a bit for each such group.
+      constexpr uint32_t kGroups = T::kKeys / 8;
+      auto tile_pages = [&](uint32_t kb) {
+        const uint32_t key = kb + 8 * (lane % kGroups);
+        const uint32_t page = key < seg_end ? s_page[(key >> a.log_block) - page0] : ~0u;
+        return page < a.blocks ? page : ~0u;
+      };
       u32x4 rk[T::kEach], rv[T::kEach];
-      bool odd = false;
+      uint32_t absent = 0, coming = tile_pages(seg);
+      // A wave's pieces of one load lie in one page: key rows in a group of 8 keys,
+      // values in the part of the tile that a page holds.  So the page is a scalar,
+      // and nothing branches: where a group does not exist, page 0 is read instead.
       auto load = [&](uint32_t kb) {
-        odd = false;
+        absent = (uint32_t)__ballot(coming == ~0u) & ((1u << kGroups) - 1);
+        const uint32_t pages_now = coming == ~0u ? 0u : coming;
+        coming = tile_pages(kb + T::kKeys);
+        const uint32_t inside = kb & in_page;  // where the tile begins in a page longer than it
 #pragma unroll
         for (uint32_t j = 0; j < T::kEach; ++j) {
-          const uint32_t x = t + 256 * j, key = kb + x / T::kKPieces, d = 8 * (t % T::kKPieces);
-          rk[j] = u32x4{};
-          if (key < seg_end && (!PAD || d < dim)) {
-            const uint32_t page = s_page[(key >> a.log_block) - page0];
-            if (page < a.blocks)
-              rk[j] = *reinterpret_cast<const u32x4*>(a.kc + ((uint64_t)page * a.heads + it.head) * page_len +
-                                                      ((key & in_page) * dim + d));
-          }
+          const uint32_t row_w = (64 * wave + 256 * j) / T::kKPieces;
+          const uint8_t* from = keys + (uint64_t)__builtin_amdgcn_readlane(pages_now, row_w / 8) * page_bytes;
+          const uint32_t at = (inside + (row_w & in_page)) * (2 * dim) + k_lane;
+          rk[j] = !PAD || 8 * (t % T::kKPieces) < dim ? *reinterpret_cast<const u32x4*>(from + at) : u32x4{};
         }
 #pragma unroll
         for (uint32_t j = 0; j < T::kEach; ++j) {
-          const uint32_t x = t + 256 * j, y = x & ((DP << log_vp) - 1), row = y >> log_vp;
-          const uint32_t key = kb + 8 * value_piece(x);
-          rv[j] = u32x4{};
-          if (key < seg_end && (!PAD || row < dim)) {
-            const uint32_t page = s_page[(key >> a.log_block) - page0];
-            if (page < a.blocks)
-              rv[j] = *reinterpret_cast<const u32x4*>(a.vc + ((uint64_t)page * a.heads + it.head) * page_len +
-                                                      ((row << a.log_block) + (key & in_page)));
-          }
+          const uint32_t x_w = 64 * wave + 256 * j, part = x_w >> log_part;
+          const uint32_t y_w = x_w & ((1u << log_part) - 1);  // the wave's first piece within the part
+          const uint8_t* from = values + (uint64_t)__builtin_amdgcn_readlane(pages_now, part << log_vp) * page_bytes;
+          const uint32_t at = 2 * (((y_w >> log_vp) << a.log_block) + inside) + v_lane;
+          rv[j] = !PAD || (y_w + lane) >> log_vp < dim ? *reinterpret_cast<const u32x4*>(from + at) : u32x4{};
         }
       };
       // Values of keys that do not exist become zero, and a drafted value that is
       // not finite is noted: a weight of zero times it is not zero.
+      bool odd = false;
       auto store = [&](uint32_t kb, uint32_t buf) {
-        const bool edge = kb + T::kKeys > sh.ctx;
+        const bool edge = kb + T::kKeys > sh.ctx || absent;
+        odd = false;
 #pragma unroll
         for (uint32_t j = 0; j < T::kEach; ++j) {
           const uint32_t x = t + 256 * j;
@@ -612,9 +733,10 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
 #pragma unroll
         for (uint32_t j = 0; j < T::kEach; ++j) {
           const uint32_t x = t + 256 * j, row = (x & ((DP << log_vp) - 1)) >> log_vp;
-          const uint32_t piece = value_piece(x), key = kb + 8 * piece;
+          const uint32_t piece = value_piece(x);
           if (edge) {
-            const uint32_t real = key < sh.keys ? min(sh.keys - key, 8u) : 0u;
+            const uint32_t key = kb + 8 * piece;
+            const uint32_t real = (absent >> piece) & 1 || key >= sh.keys ? 0u : min(sh.keys - key, 8u);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               uint32_t v = rv[j][w];
@@ -635,38 +757,49 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
       uint32_t buf = 0;
       for (uint32_t kb = seg; kb < seg_end; kb += T::kKeys, buf ^= 1) {
         const bool more = kb + T::kKeys < seg_end, odd_now = odd;
+        const uint32_t absent_now = absent;
         if (more) load(kb + T::kKeys);
         if (works) {
           const u32x4* bk = s_k + buf * T::kPieces;
           const u32x4* bv = s_v + buf * T::kPieces;
+          // Operands are read a step ahead of the products that take them (left to
+          // itself the compiler reads each right before its use, 32 waits a tile).
           floatx4 s[RT][NS];
+          u32x4 kf[2][KS];
+          auto read_keys = [&](int h) {
+            const uint32_t row = 32 * (h >> 1) + 8 * (l16 >> 2) + 4 * (h & 1) + (l16 & 3);
+#pragma unroll
+            for (int x = 0; x < KS; ++x) kf[h & 1][x] = bk[T::k_at(row, 4 * x + g)];
+          };
+          constexpr int kVf = 4, kVSteps = NS / 2 * DT / kVf;
+          u32x4 vf[2][kVf];
+          auto read_values = [&](int i) {
+#pragma unroll
+            for (int e = 0; e < kVf; ++e)
+              vf[i & 1][e] = bv[T::v_at(16 * ((i * kVf + e) % DT) + l16, 4 * (i * kVf / DT) + g)];
+          };
+          read_keys(0);
 #pragma unroll
           for (int h = 0; h < NS; ++h) {
-            const uint32_t row = 32 * (h >> 1) + 8 * (l16 >> 2) + 4 * (h & 1) + (l16 & 3);
+            if (h + 1 < NS) read_keys(h + 1);
+            else read_values(0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < RT; ++i) s[i][h] = floatx4{};
 #pragma unroll
-            for (int x = 0; x < KS; ++x) {
-              const u32x4 kf = bk[T::k_at(row, 4 * x + g)];
+            for (int x = 0; x < KS; ++x)
 #pragma unroll
-              for (int i = 0; i < RT; ++i) s[i][h] = E::mfma(kf, q[i][x], s[i][h]);
-            }
+              for (int i = 0; i < RT; ++i) s[i][h] = E::mfma(kf[h & 1][x], q[i][x], s[i][h]);
+            __builtin_amdgcn_sched_barrier(0);
           }
           // scores of unseen keys become -inf: past the cached keys, and on missing pages
-          bool missing[NS / 2];
-          bool edge = kb + T::kKeys > sh.ctx;
-#pragma unroll
-          for (int h = 0; h < NS / 2; ++h) {
-            const uint32_t kv = kb + 32 * h + 8 * g;
-            missing[h] = kv < seg_end && s_page[(kv >> a.log_block) - page0] >= a.blocks;
-            edge |= missing[h];
-          }
-          if (__any(edge)) {
+          if (kb + T::kKeys > sh.ctx || absent_now) {
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
               for (int h = 0; h < NS / 2; ++h) {
-                const uint32_t bits = missing[h] ? 0u : seen_bits(a, sh, tok[i], kb + 32 * h + 8 * g);
+                const bool held = !((absent_now >> (4 * h + g)) & 1);
+                const uint32_t bits = held ? seen_bits(a, sh, tok[i], kb + 32 * h + 8 * g) : 0u;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   if (!((bits >> e) & 1)) s[i][2 * h + (e >> 2)][e & 3] = -INFINITY;
@@ -675,21 +808,29 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const float keep = softmax_step<NS>(s[i], m[i], l[i], a.scale);
+            if (__any(keep != 1.f)) {  // a maximum moved: rare once some keys are seen
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[i][d] *= keep;
+              for (int d = 0; d < DT; ++d) o[i][d] *= keep;
+            }
           }
           if (!odd_now) {
+            u32x4 p[NS / 2][RT];
 #pragma unroll
-            for (int h = 0; h < NS / 2; ++h) {
-              u32x4 p[RT];
+            for (int h = 0; h < NS / 2; ++h)
 #pragma unroll
-              for (int i = 0; i < RT; ++i) p[i] = weights<E>(s[i][2 * h], s[i][2 * h + 1]);
+              for (int i = 0; i < RT; ++i) p[h][i] = weights<E>(s[i][2 * h], s[i][2 * h + 1]);
 #pragma unroll
-              for (int d = 0; d < DT; ++d) {
-                const u32x4 vf = bv[T::v_at(16 * d + l16, 4 * h + g)];
+            for (int v = 0; v < kVSteps; ++v) {
+              if (v + 1 < kVSteps) read_values(v + 1);
+              __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) o[i][d] = E::mfma(vf, p[i], o[i][d]);
-              }
+              for (int e = 0; e < kVf; ++e)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                  const int d = (v * kVf + e) % DT;
+                  o[i][d] = E::mfma(vf[v & 1][e], p[v * kVf / DT][i], o[i][d]);
+                }
+              __builtin_amdgcn_sched_barrier(0);
             }
           } else {
             // key by key, leaving out those of weight zero
@@ -725,15 +866,12 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
     }
 
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      l[i] += __shfl_xor(l[i], 16, 64);
-      l[i] += __shfl_xor(l[i], 32, 64);
-    }
+    for (int i = 0; i < RT; ++i) l[i] = row_sum(l[i]);
     bool write = it.whole;
     if (!it.whole) {
       // outputs lie in the order of the lanes that hold them
-      const Parts<ROWS, DP> parts(a, run, it, sh.chunks);
-      const uint32_t mine = parts.of(blockIdx.x), at0 = 4 * (wave * RT * DT * 64 + lane);
+      const Parts<ROWS, DP> parts(a, run, it, sh);
+      const uint32_t mine = parts.of(run.wg, it.first), at0 = 4 * (wave * RT * DT * 64 + lane);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         const uint32_t r = wave * 16 * RT + 16 * i + l16;
@@ -751,7 +889,15 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const uint32_t r = wave * 16 * RT + 16 * i + l16;
-          if (it.row0 + r < it.rows) l[i] = parts.join(r, at0 + i * DT * 256, 256, o[i], a.scale);
+          if (it.row0 + r < it.rows) {
+#pragma unroll
+            for (int d = 0; d < DT; d += 4) {
+              floatx4 four[4];
+              l[i] = parts.join(r, at0 + (i * DT + d) * 256, 256, four, a.scale);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][d + e] = four[e];
+            }
+          }
         }
       }
     }
@@ -786,8 +932,8 @@ AttnPlan plan_attention(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint
   const uint64_t rows = (uint64_t)tokens * (heads / kv_heads) / std::max(requests, 1u);
   p.rt = rows <= 16 ? 0 : rows <= 64 || p.dp == 256 ? 1 : 2;
   p.grid = kCUs * (p.rt == 0 ? 3 : 2);
-  p.part_off = ((size_t)p.grid * 4 + 255) / 256 * 256;
-  p.ws_bytes = p.part_off + (size_t)p.grid * 2 * (p.rt ? 64 * p.rt : 16) * (p.dp + 2) * 4;
+  p.part_off = ((size_t)p.grid * kRoom * 4 + 255) / 256 * 256;
+  p.ws_bytes = p.part_off + (size_t)p.grid * kRoom * (p.rt ? 64 * p.rt : 16) * (p.dp + 2) * 4;
   return p;
 }
 
@@ -865,9 +1011,13 @@ int dgt_tree_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t 
   if (!aligned(d_q, 16) || !aligned(d_k_cache, 16) || !aligned(d_v_cache, 16) || !aligned(d_out, 4) ||
       !aligned(d_ws, 256) || q_row % 8 || q_head % 8 || out_row % 2 || out_head % 2)
     return DGT_E_ARG;
-  if (blocks == 0) return DGT_E_SHAPE;
+  // (a page's bytes are counted in 32 bits)
+  if (blocks == 0 || (uint64_t)kv_heads * block * dim * 2 >= (1ull << 32)) return DGT_E_SHAPE;
   const AttnPlan p = plan_attention(tokens, heads, kv_heads, dim, requests);
   if (ws_bytes < p.ws_bytes) return DGT_E_BUFSIZE;
+  // units of all requests, if each had its table full
+  const uint64_t tile = p.rt ? 64 * p.rt : 16, tiles = (uint64_t)tokens * (heads / kv_heads) / tile + requests;
+  if (tiles * ((uint64_t)width * block / kUnitKeys + 1) * kv_heads >= (1ull << 31)) return DGT_E_SHAPE;
   AttnArgs a;
   a.q = static_cast<const uint16_t*>(d_q);
   a.kc = static_cast<const uint16_t*>(d_k_cache);

@@ -245,7 +245,7 @@ int dgt_dense_gemm(uint32_t fmt, uint32_t n, uint32_t k, uint32_t tile_n, const 
  *   values [blocks, kv_heads, dim, block]   (each page transposed)
  * A slot is page * block + place in the page (blocks * block < 2^31).  A block
  * table [requests, width] names each request's pages; token p of a request is
- * in page table[b, p / block].  At most 16384 requests a call.
+ * in page table[b, p / block].  At most 8192 requests a call.
  * Lengths, offsets, tables, slots and ids are device data that the host does
  * not see: the kernels hold every access inside the buffers whatever they hold
  * (lengths are cut to the table, offsets to the rows, a page or adapter id out

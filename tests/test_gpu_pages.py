@@ -123,7 +123,7 @@ def test_plan_of_nothing():
 
 
 def test_plan_of_the_most_requests():
-    _check_plan(_plan_case(11, 16384, 60, 3, 16))
+    _check_plan(_plan_case(11, 8192, 60, 3, 16))
 
 
 def test_plan_of_garbage_lengths_stays_inside():

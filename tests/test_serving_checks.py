@@ -118,7 +118,7 @@ def test_c_abi_refusals():
                                    words, p, p, p, mask, p, None)
     assert plan(ctx=None) == -1 and plan(head=None) == -1
     assert plan(block=24) == -2 and plan(block=4) == -2 and plan(block=2048) == -2
-    assert plan(blocks=1 << 28) == -2 and plan(requests=16385) == -2 and plan(tokens=(1 << 28) + 1) == -2
+    assert plan(blocks=1 << 28) == -2 and plan(requests=8193) == -2 and plan(tokens=(1 << 28) + 1) == -2
     assert plan(width=1 << 28) == -2
     assert plan(parents=p) == -1 and plan(words=1) == -1 and plan(parents=p, words=1) == -1
     store = lambda k=p, source=3, heads=2, dim=64, cache=1, kc=p, blocks=8, block=16: L.dgt_kv_store(
