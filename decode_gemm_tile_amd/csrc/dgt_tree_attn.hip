@@ -44,6 +44,7 @@ struct AttnArgs {
 constexpr uint32_t kWaves = 4, kTileKeys = 32, kUnitKeys = kWaves * kTileKeys;
 constexpr uint32_t kMinUnits = 2;  // a workgroup's run is not cut below this
 constexpr uint32_t kDies = 8;
+constexpr uint32_t kNarrowPerCU = 3, kWidePerCU = 2;  // workgroups, as registers and LDS allow
 
 struct Shape {  // of one request
   uint32_t first, count, ctx, keys, tiles, chunks;
@@ -425,10 +426,18 @@ constexpr uint32_t kPageRoom = 1024;
 // ----------------------------------------------------------- 16 rows and fewer
 // Each wave streams its own 32 keys of a unit from memory straight into the
 // operands; the waves meet once an item.
+template <int DP>
+struct Narrow {
+  static constexpr uint32_t kRows = 16, kLine = DP + 4;  // floats of a row in LDS
+  static constexpr uint32_t kBytes = kWaves * kRows * kLine * 4;
+};
+
 template <class E, int DP, bool PAD>
 __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(AttnArgs a) {
   constexpr int KS = DP / 32, DT = DP / 16, ROWS = 16;
-  __shared__ float s_o[ROWS][DP + 4];
+  constexpr uint32_t kLine = Narrow<DP>::kLine;
+  extern __shared__ u32x4 lds[];
+  float* s_o = reinterpret_cast<float*>(lds);  // [waves][rows][kLine]
   __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
   __shared__ uint32_t s_sum[6];
   __shared__ uint32_t s_last;
@@ -452,13 +461,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
     for (int d = 0; d < DT; ++d) o[d] = floatx4{};
 
     const int32_t* pages = a.table + (uint64_t)run.b * a.width;
+    // pages of the lane's group of 8 keys for masks and values, and for its key rows,
+    // asked for a unit ahead
+    auto page_of = [&](uint32_t key) { return key < sh.keys ? (uint32_t)pages[key >> a.log_block] : ~0u; };
+    const uint32_t kb0 = it.c0 * kUnitKeys + wave * kTileKeys;
+    uint32_t next_v = page_of(kb0 + 8 * g), next_k = page_of(kb0 + 8 * (l16 >> 2));
     for (uint32_t c = it.c0; c < it.c1; ++c) {
       const uint32_t kb = c * kUnitKeys + wave * kTileKeys;
       if (kb >= sh.keys) break;
-      // the lane's group of 8 keys for masks and values, and for its key rows
       const uint32_t kv = kb + 8 * g, kk = kb + 8 * (l16 >> 2);
-      uint32_t pv = kv < sh.keys ? (uint32_t)pages[kv >> a.log_block] : ~0u;
-      uint32_t pk = kk < sh.keys ? (uint32_t)pages[kk >> a.log_block] : ~0u;
+      uint32_t pv = next_v, pk = next_k;
+      next_v = page_of(kv + kUnitKeys);
+      next_k = page_of(kk + kUnitKeys);
       const bool held = pv < a.blocks;
       pv = held ? pv : 0u;
       pk = pk < a.blocks ? pk : 0u;
@@ -545,60 +559,48 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
       }
     }
 
-    // the four waves' parts, added in order
+    // the four waves' parts meet in LDS and are added in order
     l = row_sum(l);
     if (g == 0) {
       s_m[wave][l16] = m;
       s_l[wave][l16] = l;
     }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      *reinterpret_cast<floatx4*>(s_o + (wave * ROWS + l16) * kLine + 16 * d + 4 * g) = o[d];
     __syncthreads();
-    const float top = fmaxf(fmaxf(s_m[0][l16], s_m[1][l16]), fmaxf(s_m[2][l16], s_m[3][l16]));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float total = 0.f;
+    constexpr uint32_t kFours = DP / 4;  // of a row
+    const uint32_t live = min(it.rows - it.row0, (uint32_t)ROWS);
+    const Parts<ROWS, DP> parts(a, run, it, sh);
+    const uint32_t mine = it.whole ? 0u : parts.of(run.wg, it.first);
+    for (uint32_t i = t; i < live * kFours; i += 256) {
+      const uint32_t r = i / kFours, d = 4 * (i % kFours);
+      const float top = fmaxf(fmaxf(s_m[0][r], s_m[1][r]), fmaxf(s_m[2][r], s_m[3][r]));
+      const float ref = top == -INFINITY ? 0.f : top;
+      float total = 0.f;
+      floatx4 sum = {};
 #pragma unroll
-    for (uint32_t w = 0; w < kWaves; ++w)
-      total += s_l[w][l16] * __builtin_amdgcn_exp2f((s_m[w][l16] - ref) * a.scale);
-    const float f = __builtin_amdgcn_exp2f((m - ref) * a.scale);
-    for (uint32_t w = 0; w < kWaves; ++w) {
-      if (w == wave) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          floatx4* p = reinterpret_cast<floatx4*>(&s_o[l16][16 * d + 4 * g]);
-          if (w == 0) *p = o[d] * f;
-          else *p += o[d] * f;
+      for (uint32_t w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f((s_m[w][r] - ref) * a.scale);
+        total = fmaf(s_l[w][r], f, total);
+        sum += *reinterpret_cast<floatx4*>(s_o + (w * ROWS + r) * kLine + d) * f;
+      }
+      if (it.whole) {
+        if (!PAD || d < dim) write4<E>(out_at(a, sh, it, r) + d, sum, inverse(total));
+      } else {
+        part_store(parts.at, mine + 2 * ROWS + 4 * i, sum);
+        if (d == 0) {
+          part_store(parts.at, mine + r, top);
+          part_store(parts.at, mine + ROWS + r, total);
         }
       }
-      __syncthreads();
     }
-    if (wave == 0 && g == 0) {  // the joined statistics, for the threads that write
-      s_m[0][l16] = top;
-      s_l[0][l16] = total;
-    }
-    __syncthreads();
-    const uint32_t live = min(it.rows - it.row0, (uint32_t)ROWS);
-    constexpr uint32_t kFours = DP / 4;  // of a row
-    if (it.whole) {
+    if (!it.whole && parts.last(a, &s_last)) {
       for (uint32_t i = t; i < live * kFours; i += 256) {
         const uint32_t r = i / kFours, d = 4 * (i % kFours);
-        if (!PAD || d < dim)
-          write4<E>(out_at(a, sh, it, r) + d, *reinterpret_cast<floatx4*>(&s_o[r][d]), inverse(s_l[0][r]));
-      }
-    } else {
-      const Parts<ROWS, DP> parts(a, run, it, sh);
-      const uint32_t mine = parts.of(run.wg, it.first);
-      if (t < live) {
-        part_store(parts.at, mine + t, s_m[0][t]);
-        part_store(parts.at, mine + ROWS + t, s_l[0][t]);
-      }
-      for (uint32_t i = t; i < live * kFours; i += 256)
-        part_store(parts.at, mine + 2 * ROWS + 4 * i, *reinterpret_cast<floatx4*>(&s_o[i / kFours][4 * (i % kFours)]));
-      if (parts.last(a, &s_last)) {
-        for (uint32_t i = t; i < live * kFours; i += 256) {
-          const uint32_t r = i / kFours, d = 4 * (i % kFours);
-          floatx4 sum[1];
-          const float all = parts.join(r, 4 * i, 0, sum, a.scale);
-          if (!PAD || d < dim) write4<E>(out_at(a, sh, it, r) + d, sum[0], inverse(all));
-        }
+        floatx4 sum[1];
+        const float all = parts.join(r, 4 * i, 0, sum, a.scale);
+        if (!PAD || d < dim) write4<E>(out_at(a, sh, it, r) + d, sum[0], inverse(all));
       }
     }
     __syncthreads();  // the LDS is reused by the next item
@@ -931,8 +933,10 @@ AttnPlan plan_attention(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint
   // rows of a request and key head, on the average
   const uint64_t rows = (uint64_t)tokens * (heads / kv_heads) / std::max(requests, 1u);
   p.rt = rows <= 16 ? 0 : rows <= 64 || p.dp == 256 ? 1 : 2;
-  p.grid = kCUs * (p.rt == 0 ? 3 : 2);
-  p.part_off = ((size_t)p.grid * kRoom * 4 + 255) / 256 * 256;
+  p.grid = kCUs * (p.rt == 0 ? kNarrowPerCU : kWidePerCU);
+  // the counters' room is the same for every call, so that no call's parts lie where
+  // another's counters are
+  p.part_off = (kCUs * kNarrowPerCU * kRoom * 4 + 255) / 256 * 256;
   p.ws_bytes = p.part_off + (size_t)p.grid * kRoom * (p.rt ? 64 * p.rt : 16) * (p.dp + 2) * 4;
   return p;
 }
@@ -946,7 +950,12 @@ bool attn_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t 
 template <class E, int DP, int RT, bool PAD>
 int launch_attention(const AttnArgs& a, uint32_t grid, hipStream_t st) {
   if constexpr (RT == 0) {
-    hipLaunchKernelGGL((k_attention_narrow<E, DP, PAD>), dim3(grid), dim3(256), 0, st, a);
+    const auto kernel = k_attention_narrow<E, DP, PAD>;
+    constexpr uint32_t kLds = Narrow<DP>::kBytes;
+    if (kLds > 60 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds) != hipSuccess)
+      return DGT_E_HIP;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), kLds, st, a);
   } else {
     const auto kernel = k_attention_wide<E, DP, RT, PAD>;
     if (Tile<DP>::kBytes > 64 * 1024 &&

@@ -273,6 +273,21 @@ def test_long_contexts_repeat_bit_for_bit(ctx, new, heads, kv):
         assert torch.equal(_run(d, ws=ws), first)
 
 
+def test_one_workspace_for_every_kind_of_call():
+    """Calls with few and with many rows, each with as many parts as there can be, take turns
+    on one workspace: the parts of one never lie where another counts."""
+    import torch
+    few = _make(120, [50000], [1], 8, 8, 64, 64, extra=0)
+    many = _make(121, [9000, 6000], [40, 30], 8, 2, 64, 64, words=1, extra=0)
+    some = _make(122, [9000], [9], 8, 2, 128, 64, words=1, extra=0)
+    cases = (few, many, some)
+    own = [_run(d) for d in cases]  # each on a workspace of its own
+    ws = dgt.alloc_workspace(max(dgt.dgt_tree_attention_workspace(d["q"].shape, d["kc"].shape[1], len(d["ctx"]))
+                                 for d in cases))
+    for i in (0, 1, 0, 2, 0, 1, 2, 0):
+        assert torch.equal(_run(cases[i], ws=ws), own[i]), i
+
+
 def test_scale_is_taken():
     d = _make(101, [150], [4], 4, 2, 64, 16)
     for scale in (1e-3, 0.3):
