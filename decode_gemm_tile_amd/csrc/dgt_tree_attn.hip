@@ -227,8 +227,8 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f 
 // Where the parts of a tile of rows lie.  Each of its spans is held by the runs from
 // owner(span's first unit) to owner(its last); a run has room for three parts: one
 // of a span that began before it, and one of a span that begins in either half of it
-// (spans of a tile that is not whole are no shorter than half the longest run).  A part is m[ROWS], l[ROWS] and the
-// outputs, in floats.
+// (spans of a tile that is not whole are no shorter than half the longest run).  A part is ref[ROWS], l[ROWS] and
+// the outputs, in floats.
 constexpr uint32_t kRoom = 3;
 
 template <int ROWS, int DP>
@@ -299,7 +299,7 @@ struct Parts {
   // at0, at0 + step, ..., within a part.  Returns the sum of weights.  The parts come
   // from other dies' memory, microseconds away, so four are asked for at a time.
   template <int N>
-  __device__ __forceinline__ float join(uint32_t r, uint32_t at0, uint32_t step, floatx4 (&o)[N], float scale) const {
+  __device__ __forceinline__ float join(uint32_t r, uint32_t at0, uint32_t step, floatx4 (&o)[N]) const {
     constexpr int kBatch = 4;
     float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -326,7 +326,7 @@ struct Parts {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const float now = fmaxf(m, mw[k]), ref = now == -INFINITY ? 0.f : now;
-        const float f = __builtin_amdgcn_exp2f((m - ref) * scale), fw = __builtin_amdgcn_exp2f((mw[k] - ref) * scale);
+        const float f = __builtin_amdgcn_exp2f(m - ref), fw = __builtin_amdgcn_exp2f(mw[k] - ref);
         m = now;
         l = fmaf(lw[k], fw, l * f);
 #pragma unroll
@@ -378,24 +378,38 @@ __device__ __forceinline__ float row_sum(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// One step of the running softmax over the 4 N scores that a lane holds of its
-// row: s becomes the weights, m and l are updated; returns what the output so
-// far is multiplied by.  l counts this lane's keys only, the lanes of a row are
-// added at the end.
+// The running softmax of one row.  Weights are 2^(score * scale - ref) against a
+// reference that follows the maximum at a distance: it moves only when a score
+// passes it by kSlack, so that the outputs are rarely multiplied (fp32 sums and
+// 16-bit weights up to 2^kSlack lose nothing by it; following the maximum itself
+// multiplied them in a third of the tiles).  ref is -inf until a key is seen.
+constexpr float kSlack = 8.f;
+
+struct Softmax {
+  float ref = -INFINITY, l = 0.f;
+};
+
+// One step over the 4 N scores that a lane holds of its row: s becomes the weights;
+// true, for the whole wave, if the outputs so far are to be multiplied by `keep`.  l
+// counts this lane's keys only, the lanes of a row are added at the end.
 template <int N>
-__device__ __forceinline__ float softmax_step(floatx4 (&s)[N], float& m, float& l, float scale) {
+__device__ __forceinline__ bool softmax_step(floatx4 (&s)[N], Softmax& m, float& keep, float scale) {
   // (a maximum of three is one instruction; of two it is two more, to settle NaNs)
-  float top = m;
+  float top = s[0][0];
 #pragma unroll
   for (int h = 0; h < N; ++h) {
     top = fmaxf(fmaxf(top, s[h][0]), s[h][1]);
     top = fmaxf(fmaxf(top, s[h][2]), s[h][3]);
   }
-  const float now = row_max(top);
-  // a row that has seen nothing yet keeps -inf; its weights are exp2(-inf) = 0
-  const float ref = now == -INFINITY ? 0.f : now * scale;
-  const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(fmaf(m, scale, -ref));
-  m = now;
+  top = row_max(top) * scale;
+  const bool moves = __any(top > m.ref + kSlack);
+  if (moves) {
+    const float now = fmaxf(m.ref, top);
+    keep = m.ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m.ref - now);
+    m.ref = now;
+    m.l *= keep;
+  }
+  const float ref = m.ref == -INFINITY ? 0.f : m.ref;  // nothing seen: the weights are 2^-inf = 0
   float sum = 0.f;
 #pragma unroll
   for (int h = 0; h < N; ++h)
@@ -405,8 +419,8 @@ __device__ __forceinline__ float softmax_step(floatx4 (&s)[N], float& m, float& 
       s[h][e] = p;
       sum += p;
     }
-  l = fmaf(l, keep, sum);
-  return keep;
+  m.l += sum;
+  return moves;
 }
 
 // The weights are rounded to the cache's type, as the matrix instruction takes
@@ -456,7 +470,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
     uint32_t tok[1];
     load_queries<1, KS, PAD>(a, sh, it, it.row0, q, tok);
     floatx4 o[DT];
-    float m = -INFINITY, l = 0.f;
+    Softmax m;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = floatx4{};
 
@@ -522,8 +536,8 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
         odd_values = __any(odd_values);
       }
 
-      const float keep = softmax_step<2>(s, m, l, a.scale);
-      if (__any(keep != 1.f)) {  // a maximum moved: rare once some keys are seen
+      float keep;
+      if (softmax_step<2>(s, m, keep, a.scale)) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= keep;
       }
@@ -560,10 +574,10 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
     }
 
     // the four waves' parts meet in LDS and are added in order
-    l = row_sum(l);
+    m.l = row_sum(m.l);
     if (g == 0) {
-      s_m[wave][l16] = m;
-      s_l[wave][l16] = l;
+      s_m[wave][l16] = m.ref;
+      s_l[wave][l16] = m.l;
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -581,7 +595,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
       floatx4 sum = {};
 #pragma unroll
       for (uint32_t w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f((s_m[w][r] - ref) * a.scale);
+        const float f = __builtin_amdgcn_exp2f(s_m[w][r] - ref);
         total = fmaf(s_l[w][r], f, total);
         sum += *reinterpret_cast<floatx4*>(s_o + (w * ROWS + r) * kLine + d) * f;
       }
@@ -599,7 +613,7 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
       for (uint32_t i = t; i < live * kFours; i += 256) {
         const uint32_t r = i / kFours, d = 4 * (i % kFours);
         floatx4 sum[1];
-        const float all = parts.join(r, 4 * i, 0, sum, a.scale);
+        const float all = parts.join(r, 4 * i, 0, sum);
         if (!PAD || d < dim) write4<E>(out_at(a, sh, it, r) + d, sum[0], inverse(all));
       }
     }
@@ -666,14 +680,11 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
     uint32_t tok[RT];
     load_queries<RT, KS, PAD>(a, sh, it, row_w, q, tok);
     floatx4 o[RT][DT];
-    float m[RT], l[RT];
+    Softmax m[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[i][d] = floatx4{};
-    }
     const int32_t* pages = a.table + (uint64_t)run.b * a.width;
     const uint32_t k_end = min(it.c1 * kUnitKeys, sh.keys);
     const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.kc + it.head * page_len);
@@ -809,8 +820,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
           }
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
-            const float keep = softmax_step<NS>(s[i], m[i], l[i], a.scale);
-            if (__any(keep != 1.f)) {  // a maximum moved: rare once some keys are seen
+            float keep;
+            if (softmax_step<NS>(s[i], m[i], keep, a.scale)) {
 #pragma unroll
               for (int d = 0; d < DT; ++d) o[i][d] *= keep;
             }
@@ -868,7 +879,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
     }
 
 #pragma unroll
-    for (int i = 0; i < RT; ++i) l[i] = row_sum(l[i]);
+    for (int i = 0; i < RT; ++i) m[i].l = row_sum(m[i].l);
     bool write = it.whole;
     if (!it.whole) {
       // outputs lie in the order of the lanes that hold them
@@ -879,8 +890,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
         const uint32_t r = wave * 16 * RT + 16 * i + l16;
         if (it.row0 + r < it.rows) {
           if (g == 0) {
-            part_store(parts.at, mine + r, m[i]);
-            part_store(parts.at, mine + ROWS + r, l[i]);
+            part_store(parts.at, mine + r, m[i].ref);
+            part_store(parts.at, mine + ROWS + r, m[i].l);
           }
 #pragma unroll
           for (int d = 0; d < DT; ++d) part_store(parts.at, mine + 2 * ROWS + at0 + (i * DT + d) * 256, o[i][d]);
@@ -895,7 +906,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
 #pragma unroll
             for (int d = 0; d < DT; d += 4) {
               floatx4 four[4];
-              l[i] = parts.join(r, at0 + (i * DT + d) * 256, 256, four, a.scale);
+              m[i].l = parts.join(r, at0 + (i * DT + d) * 256, 256, four);
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[i][d + e] = four[e];
             }
@@ -908,7 +919,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
       for (int i = 0; i < RT; ++i) {
         const uint32_t r = wave * 16 * RT + 16 * i + l16;
         if (it.row0 + r < it.rows) {
-          const float inv = inverse(l[i]);
+          const float inv = inverse(m[i].l);
           uint16_t* p = out_at(a, sh, it, r);
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
