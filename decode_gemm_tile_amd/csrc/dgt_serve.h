@@ -29,6 +29,10 @@ struct Bf16 {
     x2 v = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(uint32_t, v);
   }
+  static __device__ __forceinline__ float add2(uint32_t v, float c) {  // c + both halves
+    typedef __bf16 x2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(x2, v), __builtin_bit_cast(x2, 0x3F803F80u), c, false);
+  }
   static __device__ __forceinline__ bool finite2(uint32_t v) {  // both halves finite
     return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u;
   }
@@ -47,6 +51,10 @@ struct F16 {
     typedef _Float16 x2 __attribute__((ext_vector_type(2)));
     x2 v = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, v);
+  }
+  static __device__ __forceinline__ float add2(uint32_t v, float c) {
+    typedef _Float16 x2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(x2, v), __builtin_bit_cast(x2, 0x3C003C00u), c, false);
   }
   static __device__ __forceinline__ bool finite2(uint32_t v) {
     return (v & 0x7C00u) != 0x7C00u && (v & 0x7C000000u) != 0x7C000000u;

@@ -390,8 +390,9 @@ struct Softmax {
 };
 
 // One step over the 4 N scores that a lane holds of its row: s becomes the weights;
-// true, for the whole wave, if the outputs so far are to be multiplied by `keep`.  l
-// counts this lane's keys only, the lanes of a row are added at the end.
+// true, for the whole wave, if the outputs so far are to be multiplied by `keep`.  The
+// weights are added to l where they are used (this lane's keys only; the lanes of a
+// row are added at the end).
 template <int N>
 __device__ __forceinline__ bool softmax_step(floatx4 (&s)[N], Softmax& m, float& keep, float scale) {
   // (a maximum of three is one instruction; of two it is two more, to settle NaNs)
@@ -410,24 +411,29 @@ __device__ __forceinline__ bool softmax_step(floatx4 (&s)[N], Softmax& m, float&
     m.l *= keep;
   }
   const float ref = m.ref == -INFINITY ? 0.f : m.ref;  // nothing seen: the weights are 2^-inf = 0
-  float sum = 0.f;
 #pragma unroll
   for (int h = 0; h < N; ++h)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[h][e], scale, -ref));
-      s[h][e] = p;
-      sum += p;
-    }
-  m.l += sum;
+    for (int e = 0; e < 4; ++e) s[h][e] = __builtin_amdgcn_exp2f(fmaf(s[h][e], scale, -ref));
   return moves;
 }
 
-// The weights are rounded to the cache's type, as the matrix instruction takes
-// them; the sum that divides them is of the unrounded ones.
+// The weights of 8 keys, rounded to the cache's type as the matrix instruction takes
+// them.  l, which divides the outputs, adds the rounded ones: where few keys hold most
+// of the weight their rounding cancels.
 template <class E>
-__device__ __forceinline__ u32x4 weights(const floatx4& s0, const floatx4& s1) {
-  return u32x4{E::pack2(s0[0], s0[1]), E::pack2(s0[2], s0[3]), E::pack2(s1[0], s1[1]), E::pack2(s1[2], s1[3])};
+__device__ __forceinline__ u32x4 weights(const floatx4& s0, const floatx4& s1, float& l) {
+  const u32x4 p = {E::pack2(s0[0], s0[1]), E::pack2(s0[2], s0[3]), E::pack2(s1[0], s1[1]), E::pack2(s1[2], s1[3])};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) l = E::add2(p[w], l);
+  return p;
+}
+
+// The weights as they are, where they are used key by key.
+template <int N>
+__device__ __forceinline__ void add_weights(const floatx4 (&s)[N], float& l) {
+#pragma unroll
+  for (int h = 0; h < N; ++h) l += (s[h][0] + s[h][1]) + (s[h][2] + s[h][3]);
 }
 
 // Keeps what is computed from v inside the loop it stands in: the rare paths'
@@ -542,13 +548,14 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
         for (int d = 0; d < DT; ++d) o[d] *= keep;
       }
       if (!odd_values) {
-        const u32x4 p = weights<E>(s[0], s[1]);
+        const u32x4 p = weights<E>(s[0], s[1], m.l);
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] = E::mfma(vf[d], p, o[d]);
       } else {
         // A drafted value is infinite or NaN: rows that do not see it must not
         // meet it, so keys of weight zero are left out one by one.
         const uint32_t real = min(sh.keys - kb, kTileKeys);
+        add_weights(s, m.l);
 #pragma unroll 1
         for (uint32_t x = 0; x < real; ++x) {
           const uint32_t key = kb + x, page = (uint32_t)pages[key >> a.log_block];
@@ -831,7 +838,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
 #pragma unroll
             for (int h = 0; h < NS / 2; ++h)
 #pragma unroll
-              for (int i = 0; i < RT; ++i) p[h][i] = weights<E>(s[i][2 * h], s[i][2 * h + 1]);
+              for (int i = 0; i < RT; ++i) p[h][i] = weights<E>(s[i][2 * h], s[i][2 * h + 1], m[i].l);
 #pragma unroll
             for (int v = 0; v < kVSteps; ++v) {
               if (v + 1 < kVSteps) read_values(v + 1);
@@ -848,6 +855,8 @@ __global__ __launch_bounds__(256, 2) void k_attention_wide(AttnArgs a) {
           } else {
             // key by key, leaving out those of weight zero
             const uint16_t* values = reinterpret_cast<const uint16_t*>(bv);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) add_weights(s[i], m[i].l);
 #pragma unroll 1
             for (uint32_t x = 0; x < T::kKeys; ++x) {
               uint32_t g_now = g;
