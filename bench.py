@@ -56,13 +56,14 @@ def parse_args():
 
 
 def source_hash() -> str:
-    """Hash of the sources compiled into device code and its launch planning
-    (every file under csrc/ but the host-only encoder): profile figures are
-    valid only for this code."""
+    """Hash of the sources compiled into the decode kernels and their launch
+    planning (every file under csrc/ but the host-only encoder and the serving
+    operators, which share no code with them): profile figures are valid only
+    for this code."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "decode_gemm_tile_amd", "csrc")
     for name in sorted(os.listdir(d)):
-        if name == "dgt_host.cpp":
+        if name in ("dgt_host.cpp", "dgt_serve.h", "dgt_pages.hip", "dgt_tree_attn.hip", "dgt_lora.hip"):
             continue
         with open(os.path.join(d, name), "rb") as fh:
             h.update(name.encode() + fh.read())
