@@ -42,7 +42,9 @@ struct AttnArgs {
 };
 
 constexpr uint32_t kWaves = 4, kTileKeys = 32, kUnitKeys = kWaves * kTileKeys;
-constexpr uint32_t kMinUnits = 2;  // a workgroup's run is not cut below this
+// A workgroup's run is not cut below this (one token over 1000 keys: 11.2 us with two,
+// 13.0 with four, 17.7 with six).
+constexpr uint32_t kMinUnits = 2;
 constexpr uint32_t kDies = 8;
 constexpr uint32_t kNarrowPerCU = 3, kWidePerCU = 2;  // workgroups, as registers and LDS allow
 
@@ -443,9 +445,13 @@ __device__ __forceinline__ void keep_here(uint32_t& v) { asm volatile("" : "+v"(
 // Pages of the keys at hand, kept in LDS: table entries of up to kPageRoom pages.
 constexpr uint32_t kPageRoom = 1024;
 
-// ----------------------------------------------------------- 16 rows and fewer
+// ------------------------------------------------------------------ few rows
 // Each wave streams its own 32 keys of a unit from memory straight into the
-// operands; the waves meet once an item.
+// operands; the waves meet once an item.  Bound by memory: 96 requests of up to 8100
+// keys, one token on 8 key heads of 128, take 232 us for 1.29 GB, 5.6 TB/s (a large
+// copy moves 5.1), three workgroups a CU keeping the loads in flight.  Small calls are
+// a chain of latencies: lengths, table, keys, the waves' meeting, and where a tile's
+// keys are split the parts (one token over 1000 keys: 11.2 us).
 template <int DP>
 struct Narrow {
   static constexpr uint32_t kRows = 16, kLine = DP + 4;  // floats of a row in LDS
@@ -453,7 +459,7 @@ struct Narrow {
 };
 
 template <class E, int DP, bool PAD>
-__global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(AttnArgs a) {
+__global__ __launch_bounds__(256, 3) void k_attention_narrow(AttnArgs a) {
   constexpr int KS = DP / 32, DT = DP / 16, ROWS = 16;
   constexpr uint32_t kLine = Narrow<DP>::kLine;
   extern __shared__ u32x4 lds[];
@@ -628,11 +634,18 @@ __global__ __launch_bounds__(256, DP == 256 ? 2 : 3) void k_attention_narrow(Att
   }
 }
 
-// -------------------------------------------------------------- more than 16 rows
+// ----------------------------------------------------------------- more rows
 // The waves take 16 RT rows each and share tiles of keys and values in LDS, two
 // buffers deep: the next tile is loaded into registers while this one is
 // multiplied.  16-byte pieces of a row are permuted by its number so that the
 // lanes of an operand read fall on different banks.
+//
+// 64 rows are bound by memory (64 requests of 8000 keys, 8 key heads of 128: 6.1 TB/s
+// with 16-token pages).  128 rows reach 650 TFLOP/s over keys in the caches (760 with
+// 64-token pages): beside 64 matrix instructions a tile and wave has 216 vector ones,
+// the exponentials among them, and the registers of two waves a SIMD leave no room to
+// run one tile's products into another's softmax (tiles of 32 keys, the next tile's
+// loads between the products, and wave priorities were measured and were no faster).
 template <int DP>
 struct Tile {
   static constexpr uint32_t kKeys = DP == 256 ? 32 : 64;
@@ -950,9 +963,15 @@ struct AttnPlan {
 AttnPlan plan_attention(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim, uint32_t requests) {
   AttnPlan p;
   p.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-  // rows of a request and key head, on the average
+  // By the rows of a request and key head, on the average.  32 requests of 4000 keys, 8
+  // key heads of 128, narrow against wide: 4 rows 102 and 95 us, 8 rows 104 and 95, 16
+  // rows 113 and 95, 32 rows 193 and 97; but 8 requests of 1000 keys at 4 rows 13 and 18,
+  // one of 4000 17 and 30: up to 8 rows the narrow kernel, whose workgroups need no
+  // common tile, loses little where it loses.  64-row tiles against 128: 64 rows 103 and
+  // 113 us, 80 rows 130 and 113.  Heads over 128 leave the narrow kernel too few
+  // registers (16 requests of 4000 keys, 8 rows of 256: 78 and 63 us).
   const uint64_t rows = (uint64_t)tokens * (heads / kv_heads) / std::max(requests, 1u);
-  p.rt = rows <= 16 ? 0 : rows <= 64 || p.dp == 256 ? 1 : 2;
+  p.rt = rows <= 8 && p.dp <= 128 ? 0 : rows <= 64 || p.dp == 256 ? 1 : 2;
   p.grid = kCUs * (p.rt == 0 ? kNarrowPerCU : kWidePerCU);
   // the counters' room is the same for every call, so that no call's parts lie where
   // another's counters are
@@ -970,12 +989,7 @@ bool attn_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t 
 template <class E, int DP, int RT, bool PAD>
 int launch_attention(const AttnArgs& a, uint32_t grid, hipStream_t st) {
   if constexpr (RT == 0) {
-    const auto kernel = k_attention_narrow<E, DP, PAD>;
-    constexpr uint32_t kLds = Narrow<DP>::kBytes;
-    if (kLds > 60 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds) != hipSuccess)
-      return DGT_E_HIP;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), kLds, st, a);
+    hipLaunchKernelGGL((k_attention_narrow<E, DP, PAD>), dim3(grid), dim3(256), Narrow<DP>::kBytes, st, a);
   } else {
     const auto kernel = k_attention_wide<E, DP, RT, PAD>;
     if (Tile<DP>::kBytes > 64 * 1024 &&
@@ -1001,7 +1015,6 @@ int launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     case 128 * 8 + 0: return launch_attention<E, 128, 0>(a, p.grid, st);
     case 128 * 8 + 1: return launch_attention<E, 128, 1>(a, p.grid, st);
     case 128 * 8 + 2: return launch_attention<E, 128, 2>(a, p.grid, st);
-    case 256 * 8 + 0: return launch_attention<E, 256, 0>(a, p.grid, st);
     case 256 * 8 + 1: return launch_attention<E, 256, 1>(a, p.grid, st);
   }
   return DGT_E_UNSUPPORTED;

@@ -105,6 +105,14 @@ SHAPES = [  # ctx, new, heads, kv_heads, dim, block
     ([2500], [2], 32, 2, 128, 1024),
     ([60] * 40, [2] * 40, 4, 1, 64, 16),
     ([9] * 300, [1] * 300, 2, 1, 64, 16),
+    # few rows on the average, many in one request; with a long context too
+    ([300] + [20] * 30, [40] + [1] * 30, 4, 2, 128, 16),
+    ([30000] + [5] * 30, [40] + [1] * 30, 2, 1, 64, 64),
+    # narrower heads than the kernels are made for, at every number of rows
+    ([77, 1200], [1, 2], 4, 2, 104, 16),
+    ([50, 300], [20, 3], 4, 2, 40, 16),
+    ([120], [40], 4, 1, 96, 16),
+    ([100, 7], [64, 50], 4, 2, 48, 32),
 ]
 
 
