@@ -48,8 +48,10 @@ __device__ __forceinline__ void store4(float* row, uint32_t n, uint32_t n1, bool
 // cache lookups would bound the kernel (a load of 1 KB took 120 cycles); so the
 // rows come in whole lines, a stage of K at a time, and turn in LDS.  Eight waves
 // share a stage's steps of 32 and are added in LDS at the end.  The next stage is
-// on its way in registers while this one is multiplied.  (32 tokens a workgroup were
-// slower: 18.6 against 14.4 us for 2050 tokens, K = 4096, rank 64.)
+// on its way in registers while this one is multiplied.  Bound by memory and its
+// latency: 64 rows of 56 adapters at K = 16384, rank 16, take 8.9 us for 33 MB.
+// (32 tokens a workgroup were slower: 18.6 against 14.4 us for 2050 tokens, K = 4096,
+// rank 64.)
 constexpr uint32_t kShrinkWaves = 8;
 
 template <int RT>
@@ -146,7 +148,8 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_lora_shrink(LoraArgs p) {
 //
 // Results turn in LDS, so that y and out are met in whole lines a row (in the
 // instruction's layout 16 lanes would ask for 16 rows).  MT = 2 takes 32 tokens,
-// MT = 1 up to 16.
+// MT = 1 up to 16.  2050 rows by 14336 columns at rank 64 take 51 us for 235 MB, 64
+// single rows by 53248 at rank 16 26 us for 122 MB: 4.6 TB/s, where a large copy moves 5.1.
 template <int MT>
 struct Expand {
   static constexpr uint32_t kRows = 16 * MT;
