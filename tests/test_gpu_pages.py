@@ -122,8 +122,10 @@ def test_plan_of_nothing():
         _check_plan(case)
 
 
-def test_plan_of_the_most_requests():
-    _check_plan(_plan_case(11, 8192, 60, 3, 16))
+@pytest.mark.parametrize("requests", [4096, 4800, 5200, 5461, 8192])
+def test_plan_of_many_requests(requests):
+    """Up to the most there may be; around 5000 the sums' LDS passes what a plain launch has."""
+    _check_plan(_plan_case(11, requests, 60, 3, 16))
 
 
 def test_plan_of_garbage_lengths_stays_inside():
