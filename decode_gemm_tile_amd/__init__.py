@@ -464,7 +464,8 @@ def dgt_page_plan(ctx_lens, new_lens, free_blocks, free_head, block_table, block
     """Offsets, slots, positions and tree masks of one step, and the pages it takes from
     the free list (written into block_table).  parents: int32[tokens] for drafted trees,
     with mask_words 64-bit words a token (default: one); None for chains.  out: a PagePlan
-    to write into.  out.counts[1:2] is the next step's free_head."""
+    to write into.  out.counts[1:2] is the next step's free_head, also where that step
+    writes into the same `out`."""
     import torch
     i32, words = torch.int32, mask_words
     if parents is not None and words == 0:

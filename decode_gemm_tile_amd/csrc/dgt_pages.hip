@@ -20,6 +20,7 @@ struct PlanArgs {
   int32_t *table, *cu, *slots, *positions, *counts;
   uint64_t* mask;
   uint32_t requests, free_len, width, log_block, blocks, tokens, words;
+  bool rows, sums;  // write what belongs to tokens and pages; write cu and counts
 };
 
 constexpr uint32_t kPlanThreads = 256;
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_page_plan(PlanArgs p) {
   auto fits = [&](uint32_t b, const Request& r) {
     return r.wide && s_cu[b + 1] <= p.tokens && (r.need == 0 || s_end[b] <= left);
   };
-  if (blockIdx.x == 0) {
+  if (p.sums && blockIdx.x == 0) {
     uint32_t refused = 0, taken = 0;
     for (uint32_t b = t; b < p.requests; b += kPlanThreads) {
       const Request r = request(b);
@@ -136,6 +137,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_page_plan(PlanArgs p) {
       p.counts[2] = (int32_t)s_out[0];
     }
   }
+  if (!p.rows) return;
 
   const uint32_t total = min(s_cu[p.requests], p.tokens), block = 1u << p.log_block;
   for (uint32_t tile = blockIdx.x * kPlanThreads; tile < p.tokens; tile += gridDim.x * kPlanThreads) {
@@ -377,9 +379,23 @@ int dgt_page_plan(const int32_t* d_ctx, const int32_t* d_new, uint32_t requests,
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
     return DGT_E_HIP;
   const uint32_t grid = std::min(std::max((tokens + kPlanThreads - 1) / kPlanThreads, 1u), 4 * kCUs);
-  hipLaunchKernelGGL(k_page_plan, dim3(grid), dim3(kPlanThreads), lds,
-                     static_cast<hipStream_t>(stream), p);
-  return launched();
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  auto run = [&](uint32_t workgroups, bool rows, bool sums) {
+    p.rows = rows;
+    p.sums = sums;
+    hipLaunchKernelGGL(k_page_plan, dim3(workgroups), dim3(kPlanThreads), lds, st, p);
+    return launched();
+  };
+  // Every workgroup reads the list's head.  Where it lies in the counts (a step that
+  // goes on from its own last result), the new one may be written only after the last
+  // of them has read the old one, which the order of two launches gives; a single
+  // workgroup has its barriers.
+  const uintptr_t head = reinterpret_cast<uintptr_t>(d_free_head), counts = reinterpret_cast<uintptr_t>(d_counts);
+  if (grid > 1 && head + 4 > counts && head < counts + 12) {
+    const int rc = run(grid, true, false);
+    return rc ? rc : run(1, false, true);
+  }
+  return run(grid, true, true);
 }
 
 int dgt_kv_store(const void* d_k, const void* d_v, uint32_t source, int64_t k_row, int64_t k_head,

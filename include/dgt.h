@@ -258,7 +258,10 @@ enum dgt_element {
   DGT_ELT_F32 = 3
 };
 
-/* Page plan of one step, in one launch.  All arrays are on the device.
+/* Page plan of one step, in one launch.  All arrays are on the device, and no
+ * output overlaps an input but for one case: *d_free_head may lie in d_counts, so
+ * that a step with fixed buffers goes on from its own last result (d_counts + 1);
+ * above 256 tokens that takes a second launch.
  *   d_ctx, d_new: int32[requests]; negative values count as 0.
  *   d_free: int32[free_len] page ids that may be taken, from *d_free_head on.
  *   d_table: int32[requests, width]; columns of pages taken now are written.

@@ -171,6 +171,70 @@ def test_plan_steps_chain_through_the_head():
     assert len(set(used.tolist())) == len(used) == head
 
 
+def _chained_steps(requests, most, steps, tree, run):
+    """Steps that read the list's head out of the counts that they write.  run(call) makes one
+    pass: call(out) is the plan, out the PagePlan that all steps share."""
+    import torch
+    rng = np.random.default_rng(requests)
+    block, tokens, words = 16, most * requests, -(-most // 64) if tree else 0
+    width, blocks = -(-most * steps // block), requests * (-(-most * steps // block) + 1)
+    free = rng.permutation(blocks)
+    d_ctx, d_new, d_free, d_table = _dev([0] * requests), _dev([0] * requests), _dev(free), _dev(np.full((requests, width), -1))
+    d_parents = _dev(np.zeros(tokens)) if tree else None
+    out = dgt.PagePlan.empty(requests, tokens, words)
+    out.counts.zero_()
+    table, ctx, head = np.full((requests, width), -1), np.zeros(requests, np.int64), 0
+
+    def call():
+        dgt.dgt_page_plan(d_ctx, d_new, d_free, out.counts[1:2], d_table, block, blocks, tokens, parents=d_parents,
+                          mask_words=words, out=out)
+        d_ctx.add_(d_new)
+
+    step = run(call)
+    d_ctx.zero_(), out.counts.zero_(), d_table.fill_(-1)
+    for _ in range(steps):
+        new = rng.integers(0, most + 1, requests)
+        parents = None
+        if tree:
+            parents = np.concatenate([[rng.integers(-1, i) for i in range(n)] for n in new] + [np.zeros(tokens)])[:tokens]
+            d_parents.copy_(_dev(parents))
+            parents = parents.astype(np.int64)
+        d_new.copy_(_dev(new))
+        step()
+        torch.cuda.synchronize()
+        table, cu, slots, pos, mask, counts = serving.page_plan(ctx, new, free, head, table, block, blocks, tokens,
+                                                                parents, words)
+        for got, ref in ((d_table, table), (out.cu, cu), (out.slots, slots), (out.positions, pos), (out.counts, counts)):
+            assert np.array_equal(got.cpu().numpy(), ref)
+        if tree:
+            assert np.array_equal(out.mask.cpu().numpy().view(np.uint64), mask)
+        ctx, head = ctx + new, int(counts[1])
+    used = table[table >= 0]
+    assert len(set(used.tolist())) == len(used) == head > 0
+
+
+@pytest.mark.parametrize("requests,most,tree", [(5, 40, False), (8, 32, False), (9, 32, True), (900, 50, False), (500, 70, True)])
+def test_plan_steps_chain_in_fixed_buffers(requests, most, tree):
+    """The head is read where the step writes the next one: with one workgroup (up to 256 rows)
+    and with up to 176."""
+    _chained_steps(requests, most, 5, tree, lambda call: call)
+
+
+def test_plan_steps_chain_in_a_graph():
+    """A captured step in fixed buffers, replayed: each replay goes on where the last one stopped."""
+    import torch
+
+    def capture(call):
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        return graph.replay
+
+    _chained_steps(300, 50, 5, True, capture)
+
+
 def test_plan_on_another_stream():
     import torch
     s = torch.cuda.Stream()
