@@ -64,7 +64,13 @@ __device__ __forceinline__ Shape request_shape(const AttnArgs& a, uint32_t b) {
   return s;
 }
 
-// (The host has made sure that the batch's units stay below 2^31.)
+// The host has made sure that a batch whose offsets never fall has fewer units than
+// this, and any one request too.  Offsets that fall can name the same rows again and
+// again; sums stop growing here (min(a + b, most) is associative over numbers up to
+// it), and a batch that reaches it is not computed.
+constexpr uint32_t kMostUnits = 0x7FFFFFFF;
+__device__ __forceinline__ uint32_t add_units(uint32_t a, uint32_t b) { return min(a + b, kMostUnits); }
+
 template <int ROWS>
 __device__ __forceinline__ uint32_t request_units(const AttnArgs& a, uint32_t b) {
   const Shape s = request_shape<ROWS>(a, b);
@@ -135,26 +141,26 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, uint32_t* s_sum) {
   const uint32_t per = (a.requests + 255) / 256;
   const uint32_t b_lo = min(t * per, a.requests), b_hi = min(b_lo + per, a.requests);
   uint32_t mine = 0;
-  for (uint32_t b = b_lo; b < b_hi; ++b) mine += request_units<ROWS>(a, b);
+  for (uint32_t b = b_lo; b < b_hi; ++b) mine = add_units(mine, request_units<ROWS>(a, b));
   uint32_t scan = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const uint32_t o = __shfl_up(scan, d, 64);
-    if (lane >= (uint32_t)d) scan += o;
+    if (lane >= (uint32_t)d) scan = add_units(scan, o);
   }
   if (lane == 63) s_sum[wave] = scan;
   __syncthreads();
   uint32_t units = 0;
   for (uint32_t w = 0; w < 4; ++w) {
-    if (w < wave) scan += s_sum[w];
-    units += s_sum[w];
+    if (w < wave) scan = add_units(scan, s_sum[w]);
+    units = add_units(units, s_sum[w]);
   }
   units = __builtin_amdgcn_readfirstlane(units);
   Run run{Deal(units, min(gridDim.x, max((units + kMinUnits - 1) / kMinUnits, 1u))), 0, 0, 0, 0, 0};
   // Workgroups go round the dies; neighbouring runs, which read the same keys for
   // other rows, stay on one, so that its cache serves all but the first.
   const uint32_t runs = run.deal.count, die = blockIdx.x % kDies, nth = blockIdx.x / kDies;
-  if (units == 0 || nth >= runs / kDies + (die < runs % kDies)) return run;
+  if (units == 0 || units == kMostUnits || nth >= runs / kDies + (die < runs % kDies)) return run;
   run.wg = die * (runs / kDies) + min(die, runs % kDies) + nth;
   run.u = run.deal.begin(run.wg);
   run.end = run.deal.begin(run.wg + 1);
@@ -1059,7 +1065,7 @@ int dgt_tree_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t 
   if (ws_bytes < p.ws_bytes) return DGT_E_BUFSIZE;
   // units of all requests, if each had its table full
   const uint64_t tile = p.rt ? 64 * p.rt : 16, tiles = (uint64_t)tokens * (heads / kv_heads) / tile + requests;
-  if (tiles * ((uint64_t)width * block / kUnitKeys + 1) * kv_heads >= (1ull << 31)) return DGT_E_SHAPE;
+  if (tiles * ((uint64_t)width * block / kUnitKeys + 1) * kv_heads >= kMostUnits) return DGT_E_SHAPE;
   AttnArgs a;
   a.q = static_cast<const uint16_t*>(d_q);
   a.kc = static_cast<const uint16_t*>(d_k_cache);

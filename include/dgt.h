@@ -249,7 +249,7 @@ int dgt_dense_gemm(uint32_t fmt, uint32_t n, uint32_t k, uint32_t tile_n, const 
  * Lengths, offsets, tables, slots and ids are device data that the host does
  * not see: the kernels hold every access inside the buffers whatever they hold
  * (lengths are cut to the table, offsets to the rows, a page or adapter id out
- * of range counts as absent). */
+ * of range counts as absent; offsets that fall leave the rows undefined). */
 
 /* Element types of cache and activations. */
 enum dgt_element {

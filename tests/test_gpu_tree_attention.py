@@ -317,6 +317,28 @@ def test_garbage_offsets_and_lengths_stay_inside():
     _check(d, _run(d, ws=ws))
 
 
+def test_offsets_that_name_rows_again_and_again():
+    """Offsets that go up and down over 1024 requests with full tables: 8.6e9 units of work, more
+    than 32 bits hold.  Nothing is written; a sound call on the same workspace after it is right."""
+    import torch
+    requests, tokens, heads, kv, dim, block, width = 1024, 65536, 32, 8, 8, 1024, 128
+    # units: 512 requests of 65536 * 4 rows in tiles of 128, tables of 1024 times 128 keys, 8 heads
+    assert 512 * (tokens * 4 // 128) * (width * block // 128) * kv >= 2 ** 33
+    q = torch.zeros((tokens, heads, dim), dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros((2, kv, block, dim), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros((2, kv, dim, block), dtype=torch.bfloat16, device="cuda")
+    table, ctx = _i32(np.zeros((requests, width))), _i32([2 ** 31 - 1] * requests)
+    cu = np.zeros(requests + 1)
+    cu[1::2] = tokens
+    ws = dgt.alloc_workspace(dgt.dgt_tree_attention_workspace(q.shape, kv, requests))
+    out = torch.full_like(q, 3.0)
+    dgt.dgt_tree_attention(q, kc, vc, table, ctx, _i32(cu), out=out, ws=ws)
+    torch.cuda.synchronize()
+    assert (out == 3).all()
+    d = _make(123, [700, 40], [40, 30], 8, 2, 64, 16, words=1)
+    _check(d, _run(d, ws=ws))
+
+
 def test_pool_past_32_bit_offsets():
     """Pages at both ends of a pool of more than 2^32 elements."""
     import torch
