@@ -145,6 +145,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_lora_shrink(LoraArgs p) {
 // products take the place of one.  They are hidden: the kernel is bound by y and
 // out, 8 bytes an element against 6 rank operations.  B's rows (columns of out) are
 // the first operand, read from memory in its layout, tokens the second, from LDS.
+// Parts are cut off, not rounded: they have low's sign, and none passes the largest
+// bf16 value.  A part may be zero where low is not, and zero times an infinity of B is
+// NaN; so sums that are NaN are formed again from whole products (looking for them
+// takes 26.3 to 27.0 us for 64 single rows, 48.6 to 49.1 for 2050).
 //
 // Results turn in LDS, so that y and out are met in whole lines a row (in the
 // instruction's layout 16 lanes would ask for 16 rows).  MT = 2 takes 32 tokens,
@@ -161,6 +165,18 @@ struct Expand {
   static __host__ __device__ uint32_t low_row(uint32_t rank) { return (rank + 31) / 32 * 32 + 8; }
   static uint32_t bytes(uint32_t rank) { return 3 * kRows * low_row(rank) * 2 + kRows * kTurn * 4; }
 };
+
+// One element of low B^T, product by product: `low` at the token's row of the parts,
+// `part` elements apart, `b` the column's row of B.
+__device__ __forceinline__ float whole_products(const uint16_t* low, uint32_t part, const uint16_t* b, uint32_t rank) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (uint32_t r = 0; r < rank && !isnan(sum); ++r) {
+    const float v = Bf16::up(low[r]) + (Bf16::up(low[part + r]) + Bf16::up(low[2 * part + r]));
+    sum = fmaf(v, Bf16::up(b[r]), sum);
+  }
+  return sum;
+}
 
 template <int MT>
 __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs p) {
@@ -211,17 +227,21 @@ __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs p) {
     u32x4 out[3];
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      // v = hi + mid + lo; an infinity or NaN stays in hi alone
+      // v = hi + mid + lo, 8 bits each; an infinity stays in hi alone, and a NaN whose
+      // upper bits are an infinity's is one in the next part
       float rest[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) rest[e] = v[j + e] * scale;
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
-        const uint32_t two = Bf16::pack2(rest[0], rest[1]);
-        const float lo = Bf16::up(two & 0xFFFFu), hi = Bf16::up(two >> 16);
-        out[x][j / 2] = two;
-        rest[0] = fabsf(lo) < INFINITY ? rest[0] - lo : 0.f;
-        rest[1] = fabsf(hi) < INFINITY ? rest[1] - hi : 0.f;
+        uint32_t top[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[e] = __float_as_uint(rest[e]) & 0xFFFF0000u;
+          const float part = __uint_as_float(top[e]);
+          rest[e] = rest[e] == part ? 0.f : rest[e] - part;
+        }
+        out[x][j / 2] = top[0] >> 16 | top[1];
       }
     }
 #pragma unroll
@@ -265,6 +285,23 @@ __global__ __launch_bounds__(256, 4) void k_lora_expand(LoraArgs p) {
         for (int c = 0; c < NT; ++c)
           *reinterpret_cast<floatx4*>(turn + (16 * i + l16) * X::kTurn + wave * 16 * NT + 16 * c + 4 * g) = acc[c][i];
       }
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+        odd |= __builtin_isunordered(acc[c][i][0], acc[c][i][1]) || __builtin_isunordered(acc[c][i][2], acc[c][i][3]);
+    if (odd) {
+#pragma unroll 1
+      for (uint32_t e = 0; e < 4 * NT * MT; ++e) {  // this lane's own sums
+        uint32_t tok = 16 * (e / (4 * NT)) + l16;
+        const uint32_t col = wave * 16 * NT + 16 * (e / 4 % NT) + 4 * g + e % 4;
+        keep_here(tok);
+        float* sum = turn + tok * X::kTurn + col;
+        if (tok < live && nb + col < n1 && isnan(*sum))
+          *sum = whole_products(low + tok * row, part, mat + (uint64_t)(nb + col) * p.rank, p.rank);
+      }
+    }
     __syncthreads();
 #pragma unroll
     for (uint32_t j = 0; j < X::kIter; ++j) {

@@ -99,6 +99,10 @@ __device__ __forceinline__ uint32_t chunk_request(const int32_t* cu, uint32_t co
   return lo;
 }
 
+// Keeps what is computed from v inside the loop it stands in: the rare paths'
+// addresses would otherwise be formed ahead of all loops and hold registers there.
+__device__ __forceinline__ void keep_here(uint32_t& v) { asm volatile("" : "+v"(v)); }
+
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool power_of_two(uint32_t v) { return v && !(v & (v - 1)); }
 inline int launched() { return hipGetLastError() == hipSuccess ? DGT_OK : DGT_E_HIP; }

@@ -444,10 +444,6 @@ __device__ __forceinline__ void add_weights(const floatx4 (&s)[N], float& l) {
   for (int h = 0; h < N; ++h) l += (s[h][0] + s[h][1]) + (s[h][2] + s[h][3]);
 }
 
-// Keeps what is computed from v inside the loop it stands in: the rare paths'
-// addresses would otherwise be formed ahead of all loops and hold registers there.
-__device__ __forceinline__ void keep_here(uint32_t& v) { asm volatile("" : "+v"(v)); }
-
 // Pages of the keys at hand, kept in LDS: table entries of up to kPageRoom pages.
 constexpr uint32_t kPageRoom = 1024;
 

@@ -158,6 +158,54 @@ def test_lora_nan_stays_in_its_rows():
     assert np.allclose(out[keep].numpy(), ref[keep], atol=1e-4)
 
 
+def _check_non_finite(d, got):
+    """Infinities and NaN where the definition has them, all else within the tolerance."""
+    with np.errstate(invalid="ignore"):
+        ref, size = _oracle(d)
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(np.isposinf(got), np.isposinf(ref)) and np.array_equal(np.isneginf(got), np.isneginf(ref))
+    k, rank = d["x"].shape[1], d["a"].shape[1]
+    ok = np.isfinite(ref)
+    tol = (k + rank + 40) * 2.0 ** -24 * size[ok] + 2.0 ** -24 * np.abs(ref[ok])
+    assert (np.abs(got[ok] - ref[ok]) <= tol).all()
+
+
+@pytest.mark.parametrize("integers", [False, True], ids=["reals", "integers"])
+@pytest.mark.parametrize("new,rank", [([1, 5, 3], 16), ([40, 33], 72)])
+def test_lora_infinite_weights(new, rank, integers):
+    """An infinity of B makes its column infinite with the sign of the shrunk value, whichever
+    bits that has (integers leave the lower parts zero); two of different signs, or one times
+    zero, make NaN; the other columns are as ever."""
+    d = _make(12, new, 150, 256, rank, 2, ids=[0, 1, 0][:len(new)], integers=integers)
+    inf = float("inf")
+    d["b"][0, 3, 2], d["b"][0, 77, 5], d["b"][1, 149, rank - 1], d["b"][1, 0, 0] = inf, -inf, inf, inf
+    d["b"][0, 100, 1], d["b"][0, 100, 9] = inf, -inf
+    d["b"][1, 50, 4] = float("nan")
+    y, *rest = _dev(d)
+    out = dgt.dgt_lora_add(y, *rest)
+    _check_non_finite(d, out)
+    assert out.isinf().any() and out.isnan().any()
+
+
+def test_lora_values_beside_the_largest():
+    """A shrunk value that no bf16 value is near from above: its products with small weights
+    are finite, with zeros zero."""
+    import torch
+    d = _make(13, [1, 2], 40, 64, 8, 1, ids=[0, 0])
+    d["x"].zero_(), d["a"].zero_()
+    d["x"][:, :2] = torch.tensor([[1.0, 1.0], [1.0, 0.0], [-1.0, -1.0]])
+    d["a"][0, 4, :2] = torch.tensor([3.375, 0.0234375])
+    d["scaling"][:] = 1e38
+    d["b"] = (d["b"].float() * 2.0 ** -100).to(torch.bfloat16)
+    d["b"][0, ::3] = 0
+    # (1e38 is not exact in fp32: the oracle takes the value that the operator gets)
+    y, *rest = _dev(d)
+    out = dgt.dgt_lora_add(y, *rest)
+    assert torch.isfinite(out).all()
+    _check_non_finite(d, out)
+
+
 def test_lora_garbage_offsets_stay_inside():
     """Offsets out of order or past the rows touch nothing outside; a sound call after it is right."""
     import torch
