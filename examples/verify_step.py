@@ -4,15 +4,16 @@ Two attention layers whose projections stay compressed serve a batch of requests
 with an adapter of its own (or none):
 
   1. a prompt step: pages for every request's prompt, keys and values into them;
-  2. a verify step: every request brings a tree of drafted tokens; one pass through the
-     layers gives each node its output, seeing the prompt and its own ancestors only;
-  3. the nodes on one path of each tree are kept: their keys and values move to the
-     places behind the prompt.
+  2. verify steps: every request brings a tree of drafted tokens; one pass through the
+     layers gives each node its output, seeing what was kept and its own ancestors only;
+  3. after each, the nodes on one path of each tree are kept: their keys and values move
+     to the places behind the cached tokens, and the pages that only the other nodes
+     needed go back to the free list.
 
 A fused projection costs almost the same for one row as for 64 (each weight is decoded
 once for all rows), which is why drafted tokens are worth verifying in trees.
 
-``python examples/verify_step.py`` runs it on cuda:0 and checks the outputs of both steps
+``python examples/verify_step.py`` runs it on cuda:0 and checks the outputs of all steps
 against a plain computation in float64 on the decompressed weights.
 """
 
@@ -95,13 +96,21 @@ class Server:
 
     def keep(self, p, path_rows, path_lens):
         """Keep the rows `path_rows` of the last step (path_lens of each request, in order):
-        their keys and values move to the places right behind the cached tokens."""
+        their keys and values move to the places right behind the cached tokens.  Pages past
+        the kept tokens go back to the free list, in front of its head: the next plan counts a
+        request's pages by its length and takes fresh ones from there on."""
         # the destinations are the slots of the first rows of each request
         at = torch.cat([p.cu[r] + torch.arange(n, device="cuda") for r, n in enumerate(path_lens.tolist())])
         src, dst = p.slots[path_rows].long(), p.slots[at]
         for k, v in zip(self.k, self.v):
             dgt.dgt_kv_store(k[src // BLOCK, :, src % BLOCK], v[src // BLOCK, :, :, src % BLOCK], dst, k, v)
         self.lens += path_lens
+        pages = (self.lens + BLOCK - 1) // BLOCK
+        surplus = (torch.arange(WIDTH, device="cuda") >= pages[:, None]) & (self.table >= 0)
+        ids = self.table[surplus]
+        self.head = self.head - len(ids)
+        self.free[self.head + torch.arange(len(ids), device="cuda")] = ids
+        self.table[surplus] = -1
 
 
 def plain_step(server, x, history, new, parents):
@@ -129,7 +138,7 @@ def plain_step(server, x, history, new, parents):
     return x, made
 
 
-def main(requests=6, seed=0):
+def main(requests=6, seed=0, steps=3):
     gen = torch.Generator().manual_seed(seed + 1)
     rng = np.random.default_rng(seed)
     s = Server(requests, seed)
@@ -138,52 +147,73 @@ def main(requests=6, seed=0):
     def rows(count):
         return torch.randn((count, HIDDEN), generator=gen).to(torch.bfloat16).cuda()
 
+    worst, drafted, kept = 0.0, 0, 0
+
+    def check(got, want):
+        nonlocal worst
+        worst = max(worst, float((got.double() - want.double()).norm() / want.double().norm()))
+
+    def check_pages():
+        # every page is either in one request's table or still free
+        held = s.table[s.table >= 0]
+        free = s.free[int(s.head):]
+        assert torch.equal(torch.cat([held, free]).sort().values, torch.arange(BLOCKS, dtype=torch.int32, device="cuda"))
+        assert torch.equal((s.table >= 0).sum(1), (s.lens.long() + BLOCK - 1) // BLOCK)
+
     prompt = rng.integers(3, 60, requests)
-    x1 = rows(int(prompt.sum()))
-    y1, p1 = s.step(x1, dev(prompt))
+    x = rows(int(prompt.sum()))
+    y, p = s.step(x, dev(prompt))
+    assert int(p.counts[2]) == 0
     s.lens += dev(prompt)
-
-    nodes = rng.integers(1, 20, requests)
-    parents = [[-1] + [int(rng.integers(-1, i)) for i in range(1, n)] for n in nodes]
-    x2 = rows(int(nodes.sum()))
-    y2, p2 = s.step(x2, dev(nodes), parents=dev(sum(parents, [])))
-
-    # each tree keeps the way to its last node
-    paths = []
-    for r, up in enumerate(parents):
-        way, j = [], len(up) - 1
-        while j >= 0:
-            way.append(j)
-            j = up[j]
-        paths.append(way[::-1])
-    cu = np.concatenate([[0], np.cumsum(nodes)])
-    s.keep(p2, torch.tensor([cu[r] + j for r, w in enumerate(paths) for j in w], device="cuda"),
-           dev([len(w) for w in paths]))
-
-    # the check, request by request
-    worst = 0.0
-    start1 = np.concatenate([[0], np.cumsum(prompt)])
+    check_pages()
+    cu = np.concatenate([[0], np.cumsum(prompt)])
+    history = []  # of each request, per layer: keys and values of its cached tokens
     for r in range(requests):
-        one = {"adapter": s.adapters[r:r + 1], "cu": [0, int(prompt[r])]}
         empty = [(torch.zeros((0, KV_HEADS, DIM), dtype=torch.float64, device="cuda"),) * 2] * LAYERS
         chain = list(range(-1, int(prompt[r]) - 1))
-        ref1, made = plain_step(s, x1[start1[r]:start1[r + 1]], empty, one, chain)
-        one["cu"] = [0, int(nodes[r])]
-        ref2, made2 = plain_step(s, x2[cu[r]:cu[r + 1]], made, one, parents[r])
-        for got, ref in ((y1[start1[r]:start1[r + 1]], ref1), (y2[cu[r]:cu[r + 1]], ref2)):
-            worst = max(worst, float((got.double() - ref.double()).norm() / ref.double().norm()))
-        # what was kept lies behind the prompt, in order
-        for i in range(LAYERS):
-            pos = torch.arange(int(prompt[r]), int(prompt[r]) + len(paths[r]), device="cuda")
+        one = {"adapter": s.adapters[r:r + 1], "cu": [0, int(prompt[r])]}
+        want, made = plain_step(s, x[cu[r]:cu[r + 1]], empty, one, chain)
+        check(y[cu[r]:cu[r + 1]], want)
+        history.append(made)
+
+    for _ in range(steps):
+        nodes = rng.integers(1, 20, requests)
+        parents = [[-1] + [int(rng.integers(-1, i)) for i in range(1, n)] for n in nodes]
+        before = s.lens.tolist()
+        x = rows(int(nodes.sum()))
+        y, p = s.step(x, dev(nodes), parents=dev(sum(parents, [])))
+        assert int(p.counts[2]) == 0
+
+        # each tree keeps the way to its last node
+        paths = []
+        for up in parents:
+            way, j = [], len(up) - 1
+            while j >= 0:
+                way.append(j)
+                j = up[j]
+            paths.append(way[::-1])
+        cu = np.concatenate([[0], np.cumsum(nodes)])
+        s.keep(p, torch.tensor([cu[r] + j for r, w in enumerate(paths) for j in w], device="cuda"),
+               dev([len(w) for w in paths]))
+        check_pages()
+        drafted, kept = drafted + len(x), kept + sum(map(len, paths))
+
+        for r in range(requests):
+            one = {"adapter": s.adapters[r:r + 1], "cu": [0, int(nodes[r])]}
+            want, made = plain_step(s, x[cu[r]:cu[r + 1]], history[r], one, parents[r])
+            check(y[cu[r]:cu[r + 1]], want)
+            # what was kept lies behind the cached tokens, in order
+            places = list(range(before[r])) + [before[r] + j for j in paths[r]]
+            history[r] = [(k[places], v[places]) for k, v in made]
+            pos = torch.arange(before[r], before[r] + len(paths[r]), device="cuda")
             page = s.table[r, pos // BLOCK].long()
-            kept = s.k[i][page, :, pos % BLOCK].double()
-            want = made2[i][0][[int(prompt[r]) + j for j in paths[r]]]
-            worst = max(worst, float((kept - want).norm() / want.norm()))
-    print("verify step: %d requests, %d prompt rows, %d drafted rows, %d kept; largest relative difference %.1e"
-          % (requests, len(x1), len(x2), sum(map(len, paths)), worst))
+            for i in range(LAYERS):
+                check(s.k[i][page, :, pos % BLOCK], history[r][i][0][before[r]:])
+                check(s.v[i][page, :, :, pos % BLOCK], history[r][i][1][before[r]:])
+    print("verify steps: %d requests, %d prompt rows, %d drafted rows in %d steps, %d kept; "
+          "largest relative difference %.1e" % (requests, prompt.sum(), drafted, steps, kept, worst))
     # bf16 roundings that fall the other way between the operators: a few of 2^-8 each
     assert worst < 2e-2, worst
-    assert int(p2.counts[2]) == 0 and int(p1.counts[2]) == 0
     return worst
 
 

@@ -281,6 +281,10 @@ enum dgt_element {
  *          ancestors.  mask_words <= 1024.
  *   d_counts: int32[3]: rows needed (tokens + 1 if more than `tokens`), the
  *          free list's new head, requests refused.
+ * A request's pages are counted by its length, ceil(ctx / block).  Where drafted
+ * tokens are dropped again, pages past the kept ones go back to the free list before
+ * the next plan, in front of its head: those ids into d_free[head - count ..
+ * head - 1], and head - count as the head.
  * A token whose index does not fit the mask, or whose way to the root meets a
  * parent that is not below its child, gets slot -1, position -1 and no bits.
  * Errors: E_ARG, E_SHAPE, E_HIP. */
