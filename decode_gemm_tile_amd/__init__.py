@@ -31,6 +31,8 @@ EXPORTS = ["dgt_version", "dgt_status_string", "dgt_compress_bound", "dgt_compre
            "dgt_lora_workspace", "dgt_lora_add"]
 # element types of the serving operators
 DGT_ELT_BF16, DGT_ELT_F16, DGT_ELT_F32 = 1, 2, 3
+# bytes at the start of dgt_tree_attention's workspace that are zero before its first use
+DGT_TREE_ATTENTION_ZEROED = 9216
 
 
 class DgtError(RuntimeError):
@@ -603,12 +605,22 @@ def _check_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask, 
     _check_gpu(dev)
 
 
+def _attention_workspace(nbytes, device):
+    """A workspace for one call: megabytes of parts, of which only the counters in front are
+    cleared."""
+    import torch
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws.narrow(0, 0, DGT_TREE_ATTENTION_ZEROED).zero_()
+    return ws
+
+
 def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None, scale=None,
                        out=None, ws=None, stream=None):
     """Attention of the new tokens q [tokens, heads, dim] over each request's cached tokens
     and over those of its new tokens (already stored) that `mask` (dgt_page_plan) lets a
     token see; without a mask each sees the ones before it and itself.  scale defaults to
-    dim ** -0.5.  Rows past cu[-1] of `out` are not written."""
+    dim ** -0.5.  Rows past cu[-1] of `out` are not written.  ws: a workspace to keep between
+    calls (alloc_workspace); without one each call makes its own."""
     import torch
     i32, words = torch.int32, 0
     try:
@@ -646,7 +658,7 @@ def dgt_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, mask=None
         out_row, out_head, _ = out.stride()
     if ws is None:
         nbytes = dgt_tree_attention_workspace(shape, kv_heads, requests)
-        ws = _made_on(stream, lambda: alloc_workspace(nbytes, dev))
+        ws = _made_on(stream, lambda: _attention_workspace(nbytes, dev))
     _call("dgt_tree_attention", dev, stream, _elements()[dtype], q.data_ptr(), q_row, q_head,
           k_cache.data_ptr(), v_cache.data_ptr(), blocks, block, block_table.data_ptr(), width,
           ctx_lens.data_ptr(), cu.data_ptr(), requests, tokens, heads, kv_heads, dim,

@@ -977,10 +977,14 @@ AttnPlan plan_attention(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint
   p.grid = kCUs * (p.rt == 0 ? kNarrowPerCU : kWidePerCU);
   // the counters' room is the same for every call, so that no call's parts lie where
   // another's counters are
-  p.part_off = (kCUs * kNarrowPerCU * kRoom * 4 + 255) / 256 * 256;
+  p.part_off = DGT_TREE_ATTENTION_ZEROED;
   p.ws_bytes = p.part_off + (size_t)p.grid * kRoom * (p.rt ? 64 * p.rt : 16) * (p.dp + 2) * 4;
   return p;
 }
+
+static_assert(DGT_TREE_ATTENTION_ZEROED % 256 == 0 &&
+                  DGT_TREE_ATTENTION_ZEROED >= kCUs * std::max(kNarrowPerCU, kWidePerCU) * kRoom * 4,
+              "a counter for each part");
 
 bool attn_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim, uint32_t requests) {
   return heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0 && heads <= 65536 && dim >= 8 &&

@@ -323,10 +323,12 @@ int dgt_kv_store(const void* d_k, const void* d_v, uint32_t source, int64_t k_ro
  *          of 2; q 16-byte aligned.  Rows past cu[requests] are not written.
  *   d_mask: uint64[tokens, mask_words] or NULL with mask_words 0.
  *   scale > 0.  dim: a multiple of 8 up to 256.
- *   d_ws: dgt_tree_attention_workspace(...) bytes, zero-filled before its first
- *          use; every call leaves it ready for the next (on one stream).
+ *   d_ws: dgt_tree_attention_workspace(...) bytes, of which the first
+ *          DGT_TREE_ATTENTION_ZEROED are zero-filled before its first use (the rest
+ *          may hold anything); every call leaves it ready for the next (on one stream).
  * One launch; the order of all sums is fixed by the lengths and shapes.
  * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED, E_HIP. */
+#define DGT_TREE_ATTENTION_ZEROED 9216
 size_t dgt_tree_attention_workspace(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim,
                                     uint32_t requests);
 int dgt_tree_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t q_head,

@@ -296,6 +296,25 @@ def test_one_workspace_for_every_kind_of_call():
         assert torch.equal(_run(cases[i], ws=ws), own[i]), i
 
 
+def test_only_the_counters_are_cleared(monkeypatch):
+    """The parts of a workspace may hold anything before its first use, and a call that makes
+    its own clears no more of it than the counters."""
+    import torch
+    cases = [_make(124, [3000], [1], 8, 2, 128, 16), _make(125, [3000, 900], [40, 9], 16, 2, 128, 16, words=1)]
+    for d in cases:
+        nbytes = dgt.dgt_tree_attention_workspace(d["q"].shape, 2, len(d["ctx"]))
+        assert nbytes > 100 * dgt.DGT_TREE_ATTENTION_ZEROED
+        ws = torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN in fp32
+        ws[:dgt.DGT_TREE_ATTENTION_ZEROED] = 0
+        want = _run(d, ws=ws)
+        _check(d, want)
+        made, cleared = torch.zeros, []
+        monkeypatch.setattr(torch, "zeros", lambda *a, **kw: cleared.append(made(*a, **kw)) or cleared[-1])
+        assert torch.equal(_run(d), want)
+        monkeypatch.undo()
+        assert all(t.nbytes <= dgt.DGT_TREE_ATTENTION_ZEROED for t in cleared)
+
+
 def test_scale_is_taken():
     d = _make(101, [150], [4], 4, 2, 64, 16)
     for scale in (1e-3, 0.3):

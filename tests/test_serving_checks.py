@@ -147,6 +147,14 @@ def test_c_abi_refusals():
     assert lora(size=dgt.dgt_lora_workspace(5, 3, 40, 64, 16) - 1) == -4
 
 
+def test_header_and_binding_agree_on_the_cleared_bytes():
+    import os
+    import re
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "dgt.h")
+    value = re.search(r"#define DGT_TREE_ATTENTION_ZEROED (\d+)", open(header).read()).group(1)
+    assert int(value) == dgt.DGT_TREE_ATTENTION_ZEROED
+
+
 def test_empty_calls_do_nothing():
     """No token: success without a launch (the pointers are never read)."""
     L = dgt.lib()
