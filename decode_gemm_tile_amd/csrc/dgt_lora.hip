@@ -370,6 +370,10 @@ int dgt_lora_add(const float* d_y, uint64_t y_row, const uint16_t* d_x, uint64_t
   if (tokens == 0) return DGT_OK;
   if (!d_y || !d_out || !d_cu || !d_x || !d_ws) return DGT_E_ARG;
   if ((requests && !d_ids) || (adapters && (!d_a || !d_b || !d_scaling))) return DGT_E_ARG;
+  if (tokens == 1) {  // one row has no stride
+    x_row = k;
+    y_row = out_row = ((uint64_t)n + 3) / 4 * 4;
+  }
   if (y_row < n || out_row < n || x_row < k || x_row % 8) return DGT_E_SHAPE;
   if (!aligned(d_x, 16) || !aligned(d_a, 16) || !aligned(d_b, 16) || !aligned(d_ws, 256)) return DGT_E_ARG;
   if (d_out == d_y && out_row != y_row) return DGT_E_ARG;

@@ -1056,6 +1056,8 @@ int dgt_tree_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t 
   if (!d_q || !d_out || !d_cu || !d_ctx || !d_ws) return DGT_E_ARG;
   if ((width && !d_table) || (blocks && (!d_k_cache || !d_v_cache))) return DGT_E_ARG;
   if ((mask_words != 0) != (d_mask != nullptr) || mask_words > 1024) return DGT_E_ARG;
+  if (tokens == 1) q_row = out_row = 0;  // one row, or one head, has no stride
+  if (heads == 1) q_head = out_head = 0;
   if (!aligned(d_q, 16) || !aligned(d_k_cache, 16) || !aligned(d_v_cache, 16) || !aligned(d_out, 4) ||
       !aligned(d_ws, 256) || q_row % 8 || q_head % 8 || out_row % 2 || out_head % 2)
     return DGT_E_ARG;

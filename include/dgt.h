@@ -320,7 +320,8 @@ int dgt_kv_store(const void* d_k, const void* d_v, uint32_t source, int64_t k_ro
  *   type: BF16 or F16, of q, the pages and out.
  *   d_q, d_out: [tokens, heads, dim] with element strides per row and head,
  *          elements of a head contiguous; strides of q multiples of 8, of out
- *          of 2; q 16-byte aligned.  Rows past cu[requests] are not written.
+ *          of 2; q 16-byte aligned.  (A single row's stride is not looked at, nor a
+ *          single head's.)  Rows past cu[requests] are not written.
  *   d_mask: uint64[tokens, mask_words] or NULL with mask_words 0.
  *   scale > 0.  dim: a multiple of 8 up to 256.
  *   d_ws: dgt_tree_attention_workspace(...) bytes, of which the first
@@ -344,7 +345,8 @@ int dgt_tree_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t 
  * id is outside 0..adapters-1, or of no request, get out[t] = y[t].
  *   d_x: bf16 [tokens, k]; d_a: bf16 [adapters, rank, k]; d_b: bf16 [adapters,
  *          n, rank]; d_scaling: float[adapters]; d_y, d_out: fp32 [tokens, n];
- *          x_row, y_row, out_row are element strides of the rows.
+ *          x_row, y_row, out_row are element strides of the rows, no shorter than a
+ *          row (not looked at where tokens is 1).
  *   d_out may be d_y (then rows without an adapter are not touched); otherwise
  *          they do not overlap.
  * k is a multiple of 8, rank a multiple of 8 up to 256; x_row a multiple of 8; x, a, b 16-byte

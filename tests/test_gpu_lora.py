@@ -144,6 +144,20 @@ def test_lora_strided_rows():
     assert (wide_y[:, :100] == 7).all() and (wide_y[:, 220:] == 7).all()
 
 
+def test_lora_single_row_of_any_stride():
+    """The stride of a dimension of size one means nothing: a transposed column is a row."""
+    import torch
+    d = _make(14, [1], 130, 64, 16, 2, ids=[1])
+    y, x, *rest = _dev(d)
+    want = dgt.dgt_lora_add(y, x, *rest, out=torch.empty_like(y))
+    _check(d, want)
+    column = lambda t: t.clone().as_strided(t.shape, (1, 1))  # as (n, 1) transposed has it
+    for y1, x1, out in ((column(y), x, None), (y, x.as_strided((1, 64), (3, 1)), column(y)),
+                        (column(y), column(x), torch.empty_like(y))):
+        assert y1.is_contiguous() and x1.is_contiguous()
+        assert torch.equal(dgt.dgt_lora_add(y1, x1, *rest, out=out), want)
+
+
 def test_lora_nan_stays_in_its_rows():
     """A NaN or infinity in one request's x or adapter does not reach the others."""
     import torch

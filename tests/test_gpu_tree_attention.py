@@ -255,6 +255,19 @@ def test_strides_of_queries_and_outputs():
         dgt.dgt_tree_attention(wide[:, 2:10, 1:65], *args, mask=_mask(d))
 
 
+def test_single_rows_and_heads_of_any_stride():
+    """The stride of a dimension of size one means nothing."""
+    import torch
+    for d in (_make(126, [50], [1], 4, 2, 64, 16), _make(127, [50], [3], 1, 1, 64, 16), _make(128, [9], [1], 1, 1, 64, 16)):
+        q = d["q"].cuda()
+        plain = _run(d)
+        _check(d, plain)
+        odd = tuple(13 if n == 1 else s for n, s in zip(q.shape[:2], q.stride())) + (1,)
+        args = (d["kc"].cuda(), d["vc"].cuda(), _i32(d["table"]), _i32(d["ctx"]), _i32(d["cu"]))
+        out = torch.empty_like(q).as_strided(q.shape, odd)
+        assert torch.equal(dgt.dgt_tree_attention(q.as_strided(q.shape, odd), *args, out=out), plain)
+
+
 def test_rows_past_the_requests_are_not_written():
     import torch
     d = _make(98, [20], [3], 4, 2, 64, 16)
