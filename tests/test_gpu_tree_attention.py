@@ -138,6 +138,58 @@ def test_drafted_keys_at_every_place_of_a_tile(offset):
     _check(d, _run(d))
 
 
+@pytest.mark.parametrize("ctx,new,heads,kv,dtype", [([0], [1000], 4, 2, "bfloat16"), ([77, 0], [300, 1100], 4, 1, "bfloat16"),
+                                                    ([1500, 9, 0], [513, 1, 2], 2, 2, "float16")])
+def test_prompts(ctx, new, heads, kv, dtype):
+    """Chains of many new tokens, with and without cached ones, split between workgroups."""
+    d = _make(len(new) + 200, ctx, new, heads, kv, 64, 16, dtype=dtype)
+    _check(d, _run(d))
+
+
+def _device_reference(q, kc, vc, pages, ctx, n, see, scale):
+    """float64 on the device for one request, head by head (the oracle takes minutes at this size).
+    q [n, heads, dim]; see [n, n] over the new tokens.  Returns (out, weighted mean of |v|)."""
+    import torch
+    heads, dim = q.shape[1:]
+    group = heads // kc.shape[1]
+    out, size = (torch.empty(q.shape, dtype=torch.float64, device="cuda") for _ in range(2))
+    seen = torch.cat([torch.ones((n, ctx), dtype=torch.bool), torch.from_numpy(see)], 1).cuda()
+    for g in range(kc.shape[1]):
+        keys = kc[pages, g].reshape(-1, dim)[:ctx + n].double().t().contiguous()
+        values = vc[pages, g].transpose(1, 2).reshape(-1, dim)[:ctx + n].double().contiguous()
+        for h in range(g * group, (g + 1) * group):
+            z = torch.mm(q[:, h].double(), keys) * scale
+            w = torch.softmax(z.masked_fill(~seen, -float("inf")), 1)
+            out[:, h], size[:, h] = torch.mm(w, values), torch.mm(w, values.abs())
+    return out, size
+
+
+@pytest.mark.parametrize("new", [5, 40])
+def test_runs_of_more_pages_than_fit_in_lds(new):
+    """Small pages and so many keys that one workgroup's run of them spans more than 1024 pages:
+    8 requests of 80000 keys, 8 key heads.  Requests share their pages, as a common prefix would."""
+    import torch
+    heads, kv, dim, block, requests = 16, 8, 64, 8, 8
+    ctx = [80000 - 999 * b for b in range(requests)]
+    # units of 128 keys, dealt to 512 workgroups (one tile of rows); pages of 8 keys
+    tiles = -(-new * heads // kv // 128)
+    assert sum(c // 128 for c in ctx) * kv * tiles // 512 * (128 // block) > 1024
+    g = torch.Generator(device="cuda").manual_seed(3)
+    blocks = -(-(max(ctx) + new) // block)
+    randn = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    kc, vc, q = randn(blocks, kv, block, dim), randn(blocks, kv, dim, block), randn(requests * new, heads, dim)
+    pages = torch.randperm(blocks, generator=g, device="cuda")
+    see = serving.ancestors([int(i) for i in np.random.default_rng(new).integers(-1, np.arange(new))])
+    mask = torch.from_numpy(np.tile(serving.pack_mask(see, 1), (requests, 1)).view(np.int64)).cuda()
+    out = dgt.dgt_tree_attention(q, kc, vc, pages.int().repeat(requests, 1).contiguous(), _i32(ctx),
+                                 _i32(np.arange(requests + 1) * new), mask=mask)
+    u = 2.0 ** -8
+    for b, c in enumerate(ctx):
+        rows = slice(b * new, (b + 1) * new)
+        ref, size = _device_reference(q[rows], kc, vc, pages, c, new, see, dim ** -0.5)
+        assert ((out[rows].double() - ref).abs() <= u * ref.abs() + (u + 4e-4) * size).all(), b
+
+
 def test_sharp_softmax():
     """Scores of some hundreds: all weight on a few keys, maxima that move between tiles."""
     d = _make(90, [900, 333], [3, 20], 8, 2, 128, 16, words=1, spread=6.0)
