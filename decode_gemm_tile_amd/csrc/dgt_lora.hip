@@ -49,7 +49,8 @@ __device__ __forceinline__ void store4(float* row, uint32_t n, uint32_t n1, bool
 // rows come in whole lines, a stage of K at a time, and turn in LDS.  Eight waves
 // share a stage's steps of 32 and are added in LDS at the end.  The next stage is
 // on its way in registers while this one is multiplied.  Bound by memory and its
-// latency: 64 rows of 56 adapters at K = 16384, rank 16, take 8.9 us for 33 MB.
+// latency: 64 rows of 56 adapters at K = 16384, rank 16, take 9.1 us for 33 MB from the
+// caches and 11.2 from memory.
 // (32 tokens a workgroup were slower: 18.6 against 14.4 us for 2050 tokens, K = 4096,
 // rank 64.)
 constexpr uint32_t kShrinkWaves = 8;
@@ -153,7 +154,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_lora_shrink(LoraArgs p) {
 // Results turn in LDS, so that y and out are met in whole lines a row (in the
 // instruction's layout 16 lanes would ask for 16 rows).  MT = 2 takes 32 tokens,
 // MT = 1 up to 16.  2050 rows by 14336 columns at rank 64 take 51 us for 235 MB, 64
-// single rows by 53248 at rank 16 26 us for 122 MB: 4.6 TB/s, where a large copy moves 5.1.
+// single rows by 53248 at rank 16 27 us for 122 MB: 4.6 TB/s, where a large copy moves
+// 5.1.  That is with what the caches hold of the call before; on inputs that change from
+// call to call they take 61 and 36 us (3.9 and 3.4 TB/s): a pass is one chain of loads,
+// products and two barriers, and memory's latency is longer.
 template <int MT>
 struct Expand {
   static constexpr uint32_t kRows = 16 * MT;
@@ -331,7 +335,8 @@ LoraPlan plan_lora(uint32_t tokens, uint32_t requests, uint32_t n, uint32_t k, u
   p.splits = (k + p.split_k - 1) / p.split_k;
   // Tokens and columns of a workgroup of the second kernel: 32 rows where requests
   // have as many (2050 tokens in 6 requests: 49 us, 16 rows 61; single tokens: 37 us
-  // against 26), four workgroups a CU (two: 59 and 34 us, sixteen: 58 and 31).
+  // against 26), four workgroups a CU (two: 59 and 34 us, sixteen: 58 and 31), all from
+  // the caches.
   p.expand_mt = each >= 32 ? 2 : 1;
   const uint32_t cols = p.expand_mt == 2 ? Expand<2>::kCols : Expand<1>::kCols;
   const uint32_t rows2 = 16 * p.expand_mt, chunks2 = std::max(std::min(tokens / rows2 + requests, tokens), 1u);

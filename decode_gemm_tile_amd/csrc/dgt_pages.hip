@@ -14,7 +14,7 @@ namespace {
 // a few microseconds of latency and no work, so every workgroup forms them for
 // itself in LDS and goes on to its own tokens: one launch, no hand-off.  Bound by its
 // chain of latencies (8 tokens of 8 requests 3.2 us, 12750 tokens of 509 requests with
-// trees of up to 61 8.2 us).
+// trees of up to 61 8.3 us).
 struct PlanArgs {
   const int32_t *ctx, *fresh_tokens, *free_list, *free_head, *parents;
   int32_t *table, *cu, *slots, *positions, *counts;
@@ -222,9 +222,11 @@ __global__ __launch_bounds__(kPlanThreads) void k_page_plan(PlanArgs p) {
 // A workgroup takes 64 tokens of one head.  Key rows are copied into their pages as
 // they are, 16 bytes a thread.  Value pages are transposed: the values turn in LDS,
 // and tokens whose slots follow one another within 8 aligned slots are written
-// together, 16 bytes where all 8 are there.  Bound by the bytes: 6792 tokens of 8
-// heads of 128 from fp32 rows take 22.5 us, 3.7 TB/s (35 us with one element a thread
-// straight to its place).
+// together, 16 bytes where all 8 are there.  6792 tokens of 8 heads of 128 from fp32
+// rows take 22.6 us, 3.7 TB/s (35 us with one element a thread straight to its place),
+// and 27.6 where no cache holds anything of them; a plain cast of as many values takes
+// 16.6.  Bytes do not bound it alone: the 856 equal workgroups are 3.3 a CU, so the last
+// round is partly empty.
 struct StoreArgs {
   const void *k, *v;
   const int32_t* slots;
@@ -388,8 +390,8 @@ int dgt_page_plan(const int32_t* d_ctx, const int32_t* d_new, uint32_t requests,
   };
   // Every workgroup reads the list's head.  Where it lies in the counts (a step that
   // goes on from its own last result), the new one may be written only after the last
-  // of them has read the old one, which the order of two launches gives; a single
-  // workgroup has its barriers.
+  // of them has read the old one, which the order of two launches gives (12750 tokens:
+  // 13.8 us a pass, 10.0 with one); a single workgroup has its barriers.
   const uintptr_t head = reinterpret_cast<uintptr_t>(d_free_head), counts = reinterpret_cast<uintptr_t>(d_counts);
   if (grid > 1 && head + 4 > counts && head < counts + 12) {
     const int rc = run(grid, true, false);

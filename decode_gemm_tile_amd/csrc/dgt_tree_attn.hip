@@ -426,9 +426,12 @@ __device__ __forceinline__ bool softmax_step(floatx4 (&s)[N], Softmax& m, float&
   return moves;
 }
 
-// The weights of 8 keys, rounded to the cache's type as the matrix instruction takes
-// them.  l, which divides the outputs, adds the rounded ones: where few keys hold most
-// of the weight their rounding cancels.
+// The weights of 8 keys, rounded to the cache's type: the matrix instruction has one
+// type for both operands, and a second product for the bits that are lost would double
+// half of the work.  It costs a bf16 result up to a third more error than its own
+// rounding has (0.0019 to 0.0023 relative, 0.0017 with fp32 weights; fp16 0.00024 and
+// 0.00021).  l, which divides the outputs, adds the rounded ones: where few keys hold
+// most of the weight their rounding cancels.
 template <class E>
 __device__ __forceinline__ u32x4 weights(const floatx4& s0, const floatx4& s1, float& l) {
   const u32x4 p = {E::pack2(s0[0], s0[1]), E::pack2(s0[2], s0[3]), E::pack2(s1[0], s1[1]), E::pack2(s1[2], s1[3])};
@@ -450,7 +453,7 @@ constexpr uint32_t kPageRoom = 1024;
 // ------------------------------------------------------------------ few rows
 // Each wave streams its own 32 keys of a unit from memory straight into the
 // operands; the waves meet once an item.  Bound by memory: 96 requests of up to 8100
-// keys, one token on 8 key heads of 128, take 232 us for 1.29 GB, 5.6 TB/s (a large
+// keys, one token on 8 key heads of 128, take 229 us for 1.29 GB, 5.6 TB/s (a large
 // copy moves 5.1), three workgroups a CU keeping the loads in flight.  Small calls are
 // a chain of latencies: lengths, table, keys, the waves' meeting, and where a tile's
 // keys are split the parts (one token over 1000 keys: 11.2 us).
@@ -639,15 +642,22 @@ __global__ __launch_bounds__(256, 3) void k_attention_narrow(AttnArgs a) {
 // ----------------------------------------------------------------- more rows
 // The waves take 16 RT rows each and share tiles of keys and values in LDS, two
 // buffers deep: the next tile is loaded into registers while this one is
-// multiplied.  16-byte pieces of a row are permuted by its number so that the
-// lanes of an operand read fall on different banks.
+// multiplied.  16-byte pieces of a row are permuted by its number, which spreads the
+// 16 rows of an operand read over 8 places; conflicts still take 24% of the LDS cycles.
 //
-// 64 rows are bound by memory (64 requests of 8000 keys, 8 key heads of 128: 6.1 TB/s
-// with 16-token pages).  128 rows reach 650 TFLOP/s over keys in the caches (760 with
-// 64-token pages): beside 64 matrix instructions a tile and wave has 216 vector ones,
-// the exponentials among them, and the registers of two waves a SIMD leave no room to
-// run one tile's products into another's softmax (tiles of 32 keys, the next tile's
-// loads between the products, and wave priorities were measured and were no faster).
+// 64 rows are bound by memory (64 requests of 8000 keys, 8 key heads of 128: 5.7 TB/s
+// with 16-token pages).  128 rows reach 560 TFLOP/s over keys in the caches (4 requests of
+// 8000 keys, 32 tokens on 128 heads; 600 with 64-token pages): beside 64 matrix
+// instructions a tile and wave has 216 vector ones, the exponentials among them, and the
+// registers of two waves a SIMD leave no room to run one tile's products into another's
+// softmax (tiles of 32 keys, the next tile's loads between the products, and wave
+// priorities were measured and were no faster).
+//
+// A tile of rows runs over all keys of its request, also where there is no mask and the
+// last of them lie behind all of its tokens, and treats every tile of keys past the cached
+// ones as one that some row does not see.  Drafts are short beside what is cached, but a
+// prompt pays twice: 4000 new tokens on 32 heads, nothing cached, take 498 us, 263 TFLOP/s
+// of the products that are needed.
 template <int DP>
 struct Tile {
   static constexpr uint32_t kKeys = DP == 256 ? 32 : 64;
@@ -966,12 +976,16 @@ AttnPlan plan_attention(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint
   AttnPlan p;
   p.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
   // By the rows of a request and key head, on the average.  32 requests of 4000 keys, 8
-  // key heads of 128, narrow against wide: 4 rows 102 and 95 us, 8 rows 104 and 95, 16
-  // rows 113 and 95, 32 rows 193 and 97; but 8 requests of 1000 keys at 4 rows 13 and 18,
-  // one of 4000 17 and 30: up to 8 rows the narrow kernel, whose workgroups need no
-  // common tile, loses little where it loses.  64-row tiles against 128: 64 rows 103 and
-  // 113 us, 80 rows 130 and 113.  Heads over 128 leave the narrow kernel too few
-  // registers (16 requests of 4000 keys, 8 rows of 256: 78 and 63 us).
+  // key heads of 128, narrow against wide: 4 rows 103 and 98 us, 8 rows 105 and 97, 16
+  // rows 112 and 98, 32 rows 196 and 100; but 8 requests of 1000 keys at 4 rows 12.5 and
+  // 17.1, one of 4000 17 and 28: up to 8 rows the narrow kernel, whose workgroups need no
+  // common tile, loses little where it loses.  64-row tiles against 128: 64 rows 107 and
+  // 114 us, 80 rows 131 and 115.  Heads over 128 leave the narrow kernel too few
+  // registers (16 requests of 4000 keys, 8 rows of 256: 286 and 110 us).
+  // Uneven batches (4000 cached keys, 32 heads on 8; narrow, 64-row, 128-row tiles): one
+  // request of 100 new tokens among 95 of one 280, 271, 286 us (the rule: narrow); 512
+  // among 63 of one 360, 230, 240 (64-row); four of 512 among 60 of one 1067, 427, 366
+  // (128-row); a prompt of 2000 among 31 of one 445, 293, 266 (128-row).
   const uint64_t rows = (uint64_t)tokens * (heads / kv_heads) / std::max(requests, 1u);
   p.rt = rows <= 8 && p.dp <= 128 ? 0 : rows <= 64 || p.dp == 256 ? 1 : 2;
   p.grid = kCUs * (p.rt == 0 ? kNarrowPerCU : kWidePerCU);

@@ -326,7 +326,8 @@ int dgt_kv_store(const void* d_k, const void* d_v, uint32_t source, int64_t k_ro
  *   scale > 0.  dim: a multiple of 8 up to 256.
  *   d_ws: dgt_tree_attention_workspace(...) bytes, of which the first
  *          DGT_TREE_ATTENTION_ZEROED are zero-filled before its first use (the rest
- *          may hold anything); every call leaves it ready for the next (on one stream).
+ *          may hold anything); every call leaves it ready for the next (on one
+ *          stream).  No other entry point's workspace: those would write over the zeros.
  * One launch; the order of all sums is fixed by the lengths and shapes.
  * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED, E_HIP. */
 #define DGT_TREE_ATTENTION_ZEROED 9216
