@@ -28,7 +28,9 @@ EXPORTS = ["dgt_version", "dgt_status_string", "dgt_compress_bound", "dgt_compre
            "dgt_fused_decode_gemm", "dgt_dense_workspace", "dgt_dense_gemm",
            "dgt_noalloc_scratch_bytes", "dgt_fused_decode_gemm_noalloc",
            "dgt_page_plan", "dgt_kv_store", "dgt_tree_attention_workspace", "dgt_tree_attention",
-           "dgt_lora_workspace", "dgt_lora_add"]
+           "dgt_lora_workspace", "dgt_lora_add", "dgt_rope_store",
+           "dgt_chunk_attention_workspace", "dgt_chunk_attention", "dgt_verify_workspace", "dgt_verify",
+           "dgt_page_keep", "dgt_page_fork", "dgt_page_free_workspace", "dgt_page_free"]
 # element types of the serving operators
 DGT_ELT_BF16, DGT_ELT_F16, DGT_ELT_F32 = 1, 2, 3
 # bytes at the start of dgt_tree_attention's workspace that are zero before its first use
@@ -115,6 +117,31 @@ def lib():
         L.dgt_lora_add.restype = ctypes.c_int
         L.dgt_lora_add.argtypes = [vp, u64, vp, u64, vp, vp, vp, u32, vp, vp, u32, u32, u32, u32,
                                    u32, vp, u64, vp, sz, vp]
+        f32 = ctypes.c_float
+        L.dgt_rope_store.restype = ctypes.c_int
+        L.dgt_rope_store.argtypes = [vp, vp, vp, u32, i64, i64, i64, i64, i64, i64, vp, vp, u32, u32, u32,
+                                     u32, vp, u32, u32, vp, vp, f32, u32, vp, i64, i64, vp, vp, u32, u32,
+                                     vp]
+        L.dgt_chunk_attention_workspace.restype = sz
+        L.dgt_chunk_attention_workspace.argtypes = [u32, u32, u32, u32, u32]
+        L.dgt_chunk_attention.restype = ctypes.c_int
+        L.dgt_chunk_attention.argtypes = [u32, vp, u64, u64, vp, vp, u32, u32, vp, u32, vp, vp, u32, u32,
+                                          u32, u32, u32, f32, vp, u64, u64, vp, sz, vp]
+        L.dgt_verify_workspace.restype = sz
+        L.dgt_verify_workspace.argtypes = [u32, u32, u32]
+        L.dgt_verify.restype = ctypes.c_int
+        L.dgt_verify.argtypes = [u32, vp, u64, vp, vp, u64, vp, vp, vp, vp, vp, u32, u32, u32, vp, vp, vp,
+                                 vp, sz, vp]
+        L.dgt_page_keep.restype = ctypes.c_int
+        L.dgt_page_keep.argtypes = [vp, vp, vp, vp, vp, u32, u32, vp, u32, vp, vp, u32, u32, u32, u32, u32,
+                                    u32, vp, vp, vp, vp, vp]
+        L.dgt_page_fork.restype = ctypes.c_int
+        L.dgt_page_fork.argtypes = [vp, vp, u32, vp, vp, u32, u32, vp, u32, vp, vp, u32, u32, u32, u32, u32,
+                                    vp, vp, vp, vp]
+        L.dgt_page_free_workspace.restype = sz
+        L.dgt_page_free_workspace.argtypes = [u32]
+        L.dgt_page_free.restype = ctypes.c_int
+        L.dgt_page_free.argtypes = [vp, u32, vp, vp, u32, u32, vp, u32, vp, vp, u32, u32, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -378,7 +405,7 @@ def _check_rows(t, name, dtypes, shape, device):
     _need(t.dtype in dtypes, "%s has dtype %s, expected one of %s"
           % (name, t.dtype, ", ".join(str(d) for d in dtypes)))
     _need(t.shape == shape, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    _need(t.stride(-1) == 1 or shape[-1] <= 1, "%s must be contiguous in its last dimension" % name)
+    _need(t.stride(-1) == 1 or shape[-1] <= 1 or 0 in shape, "%s must be contiguous in its last dimension" % name)
     _need(t.device == device, "%s is on %s, expected %s" % (name, t.device, device))
 
 
@@ -737,3 +764,409 @@ def dgt_lora_add(y, x, a, b, scaling, adapters, cu, out=None, ws=None, stream=No
           a.data_ptr(), b.data_ptr(), scaling.data_ptr(), count, adapters.data_ptr(), cu.data_ptr(),
           requests, tokens, n, k, rank, out.data_ptr(), out.stride(0), ws.data_ptr(), ws.numel())
     return out
+
+
+def _check_rope_store(q, k, v, positions, slots, freqs, k_cache, v_cache, q_weight, k_weight, q_out):
+    import torch
+    blocks, kv_heads, block, dim = _check_caches(k_cache, v_cache)
+    dev = k_cache.device
+    tokens, heads, _ = _dims(q, "q", 3)
+    _check_rows(q, "q", (torch.float32, k_cache.dtype), (tokens, heads, dim), dev)
+    _check_rows(k, "k", (q.dtype,), (tokens, kv_heads, dim), dev)
+    _check_rows(v, "v", (q.dtype,), (tokens, kv_heads, dim), dev)
+    _check_array(positions, "positions", torch.int32, (tokens,), dev)
+    _check_array(slots, "slots", torch.int32, (tokens,), dev)
+    if freqs is not None:
+        (pairs,) = _dims(freqs, "freqs", 1)
+        _check_array(freqs, "freqs", torch.float64, (pairs,), dev)
+        _need(2 * pairs <= dim, "freqs holds %d pairs, heads have %d elements" % (pairs, dim))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _check_array(w, name, torch.float32, (dim,), dev)
+    if q_out is not None:
+        _check_rows(q_out, "q_out", (k_cache.dtype,), (tokens, heads, dim), dev)
+    _check_gpu(dev)
+
+
+def dgt_rope_store(q, k, v, positions, slots, freqs, k_cache, v_cache, q_weight=None, k_weight=None, eps=1e-6,
+                   interleaved=False, q_out=None, stream=None):
+    """Norms of q and k for each head (where a weight float32[dim] is given) and their rotation by
+    positions * freqs (float64[pairs], radians a position; None: no rotation); q goes to q_out
+    [tokens, heads, dim] in the caches' dtype, k and v into the pages at `slots`.  q, k, v: the caches'
+    dtype or float32, any row and head strides.  Rows with a negative position are skipped (those of a
+    q_out made here are then undefined).  Returns q_out."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    elements, pairs = _elements(), 0
+    try:
+        dev, dtype, source = k_cache.device, k_cache.dtype, q.dtype
+        blocks, kv_heads, block, dim = k_cache.shape
+        shape = tokens, heads, _ = q.shape
+        kv_shape = (tokens, kv_heads, dim)
+        (q_row, q_head, q_one), (k_row, k_head, k_one), (v_row, v_head, v_one) = q.stride(), k.stride(), v.stride()
+        good = (dev.type == "cuda" and (dtype is torch.bfloat16 or dtype is torch.float16)
+                and k_cache.is_contiguous() and v_cache.dtype is dtype
+                and v_cache.shape == (blocks, kv_heads, dim, block) and v_cache.is_contiguous()
+                and v_cache.device == dev and (source is dtype or source is f32)
+                and shape[2] == dim and q.device == dev and q_one == 1
+                and k.dtype is source and k.shape == kv_shape and k.device == dev and k_one == 1
+                and v.dtype is source and v.shape == kv_shape and v.device == dev and v_one == 1
+                and positions.dtype is i32 and positions.shape == (tokens,) and positions.is_contiguous()
+                and positions.device == dev
+                and slots.dtype is i32 and slots.shape == (tokens,) and slots.is_contiguous() and slots.device == dev)
+        if freqs is not None:
+            (pairs,) = freqs.shape
+            good = (good and freqs.dtype is torch.float64 and 2 * pairs <= dim and freqs.is_contiguous()
+                    and freqs.device == dev)
+        for w in (q_weight, k_weight):
+            if w is not None:
+                good = good and w.dtype is f32 and w.shape == (dim,) and w.is_contiguous() and w.device == dev
+        if q_out is not None:
+            good = (good and q_out.dtype is dtype and q_out.shape == shape and q_out.stride(2) == 1
+                    and q_out.device == dev)
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_rope_store(q, k, v, positions, slots, freqs, k_cache, v_cache, q_weight, k_weight, q_out)
+    if q_out is None:
+        q_out = _made_on(stream, lambda: torch.empty(shape, dtype=dtype, device=dev))
+        out_row, out_head = heads * dim, dim
+    else:
+        out_row, out_head, _ = q_out.stride()
+    _call("dgt_rope_store", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), elements[source], q_row, q_head,
+          k_row, k_head, v_row, v_head, positions.data_ptr(), slots.data_ptr(), tokens, heads, kv_heads, dim,
+          freqs.data_ptr() if pairs else None, pairs, 1 if interleaved else 0,
+          None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+          elements[dtype], q_out.data_ptr(), out_row, out_head, k_cache.data_ptr(), v_cache.data_ptr(), blocks, block)
+    return q_out
+
+
+def dgt_chunk_attention_workspace(q_shape, kv_heads, requests) -> int:
+    """Bytes of workspace for queries of shape [tokens, heads, dim]."""
+    tokens, heads, dim = q_shape
+    n = lib().dgt_chunk_attention_workspace(tokens, heads, kv_heads, dim, requests)
+    if n == 0:
+        raise DgtError(-2, "dgt_chunk_attention_workspace")
+    return n
+
+
+def dgt_chunk_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, scale=None, out=None, ws=None,
+                        stream=None):
+    """Causal attention of the new tokens q [tokens, heads, dim] over each request's cached tokens and
+    its new ones (already stored): dgt_tree_attention without a mask, made for prompts and parts of
+    prompts.  scale defaults to dim ** -0.5.  Rows past cu[-1] of `out` are not written.  ws: a workspace
+    to keep between calls (any contents); without one each call makes its own."""
+    import torch
+    i32 = torch.int32
+    try:
+        dev, dtype = k_cache.device, k_cache.dtype
+        blocks, kv_heads, block, dim = k_cache.shape
+        shape = tokens, heads, _ = q.shape
+        requests, width = block_table.shape
+        q_row, q_head, q_one = q.stride()
+        good = (dev.type == "cuda" and (dtype is torch.bfloat16 or dtype is torch.float16)
+                and k_cache.is_contiguous() and v_cache.dtype is dtype
+                and v_cache.shape == (blocks, kv_heads, dim, block) and v_cache.is_contiguous()
+                and v_cache.device == dev
+                and q.dtype is dtype and shape[2] == dim and q_one == 1 and q.device == dev
+                and kv_heads > 0 and heads % kv_heads == 0
+                and block_table.dtype is i32 and block_table.is_contiguous() and block_table.device == dev
+                and ctx_lens.dtype is i32 and ctx_lens.shape == (requests,) and ctx_lens.is_contiguous()
+                and ctx_lens.device == dev
+                and cu.dtype is i32 and cu.shape == (requests + 1,) and cu.is_contiguous() and cu.device == dev)
+        if out is not None:
+            good = good and out.dtype is dtype and out.shape == shape and out.stride(2) == 1 and out.device == dev
+        if ws is not None:
+            good = good and ws.dtype is torch.uint8 and ws.dim() == 1 and ws.is_contiguous() and ws.device == dev
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_tree_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, None, out, ws)
+    if out is None:
+        out = _made_on(stream, lambda: torch.empty(shape, dtype=dtype, device=dev))
+        out_row, out_head = heads * dim, dim
+    else:
+        out_row, out_head, _ = out.stride()
+    if ws is None:
+        nbytes = dgt_chunk_attention_workspace(shape, kv_heads, requests)
+        ws = _made_on(stream, lambda: torch.empty(nbytes, dtype=torch.uint8, device=dev))
+    _call("dgt_chunk_attention", dev, stream, _elements()[dtype], q.data_ptr(), q_row, q_head,
+          k_cache.data_ptr(), v_cache.data_ptr(), blocks, block, block_table.data_ptr(), width,
+          ctx_lens.data_ptr(), cu.data_ptr(), requests, tokens, heads, kv_heads, dim,
+          dim ** -0.5 if scale is None else scale, out.data_ptr(), out_row, out_head, ws.data_ptr(), ws.numel())
+    return out
+
+
+class Verified:
+    """What dgt_verify returns, on the device: path int32[tokens] (the accepted rows of each
+    request as indexes within it, then -1), accepted int32[requests] (how many, row 0 among
+    them) and next int32[requests] (the token that follows)."""
+
+    __slots__ = ("path", "accepted", "next")
+
+    def __init__(self, path, accepted, next):
+        self.path, self.accepted, self.next = path, accepted, next
+
+    @classmethod
+    def empty(cls, requests, tokens, device="cuda"):
+        import torch
+        return cls(*(torch.empty(n, dtype=torch.int32, device=device) for n in (tokens, requests, requests)))
+
+
+def dgt_verify_workspace(tokens, vocab, requests) -> int:
+    n = lib().dgt_verify_workspace(tokens, vocab, requests)
+    if n == 0:
+        raise DgtError(-2, "dgt_verify_workspace")
+    return n
+
+
+def _check_verify(logits, draft, cu, accept, sample, parents, draft_probs, temperature, out, ws):
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    tokens, vocab = _dims(logits, "logits", 2)
+    dev = logits.device
+    (requests,) = _dims(sample, "sample", 1)
+    _check_rows(logits, "logits", (f32, torch.bfloat16, torch.float16), (tokens, vocab), dev)
+    _check_array(draft, "draft", i32, (tokens,), dev)
+    _check_array(cu, "cu", i32, (requests + 1,), dev)
+    _check_array(accept, "accept", f32, (tokens,), dev)
+    _check_array(sample, "sample", f32, (requests,), dev)
+    if parents is not None:
+        _check_array(parents, "parents", i32, (tokens,), dev)
+    if draft_probs is not None:
+        _need(parents is None, "draft_probs are only taken for chains, without parents")
+        _check_rows(draft_probs, "draft_probs", (f32,), (tokens, vocab), dev)
+    if temperature is not None:
+        _check_array(temperature, "temperature", f32, (requests,), dev)
+    if out is not None:
+        _check_array(out.path, "out.path", i32, (tokens,), dev)
+        _check_array(out.accepted, "out.accepted", i32, (requests,), dev)
+        _check_array(out.next, "out.next", i32, (requests,), dev)
+    if ws is not None:
+        _check_array(ws, "ws", torch.uint8, (None,), dev)
+    _check_gpu(dev)
+
+
+def dgt_verify(logits, draft, cu, accept, sample, parents=None, draft_probs=None, temperature=None, out=None,
+               ws=None, stream=None):
+    """Which drafted tokens the target accepts, and the token that follows.  logits [tokens, vocab]
+    (float32, bfloat16, float16; any row stride) of the step's rows, draft int32[tokens] their tokens;
+    row 0 of each request is decided already, row i follows parents[i] (int32[tokens], as for
+    dgt_page_plan; None: a chain).  accept float32[tokens] and sample float32[requests] are uniform
+    numbers in [0, 1).  draft_probs float32[tokens, vocab] (chains): row i is what the token after row i
+    was drawn from; None: the drafts are taken as given.  temperature float32[requests] (None: 1);
+    0 takes the most likely tokens.  Returns a Verified (out: one to write into).  ws: a workspace to
+    keep between calls (any contents)."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    try:
+        dev, dtype = logits.device, logits.dtype
+        tokens, vocab = logits.shape
+        (requests,) = sample.shape
+        row, one = logits.stride()
+        good = (dev.type == "cuda" and (dtype is f32 or dtype is torch.bfloat16 or dtype is torch.float16)
+                and (one == 1 or vocab == 1 or tokens == 0)
+                and draft.dtype is i32 and draft.shape == (tokens,) and draft.is_contiguous() and draft.device == dev
+                and cu.dtype is i32 and cu.shape == (requests + 1,) and cu.is_contiguous() and cu.device == dev
+                and accept.dtype is f32 and accept.shape == (tokens,) and accept.is_contiguous()
+                and accept.device == dev
+                and sample.dtype is f32 and sample.is_contiguous() and sample.device == dev)
+        if parents is not None:
+            good = (good and draft_probs is None and parents.dtype is i32 and parents.shape == (tokens,)
+                    and parents.is_contiguous() and parents.device == dev)
+        if draft_probs is not None:
+            good = (good and draft_probs.dtype is f32 and draft_probs.shape == (tokens, vocab)
+                    and (draft_probs.stride(1) == 1 or vocab == 1 or tokens == 0) and draft_probs.device == dev)
+        if temperature is not None:
+            good = (good and temperature.dtype is f32 and temperature.shape == (requests,)
+                    and temperature.is_contiguous() and temperature.device == dev)
+        if out is not None:
+            for o, n in ((out.path, tokens), (out.accepted, requests), (out.next, requests)):
+                good = good and o.dtype is i32 and o.shape == (n,) and o.is_contiguous() and o.device == dev
+        if ws is not None:
+            good = good and ws.dtype is torch.uint8 and ws.dim() == 1 and ws.is_contiguous() and ws.device == dev
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_verify(logits, draft, cu, accept, sample, parents, draft_probs, temperature, out, ws)
+    if out is None:
+        out = _made_on(stream, lambda: Verified.empty(requests, tokens, dev))
+    if ws is None:
+        nbytes = dgt_verify_workspace(tokens, vocab, requests)
+        ws = _made_on(stream, lambda: torch.empty(nbytes, dtype=torch.uint8, device=dev))
+    # (a step of no tokens still has parents or probabilities, if only by name)
+    up = None if parents is None else parents.data_ptr() or out.next.data_ptr()
+    probs = None if draft_probs is None else draft_probs.data_ptr() or out.next.data_ptr()
+    _call("dgt_verify", dev, stream, _elements()[dtype], logits.data_ptr(), row, draft.data_ptr(), probs,
+          0 if draft_probs is None else draft_probs.stride(0), up, cu.data_ptr(),
+          None if temperature is None else temperature.data_ptr(), accept.data_ptr(), sample.data_ptr(), requests,
+          tokens, vocab, out.path.data_ptr(), out.accepted.data_ptr(), out.next.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def _layers(k_cache, v_cache):
+    """(layers, blocks, heads, block, dim) of caches of one layer [blocks, ...] or of several
+    [layers, blocks, ...]."""
+    import torch
+    dims = k_cache.dim() if hasattr(k_cache, "data_ptr") else 0
+    _need(dims in (4, 5), "k_cache must be a 4-D or 5-D tensor")
+    layers, (blocks, heads, block, dim) = (k_cache.shape[0] if dims == 5 else 1), k_cache.shape[-4:]
+    front, dtype = tuple(k_cache.shape[:-4]), k_cache.dtype
+    _need(dtype is torch.bfloat16 or dtype is torch.float16,
+          "k_cache has dtype %s, expected torch.bfloat16 or torch.float16" % dtype)
+    _check_array(k_cache, "k_cache", dtype, front + (blocks, heads, block, dim), k_cache.device)
+    _check_array(v_cache, "v_cache", dtype, front + (blocks, heads, dim, block), k_cache.device)
+    return layers, blocks, heads, block, dim
+
+
+def _fast_layers(k_cache, v_cache):
+    """The same without the words: the five numbers, or None where something is wrong."""
+    import torch
+    front = k_cache.shape[:-4]
+    blocks, heads, block, dim = k_cache.shape[-4:]
+    dtype = k_cache.dtype
+    good = (len(front) < 2 and k_cache.device.type == "cuda" and (dtype is torch.bfloat16 or dtype is torch.float16)
+            and k_cache.is_contiguous() and v_cache.dtype is dtype and v_cache.shape == front + (blocks, heads, dim, block)
+            and v_cache.is_contiguous() and v_cache.device == k_cache.device)
+    return (front[0] if front else 1, blocks, heads, block, dim) if good else None
+
+
+def _i32(dev, *arrays):
+    """True if all (tensor, shape) are contiguous int32 tensors on `dev`."""
+    import torch
+    for t, shape in arrays:
+        if not (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and t.device == dev):
+            return False
+    return True
+
+
+def _check_i32(dev, **arrays):
+    import torch
+    for name, (t, shape) in arrays.items():
+        _check_array(t, name, torch.int32, shape, dev)
+
+
+def _counts(counts, stream, dev):
+    import torch
+    return _made_on(stream, lambda: torch.empty(2, dtype=torch.int32, device=dev)) if counts is None else counts
+
+
+def dgt_page_keep(kept, ctx_lens, cu, slots, free_blocks, free_head, block_table, k_cache, v_cache, path=None,
+                  lens=None, counts=None, stream=None):
+    """After a step (its cu and slots: dgt_page_plan): the first kept[b] rows of each request's path
+    (dgt_verify; None: of its new rows) stay.  Their keys and values move behind the cached tokens, in
+    all layers of k_cache and v_cache ([layers, blocks, ...], or one layer's [blocks, ...]); `lens`
+    (default: ctx_lens, in place) gets the new lengths; pages past them go back into free_blocks, in
+    front of its head.  Returns counts int32[2]: the list's new head, the pages that went back."""
+    out = ctx_lens if lens is None else lens
+    try:
+        dev = k_cache.device
+        (requests,), (tokens,), (free,), width = kept.shape, slots.shape, free_blocks.shape, block_table.shape[1]
+        sizes = _fast_layers(k_cache, v_cache)
+        good = sizes and _i32(dev, (kept, (requests,)), (ctx_lens, (requests,)), (cu, (requests + 1,)),
+                              (slots, (tokens,)), (free_blocks, (free,)), (free_head, (1,)),
+                              (block_table, (requests, width)), (out, (requests,)))
+        if path is not None:
+            good = good and _i32(dev, (path, (tokens,)))
+        if counts is not None:
+            good = good and _i32(dev, (counts, (2,)))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        good = False
+    if not good:
+        _layers(k_cache, v_cache)
+        dev = k_cache.device
+        (requests,), (tokens,) = _dims(kept, "kept", 1), _dims(slots, "slots", 1)
+        (free,), width = _dims(free_blocks, "free_blocks", 1), _dims(block_table, "block_table", 2)[1]
+        _check_i32(dev, kept=(kept, (requests,)), ctx_lens=(ctx_lens, (requests,)), cu=(cu, (requests + 1,)),
+                   slots=(slots, (tokens,)), free_blocks=(free_blocks, (free,)), free_head=(free_head, (1,)),
+                   block_table=(block_table, (requests, width)), lens=(out, (requests,)))
+        if path is not None:
+            _check_i32(dev, path=(path, (tokens,)))
+        if counts is not None:
+            _check_i32(dev, counts=(counts, (2,)))
+        _check_gpu(dev)
+    layers, blocks, heads, block, dim = sizes
+    counts = _counts(counts, stream, dev)
+    _call("dgt_page_keep", dev, stream, None if path is None else path.data_ptr(), kept.data_ptr(),
+          ctx_lens.data_ptr(), cu.data_ptr(), slots.data_ptr(), requests, tokens, free_blocks.data_ptr(), free,
+          free_head.data_ptr(), block_table.data_ptr(), width, layers, heads, dim, blocks, block,
+          k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), counts.data_ptr())
+    return counts
+
+
+def dgt_page_fork(src, dst, lens, free_blocks, free_head, block_table, shares, k_cache, v_cache, counts=None,
+                  stream=None):
+    """Rows dst[i] of block_table (empty: length 0) become requests that hold what rows src[i] hold: full
+    pages are shared (shares int32[blocks] counts the holders besides the first), the last page, if not
+    full, is copied into one of the free list, in all layers of k_cache and v_cache ([layers, blocks, ...]
+    or [blocks, ...]).  lens[dst[i]] becomes lens[src[i]].  Returns counts int32[2]: the list's new head,
+    the forks that were refused."""
+    try:
+        dev = k_cache.device
+        (forks,), (free,), (requests, width) = src.shape, free_blocks.shape, block_table.shape
+        sizes = _fast_layers(k_cache, v_cache)
+        good = sizes and _i32(dev, (src, (forks,)), (dst, (forks,)), (lens, (requests,)), (free_blocks, (free,)),
+                              (free_head, (1,)), (block_table, (requests, width)), (shares, (sizes[1],)))
+        if counts is not None:
+            good = good and _i32(dev, (counts, (2,)))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        good = False
+    if not good:
+        blocks = _layers(k_cache, v_cache)[1]
+        dev = k_cache.device
+        (forks,), (free,) = _dims(src, "src", 1), _dims(free_blocks, "free_blocks", 1)
+        requests, width = _dims(block_table, "block_table", 2)
+        _check_i32(dev, src=(src, (forks,)), dst=(dst, (forks,)), lens=(lens, (requests,)),
+                   free_blocks=(free_blocks, (free,)), free_head=(free_head, (1,)),
+                   block_table=(block_table, (requests, width)), shares=(shares, (blocks,)))
+        if counts is not None:
+            _check_i32(dev, counts=(counts, (2,)))
+        _check_gpu(dev)
+    layers, blocks, heads, block, dim = sizes
+    counts = _counts(counts, stream, dev)
+    _call("dgt_page_fork", dev, stream, src.data_ptr(), dst.data_ptr(), forks, lens.data_ptr(), block_table.data_ptr(),
+          requests, width, free_blocks.data_ptr(), free, free_head.data_ptr(), shares.data_ptr(), layers, heads, dim,
+          blocks, block, k_cache.data_ptr(), v_cache.data_ptr(), counts.data_ptr())
+    return counts
+
+
+def dgt_page_free_workspace(blocks) -> int:
+    return lib().dgt_page_free_workspace(blocks)
+
+
+def dgt_page_free(rows, lens, free_blocks, free_head, block_table, shares, block_size, counts=None, ws=None,
+                  stream=None):
+    """The requests in `rows` (int32, rows of block_table) end: their pages lose a holder, and those that
+    no other request holds (shares) go back into free_blocks, in front of its head; their lengths become 0.
+    ws: a workspace to keep between calls (alloc_workspace); without one each call makes its own.  Returns
+    counts int32[2]: the list's new head, the pages that went back."""
+    import torch
+    try:
+        dev = block_table.device
+        (count,), (free,), (requests, width), (blocks,) = rows.shape, free_blocks.shape, block_table.shape, shares.shape
+        good = dev.type == "cuda" and _i32(dev, (rows, (count,)), (lens, (requests,)), (free_blocks, (free,)),
+                                           (free_head, (1,)), (block_table, (requests, width)), (shares, (blocks,)))
+        if counts is not None:
+            good = good and _i32(dev, (counts, (2,)))
+        if ws is not None:
+            good = good and ws.dtype is torch.uint8 and ws.dim() == 1 and ws.is_contiguous() and ws.device == dev
+    except (AttributeError, ValueError, IndexError, TypeError):
+        good = False
+    if not good:
+        requests, width = _dims(block_table, "block_table", 2)
+        dev = block_table.device
+        (count,), (free,), (blocks,) = _dims(rows, "rows", 1), _dims(free_blocks, "free_blocks", 1), _dims(shares, "shares", 1)
+        _check_i32(dev, rows=(rows, (count,)), lens=(lens, (requests,)), free_blocks=(free_blocks, (free,)),
+                   free_head=(free_head, (1,)), block_table=(block_table, (requests, width)), shares=(shares, (blocks,)))
+        if counts is not None:
+            _check_i32(dev, counts=(counts, (2,)))
+        if ws is not None:
+            _check_array(ws, "ws", torch.uint8, (None,), dev)
+        _check_gpu(dev)
+    counts = _counts(counts, stream, dev)
+    if ws is None:
+        ws = _made_on(stream, lambda: torch.zeros(dgt_page_free_workspace(blocks), dtype=torch.uint8, device=dev))
+    _call("dgt_page_free", dev, stream, rows.data_ptr(), count, lens.data_ptr(), block_table.data_ptr(), requests,
+          width, free_blocks.data_ptr(), free, free_head.data_ptr(), shares.data_ptr(), blocks, block_size,
+          counts.data_ptr(), ws.data_ptr(), ws.numel())
+    return counts

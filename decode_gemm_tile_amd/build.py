@@ -23,7 +23,8 @@ HIP_FLAGS = [
     "-Wno-unused-result",
 ]
 # sources of one object each: the decode-GEMM entry points and the serving operators
-SOURCES = ("dgt_api", "dgt_pages", "dgt_tree_attn", "dgt_lora")
+SOURCES = ("dgt_api", "dgt_pages", "dgt_tree_attn", "dgt_lora", "dgt_rope", "dgt_verify", "dgt_moves",
+           "dgt_chunk_attn")
 FORMATS = {"int8": 1, "int4": 2, "fp8": 3, "bf16": 4, "int4p": 5, "bf16e": 6, "bf16p": 7,
            "bf16w": 8}
 

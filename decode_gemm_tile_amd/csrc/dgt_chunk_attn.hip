@@ -1,0 +1,740 @@
+// Attention of a chunk of new tokens over a paged cache.
+#include "dgt_serve.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace dgt {
+namespace serve {
+namespace {
+
+// o_i = sum_j p_ij v_j / sum_j p_ij, p_ij = exp(s q_i k_j - max), over the keys j <= ctx + i.
+//
+// Rows of a request and key head are (token, query head of the group); a tile is as many
+// whole tokens as fit kRows of them.  A workgroup runs over the keys of a tile, up to the
+// last one that its last token sees, 64 at a time: tiles of keys and values are shared in
+// LDS by four waves of 32 RT rows each.  S^T = K Q^T puts keys down and rows across the lanes;
+// keys are dealt to the first operand so that a lane's scores are 8 consecutive keys of
+// one row, the second operand of O^T = V^T P^T as it stands.
+//
+// Work is dealt in items: a piece of a tile's keys.  Whole tiles where there are enough of
+// them; long tiles are cut where the card would be partly idle (k_chunk_plan weighs it),
+// and k_chunk_join adds up their parts in the order of the keys.  Workgroups draw items
+// from one queue a die, longest first; heads go round the dies, so a die's cache holds
+// the keys of its heads.
+struct ChunkArgs {
+  const uint16_t *q, *kc, *vc;
+  const int32_t *table, *ctx, *cu;
+  uint16_t* out;
+  uint32_t* plan;   // of the call, see Plan
+  float* parts;
+  uint64_t q_row, q_head, out_row, out_head;  // element strides
+  uint32_t requests, tokens, heads, group, dim, log_block, width, blocks;
+  uint32_t tile_tokens, splits;  // tokens of a tile; tiles a token's heads take (one of the two is 1)
+  float scale;                   // times log2(e)
+};
+
+constexpr uint32_t kWaves = 4, kKeys = 64, kDies = 8;
+constexpr uint32_t kMostParts = 1024;  // of all tiles together
+
+// What k_chunk_plan leaves in the workspace, in words.
+struct Plan {
+  static constexpr uint32_t kQueue = 0;        // a counter a die, 64 bytes apart
+  static constexpr uint32_t kPiece = 128;      // keys of a piece, a multiple of kKeys
+  static constexpr uint32_t kItems = 129;      // in all
+  static constexpr uint32_t kCut = 130;        // items among which those of cut tiles are
+  static constexpr uint32_t kOrder = 160;      // [requests]: request number, longest first
+  static __host__ __device__ constexpr uint32_t item0(uint32_t requests) { return kOrder + requests; }  // [requests], first item
+  static __host__ __device__ constexpr uint32_t part0(uint32_t requests) { return kOrder + 2 * requests; }  // [requests], first part
+  static __host__ __device__ constexpr uint32_t words(uint32_t requests) { return kOrder + 3 * requests; }
+};
+
+struct Chunk {  // one request
+  uint32_t first, count, ctx, keys, tiles;
+};
+
+__device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, uint32_t b) {
+  Chunk c;
+  request_rows(a.cu, b, a.tokens, &c.first, &c.count);
+  const uint32_t room = a.width << a.log_block;
+  c.ctx = min((uint32_t)max(a.ctx[b], 0), room);
+  c.keys = min(c.ctx + c.count, room);
+  c.tiles = (c.count + a.tile_tokens - 1) / a.tile_tokens * a.splits;
+  return c;
+}
+
+template <int THREADS>
+__device__ __forceinline__ float sum_all(float v, float* s) {
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
+  __syncthreads();
+  if (lane == 0) s[wave] = v;
+  __syncthreads();
+  float all = 0.f;
+  for (int w = 0; w < THREADS / 64; ++w) all += s[w];
+  return all;
+}
+
+// One workgroup: how long pieces are, and the requests' items.  In units of a tile of 64
+// keys, a call takes about its work over the CUs and a last piece; or one piece where no
+// CU gets two; and a part written and read again costs as much as kPart of them.
+constexpr uint32_t kPlanThreads = 256, kMaxSorted = 1024;
+constexpr float kPart = 6.f;
+
+__global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
+  extern __shared__ uint32_t s_keys[];  // [requests], then [requests] sorted
+  __shared__ float s_sum[kPlanThreads / 64];
+  __shared__ uint32_t s_scan[kPlanThreads / 64];
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  float work = 0.f, rows = 0.f;
+  uint32_t most = 0;
+  for (uint32_t b = t; b < a.requests; b += kPlanThreads) {
+    const Chunk c = chunk_of(a, b);
+    s_keys[b] = c.tiles ? c.keys : 0;
+    // (their mean length: the first tiles see half of the new tokens less)
+    work += (float)c.tiles * ((float)(c.keys + min(c.ctx, c.keys)) * (0.5f / kKeys) + 1.f);
+    rows += (float)c.count;
+    most = max(most, s_keys[b]);
+  }
+  work = sum_all<kPlanThreads>(work, s_sum) * (float)a.heads;
+  // Offsets that fall name rows again and again, and no bound on items holds: such a batch
+  // is not computed.  (Sums up to 2^24 are exact, and `tokens` is 2^20 at most.)
+  const bool sound = sum_all<kPlanThreads>(rows, s_sum) <= (float)a.tokens;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, m, 64));
+  __syncthreads();
+  if (lane == 0) s_scan[wave] = most;
+  __syncthreads();
+  for (uint32_t w = 0; w < kPlanThreads / 64; ++w) most = max(most, s_scan[w]);
+  const float longest = ceilf((float)most / kKeys);
+  float best = 3.4e38f;
+  uint32_t piece = max((most + kKeys - 1) / kKeys, 1u);
+  for (uint32_t k = 1; k <= 64; k += k < 4 ? 1 : k / 4) {
+    const uint32_t len = max((uint32_t)ceilf(longest / (float)k), 2u);
+    float items = 0.f, parts = 0.f;
+    for (uint32_t b = t; b < a.requests; b += kPlanThreads) {
+      const Chunk c = chunk_of(a, b);
+      const uint32_t n = (c.keys + len * kKeys - 1) / (len * kKeys);
+      items += (float)c.tiles * (float)max(n, 1u);
+      if (n > 1) parts += (float)c.tiles * (float)n;
+    }
+    items = sum_all<kPlanThreads>(items, s_sum) * (float)a.heads;
+    parts = sum_all<kPlanThreads>(parts, s_sum) * (float)a.heads;
+    if (parts > (float)kMostParts) break;
+    const float share = parts * (kPart / kCUs);
+    const float time = (items <= (float)kCUs ? (float)len : work / kCUs + (float)len) + (parts > 0.f ? kPart + share : 0.f);
+    if (time < best) {
+      best = time;
+      piece = len;
+    }
+  }
+  piece *= kKeys;
+
+  // requests by their longest tile, descending (of equals, the first first)
+  uint32_t* s_order = s_keys + a.requests;
+  __syncthreads();
+  for (uint32_t b = t; b < a.requests; b += kPlanThreads) {
+    uint32_t rank = b;
+    if (a.requests <= kMaxSorted) {
+      rank = 0;
+      const uint32_t mine = s_keys[b];
+      for (uint32_t o = 0; o < a.requests; ++o) rank += s_keys[o] > mine || (s_keys[o] == mine && o < b);
+    }
+    s_order[rank] = b;
+  }
+  __syncthreads();
+  uint32_t items = 0, parts = 0;
+  for (uint32_t i0 = 0; i0 < a.requests; i0 += kPlanThreads) {
+    const uint32_t i = i0 + t;
+    uint32_t n = 0, p = 0;
+    if (i < a.requests) {
+      const Chunk c = chunk_of(a, s_order[i]);
+      const uint32_t pieces = max((c.keys + piece - 1) / piece, 1u);
+      n = c.tiles * pieces * a.heads;
+      p = pieces > 1 ? n : 0;
+    }
+    // exclusive sums of both
+    uint32_t sn = n, sp = p;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t on = __shfl_up(sn, d, 64), op = __shfl_up(sp, d, 64);
+      if (lane >= (uint32_t)d) {
+        sn += on;
+        sp += op;
+      }
+    }
+    __syncthreads();
+    if (lane == 63) {
+      s_scan[wave] = sn;
+      s_sum[wave] = __uint_as_float(sp);
+    }
+    __syncthreads();
+    uint32_t bn = items, bp = parts;
+    for (uint32_t w = 0; w < kPlanThreads / 64; ++w) {
+      if (w == wave) {
+        sn += bn;
+        sp += bp;
+      }
+      bn += s_scan[w];
+      bp += __float_as_uint(s_sum[w]);
+    }
+    if (i < a.requests) {
+      a.plan[Plan::kOrder + i] = s_order[i];
+      a.plan[Plan::item0(a.requests) + i] = sn - n;
+      a.plan[Plan::part0(a.requests) + i] = sp - p;
+    }
+    items = bn;
+    parts = bp;
+  }
+  if (t < kDies) a.plan[Plan::kQueue + 16 * t] = 0;
+  if (t == 0) {
+    a.plan[Plan::kPiece] = piece;
+    a.plan[Plan::kItems] = sound ? items : 0;
+    // cut tiles come first where requests are sorted
+    a.plan[Plan::kCut] = !sound || parts == 0 ? 0 : a.requests <= kMaxSorted ? parts : items;
+  }
+}
+
+struct Item {
+  Chunk c;
+  uint32_t b, head, tile, piece, pieces;
+  uint32_t token, tokens, member, members;  // its tokens, and the heads of the group that it holds
+  uint32_t keys, k0, k1;                    // that its last token sees; of the piece
+  uint32_t part;                            // where its part goes, if keys > piece
+  __device__ __forceinline__ uint32_t rows() const { return tokens * members; }
+};
+
+// Item x of the call.  Of a request: tiles from the last, which sees most, pieces, heads.
+__device__ __forceinline__ Item item_of(const ChunkArgs& a, uint32_t x, uint32_t piece, uint32_t rows) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t* item0 = a.plan + Plan::item0(a.requests);
+  uint32_t lo = 0, len = a.requests;
+  while (len > 1) {
+    const uint32_t step = (len + 63) / 64, at = lane * step;
+    const bool before = lane == 0 || (at < len && item0[lo + at] <= x);
+    const uint32_t hits = (uint32_t)__popcll(__ballot(before));
+    const uint32_t skip = (hits - 1) * step;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  Item it;
+  it.b = a.plan[Plan::kOrder + lo];
+  it.c = chunk_of(a, it.b);
+  it.pieces = max((it.c.keys + piece - 1) / piece, 1u);
+  const uint32_t in = x - item0[lo], rest = in / a.heads;
+  it.head = in - rest * a.heads;
+  it.piece = rest % it.pieces;
+  it.tile = it.c.tiles - 1 - rest / it.pieces;
+  it.part = a.plan[Plan::part0(a.requests) + lo] + in;
+  const uint32_t split = it.tile % a.splits;
+  it.token = it.tile / a.splits * a.tile_tokens;
+  it.tokens = min(it.c.count - it.token, a.tile_tokens);
+  it.member = split * rows;
+  it.members = min(a.group - it.member, rows);
+  it.keys = min(it.c.ctx + it.token + it.tokens, it.c.keys);
+  it.k0 = it.piece * piece;
+  it.k1 = min(it.keys, it.k0 + piece);
+  return it;
+}
+
+// A tile of keys and values in LDS, in 16-byte pieces, permuted so that 16 neighbouring
+// rows of an operand read lie on different banks.
+template <int DP>
+struct Tile {
+  static constexpr uint32_t kKPieces = DP / 8, kVPieces = kKeys / 8;  // of a row
+  static constexpr uint32_t kPieces = kKeys * kKPieces;               // keys or values
+  static constexpr uint32_t kEach = kPieces / 256;                    // a thread
+  static constexpr uint32_t kBytes = 2 * 2 * kPieces * 16;
+  static __device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t piece) {
+    return row * kKPieces + (piece ^ (kKPieces >= 16 ? row & 15 : (row >> 1) & 7));
+  }
+  static __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
+    return row * kVPieces + (piece ^ ((row >> 1) & 7));
+  }
+};
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+
+template <class E>
+__device__ __forceinline__ floatx16 mfma32(u32x4 a, u32x4 b, floatx16 c);
+template <>
+__device__ __forceinline__ floatx16 mfma32<Bf16>(u32x4 a, u32x4 b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ floatx16 mfma32<F16>(u32x4 a, u32x4 b, floatx16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Maximum and sum over the two lanes that hold one row.
+__device__ __forceinline__ float half_max(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// Weights are 2^(score * scale - ref) against a reference that follows the row's maximum at
+// a distance of at most 2^kSlack, so that outputs are rarely multiplied: fp32 sums and
+// 16-bit weights up to 2^kSlack lose nothing by it.
+constexpr float kSlack = 8.f;
+
+template <int DP, int RT>
+struct PartOf {  // ref[rows], l[rows], then the outputs in the order of the lanes that hold them
+  static constexpr uint32_t kRows = kWaves * 32 * RT;
+  static constexpr uint32_t kFloats = kRows * (DP + 2);
+};
+
+template <class E, int DP, int RT, bool PAD>
+__global__ __launch_bounds__(256, 1) void k_chunk_attention(ChunkArgs a) {
+  using T = Tile<DP>;
+  using P = PartOf<DP, RT>;
+  constexpr int KS = DP / 16, DT = DP / 32;
+  extern __shared__ u32x4 lds[];
+  u32x4* s_k = lds;                   // [2][kPieces]
+  u32x4* s_v = lds + 2 * T::kPieces;  // [2][kPieces]
+  __shared__ uint32_t s_item;
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const uint32_t half = lane >> 5, l32 = lane & 31;
+  const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
+  const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
+  const uint32_t page_bytes = (uint32_t)(2 * page_len) * a.heads;
+  const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kItems];
+
+  // Pieces of a page's value row that lie in one tile, as a power of two.  Piece x of a tile
+  // of values in the order of memory: page by page, value row by row.
+  const uint32_t log_vp = min(a.log_block, 6u) - 3;
+  const uint32_t log_part = log_vp + (uint32_t)__builtin_ctz(DP);
+  const uint32_t k_lane = 2 * ((lane / T::kKPieces) * dim + 8 * (lane % T::kKPieces));
+  const uint32_t v_lane = 2 * (((lane >> log_vp) << a.log_block) + 8 * (lane & ((1u << log_vp) - 1)));
+
+  uint32_t queue = blockIdx.x % kDies, tried = 0;
+  for (;;) {
+    if (t == 0) {
+      uint32_t x = ~0u;
+      for (; tried < kDies; ++tried, queue = (queue + 1) % kDies) {
+        const uint32_t n = __hip_atomic_fetch_add(a.plan + Plan::kQueue + 16 * queue, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (n < (items + kDies - 1 - queue) / kDies) {
+          x = n * kDies + queue;
+          break;
+        }
+      }
+      s_item = x;
+    }
+    __syncthreads();
+    const uint32_t x = __builtin_amdgcn_readfirstlane(s_item);
+    __syncthreads();
+    if (x == ~0u) break;
+    const Item it = item_of(a, x, piece, P::kRows);
+    // (a piece past the tile's keys; a tile of no keys at all still has rows to write)
+    if (it.k0 >= it.k1 && it.piece) continue;
+
+    const uint32_t row_w = wave * 32 * RT;  // the wave's first row
+    const uint32_t live = it.rows();
+    const bool works = row_w < live;
+    u32x4 q[RT][KS];
+    uint32_t sees[RT];  // keys that a row sees
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const uint32_t r = min(row_w + 32 * i + l32, live - 1), tok = it.token + r / it.members;
+      sees[i] = min(it.c.ctx + tok + 1, it.c.keys);
+      const uint16_t* p = a.q + (uint64_t)(it.c.first + tok) * a.q_row +
+                          (uint64_t)(it.head * a.group + it.member + r % it.members) * a.q_head;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const uint32_t d = 16 * s + 8 * half;
+        q[i][s] = (!PAD || d < dim) ? *reinterpret_cast<const u32x4*>(p + d) : u32x4{};
+      }
+    }
+    const uint32_t all_see = min(it.c.ctx + it.token + 1, it.c.keys);  // keys that every row sees
+    floatx16 o[RT][DT];
+    float ref[RT], l[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      ref[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[i][d] = floatx16{};
+    }
+
+    const int32_t* pages = a.table + (uint64_t)it.b * a.width;
+    const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.kc + it.head * page_len);
+    const uint8_t* values = reinterpret_cast<const uint8_t*>(a.vc + it.head * page_len);
+    // Pages of a tile's groups of 8 keys, one a lane (repeating), ~0 where the group does not
+    // exist; `absent` has a bit for each such group.
+    auto tile_pages = [&](uint32_t kb) {
+      const uint32_t key = kb + 8 * (lane % 8);
+      const uint32_t page = key < it.k1 ? (uint32_t)pages[key >> a.log_block] : ~0u;
+      return page < a.blocks ? page : ~0u;
+    };
+    u32x4 rk[T::kEach], rv[T::kEach];
+    uint32_t absent = 0, coming = tile_pages(it.k0);
+    // A wave's pieces of one load lie in one page, so the page is a scalar; where a group
+    // does not exist, page 0 is read instead.
+    auto load = [&](uint32_t kb) {
+      absent = (uint32_t)__ballot(coming == ~0u) & 0xFFu;
+      const uint32_t pages_now = coming == ~0u ? 0u : coming;
+      coming = tile_pages(kb + kKeys);
+      const uint32_t inside = kb & in_page;  // where the tile begins in a page longer than it
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) {
+        const uint32_t row = (64 * wave + 256 * j) / T::kKPieces;
+        const uint8_t* from = keys + (uint64_t)__builtin_amdgcn_readlane(pages_now, row / 8) * page_bytes;
+        const uint32_t at = (inside + (row & in_page)) * (2 * dim) + k_lane;
+        rk[j] = !PAD || 8 * (t % T::kKPieces) < dim ? *reinterpret_cast<const u32x4*>(from + at) : u32x4{};
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) {
+        const uint32_t x_w = 64 * wave + 256 * j, part = x_w >> log_part;
+        const uint32_t y_w = x_w & ((1u << log_part) - 1);  // the wave's first piece within the part
+        const uint8_t* from = values + (uint64_t)__builtin_amdgcn_readlane(pages_now, part << log_vp) * page_bytes;
+        const uint32_t at = 2 * (((y_w >> log_vp) << a.log_block) + inside) + v_lane;
+        rv[j] = !PAD || (y_w + lane) >> log_vp < dim ? *reinterpret_cast<const u32x4*>(from + at) : u32x4{};
+      }
+    };
+    // Values of keys that do not exist become zero, and one that is not finite is noted
+    // where some row does not see it: a weight of zero times it is not zero.
+    bool odd = false;
+    auto store = [&](uint32_t kb, uint32_t buf) {
+      const bool edge = kb + kKeys > all_see || absent;
+      odd = false;
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) {
+        const uint32_t x = t + 256 * j;
+        s_k[buf * T::kPieces + T::k_at(x / T::kKPieces, x % T::kKPieces)] = rk[j];
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) {
+        const uint32_t x = t + 256 * j, row = (x & ((DP << log_vp) - 1)) >> log_vp;
+        const uint32_t p = (x >> log_part << log_vp) + (x & ((1u << log_vp) - 1));
+        if (edge) {
+          const uint32_t key = kb + 8 * p;
+          const uint32_t real = (absent >> p) & 1 || key >= it.k1 ? 0u : min(it.k1 - key, 8u);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t v = rv[j][w];
+            v = real <= 2u * w ? 0u : real == 2u * w + 1 ? v & 0xFFFFu : v;
+            rv[j][w] = v;
+            odd |= !E::finite2(v);
+          }
+        }
+        s_v[buf * T::kPieces + T::v_at(row, p)] = rv[j];
+      }
+      if (edge) odd = __syncthreads_or(odd);
+      else __syncthreads();
+    };
+
+    if (it.k0 < it.k1) {
+      load(it.k0);
+      store(it.k0, 0);
+    }
+    uint32_t buf = 0;
+    for (uint32_t kb = it.k0; kb < it.k1; kb += kKeys, buf ^= 1) {
+      const bool more = kb + kKeys < it.k1, odd_now = odd;
+      const uint32_t absent_now = absent;
+      if (more) load(kb + kKeys);
+      if (works) {
+        const u32x4* bk = s_k + buf * T::kPieces;
+        const u32x4* bv = s_v + buf * T::kPieces;
+        floatx16 s[RT][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // row of the operand to key: bits 2 and 3 change places
+          const uint32_t key = 32 * h + ((l32 & 19) | ((l32 & 4) << 1) | ((l32 & 8) >> 1));
+#pragma unroll
+          for (int i = 0; i < RT; ++i) s[i][h] = floatx16{};
+#pragma unroll
+          for (int x = 0; x < KS; ++x) {
+            const u32x4 kf = bk[T::k_at(key, 2 * x + half)];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) s[i][h] = mfma32<E>(kf, q[i][x], s[i][h]);
+          }
+        }
+        // a lane's scores: keys kb + 32 h + 16 g + 8 half + e are element 8 g + e
+        if (kb + kKeys > all_see || absent_now) {
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t key = kb + 16 * g + 8 * half;
+              const uint32_t n = (absent_now >> (2 * g + half)) & 1 || key >= sees[i] ? 0u : min(sees[i] - key, 8u);
+#pragma unroll
+              for (uint32_t e = 0; e < 8; ++e)
+                if (e >= n) s[i][g >> 1][8 * (g & 1) + e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          float top = s[i][0][0];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(top, s[i][h][e]), s[i][h][e + 1]);
+          top = half_max(top) * a.scale;
+          if (__any(top > ref[i] + kSlack)) {
+            const float now = fmaxf(ref[i], top);
+            const float keep = ref[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[i] - now);
+            ref[i] = now;
+            l[i] *= keep;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[i][d] *= keep;
+          }
+          const float base = ref[i] == -INFINITY ? 0.f : ref[i];  // nothing seen: the weights are 2^-inf = 0
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[i][h][e] = __builtin_amdgcn_exp2f(fmaf(s[i][h][e], a.scale, -base));
+        }
+        if (!odd_now) {
+          u32x4 p[RT][4];
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                p[i][g][w] = E::pack2(s[i][g >> 1][8 * (g & 1) + 2 * w], s[i][g >> 1][8 * (g & 1) + 2 * w + 1]);
+                l[i] = E::add2(p[i][g][w], l[i]);
+              }
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              const u32x4 vf = bv[T::v_at(32 * d + l32, 2 * g + half)];
+#pragma unroll
+              for (int i = 0; i < RT; ++i) o[i][d] = mfma32<E>(vf, p[i][g], o[i][d]);
+            }
+        } else {
+          // key by key, leaving out those of weight zero
+          const uint16_t* value = reinterpret_cast<const uint16_t*>(bv);
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) l[i] += s[i][h][e];
+#pragma unroll 1
+          for (uint32_t x = 0; x < kKeys; ++x) {
+            uint32_t h_now = half;
+            keep_here(h_now);
+            float p[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              p[i] = 0.f;
+#pragma unroll
+              for (uint32_t e = 0; e < 32; ++e) p[i] = (x >> 4) * 8 + (x & 7) == e ? s[i][e >> 4][e & 15] : p[i];
+              p[i] = __shfl(p[i], ((x >> 3) & 1) * 32 + l32, 64);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float v = E::up(value[T::v_at(32 * d + (e & 3) + 4 * h_now + 8 * (e >> 2), x >> 3) * 8 + (x & 7)]);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                  if (p[i] != 0.f) o[i][d][e] = fmaf(p[i], v, o[i][d][e]);
+              }
+          }
+        }
+      }
+      if (more) store(kb + kKeys, buf ^ 1);
+    }
+
+    const bool whole = it.keys <= piece;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      l[i] = half_sum(l[i]);
+      const uint32_t r = row_w + 32 * i + l32;
+      if (r >= live) continue;
+      if (whole) {
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const uint32_t tok = it.token + r / it.members;
+        uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
+                      (uint64_t)(it.head * a.group + it.member + r % it.members) * a.out_head;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t at = 32 * d + 8 * g + 4 * half;
+            if (!PAD || at < dim) {
+              *reinterpret_cast<uint32_t*>(p + at) = E::pack2(o[i][d][4 * g] * inv, o[i][d][4 * g + 1] * inv);
+              *reinterpret_cast<uint32_t*>(p + at + 2) = E::pack2(o[i][d][4 * g + 2] * inv, o[i][d][4 * g + 3] * inv);
+            }
+          }
+      } else {
+        float* part = a.parts + (uint64_t)it.part * P::kFloats;
+        if (half == 0) {
+          part[r] = ref[i];
+          part[P::kRows + r] = l[i];
+        }
+        float* to = part + 2 * P::kRows + r * DP;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<floatx4*>(to + 32 * d + 8 * g + 4 * half) =
+                floatx4{o[i][d][4 * g], o[i][d][4 * g + 1], o[i][d][4 * g + 2], o[i][d][4 * g + 3]};
+      }
+    }
+    __syncthreads();  // the buffers are refilled
+  }
+}
+
+// Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes
+// some rows of a tile, a thread four outputs of a row.
+template <class E, int DP, int RT>
+__global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
+  using P = PartOf<DP, RT>;
+  constexpr uint32_t kFours = DP / 4, kRowsEach = 256 / kFours, kSteps = P::kRows / kRowsEach;
+  const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kCut], t = threadIdx.x;
+  for (uint64_t unit = blockIdx.x; unit < (uint64_t)items * kSteps; unit += gridDim.x) {
+    const Item it = item_of(a, (uint32_t)(unit / kSteps), piece, P::kRows);
+    if (it.piece || it.keys <= piece) continue;
+    const uint32_t r = (uint32_t)(unit % kSteps) * kRowsEach + t / kFours, d = 4 * (t % kFours);
+    if (r >= it.rows()) continue;
+    float m = -INFINITY, l = 0.f;
+    floatx4 o = {};
+    // item numbers of a tile's pieces lie `heads` apart
+    const float* part = a.parts + (uint64_t)it.part * P::kFloats;
+    for (uint32_t k = 0; k < it.keys; k += piece, part += (uint64_t)a.heads * P::kFloats) {
+      const float mw = part[r], lw = part[P::kRows + r];
+      const floatx4 ow = *reinterpret_cast<const floatx4*>(part + 2 * P::kRows + r * DP + d);
+      const float now = fmaxf(m, mw), base = now == -INFINITY ? 0.f : now;
+      const float f = __builtin_amdgcn_exp2f(m - base), fw = __builtin_amdgcn_exp2f(mw - base);
+      m = now;
+      l = fmaf(lw, fw, l * f);
+      o = o * f + ow * fw;
+    }
+    if (d >= a.dim) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const uint32_t tok = it.token + r / it.members;
+    uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
+                  (uint64_t)(it.head * a.group + it.member + r % it.members) * a.out_head + d;
+    *reinterpret_cast<uint32_t*>(p) = E::pack2(o[0] * inv, o[1] * inv);
+    *reinterpret_cast<uint32_t*>(p + 2) = E::pack2(o[2] * inv, o[3] * inv);
+  }
+}
+
+struct ChunkPlan {
+  uint32_t dp, rows, tile_tokens, splits;
+  size_t part_off, ws_bytes;
+};
+
+ChunkPlan plan_chunk(uint32_t heads, uint32_t kv_heads, uint32_t dim, uint32_t requests) {
+  ChunkPlan p;
+  p.dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
+  p.rows = p.dp == 256 ? 128 : 256;
+  const uint32_t group = heads / kv_heads;
+  p.tile_tokens = std::max(p.rows / group, 1u);
+  p.splits = (group + p.rows - 1) / p.rows;
+  p.part_off = ((size_t)Plan::words(requests) * 4 + 255) / 256 * 256;
+  p.ws_bytes = p.part_off + (size_t)kMostParts * p.rows * (p.dp + 2) * 4;
+  return p;
+}
+
+bool chunk_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim, uint32_t requests) {
+  return heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0 && heads <= 65536 && dim >= 8 &&
+         dim <= 256 && dim % 8 == 0 && requests <= kMaxRequests && tokens <= (1u << 20) &&
+         (uint64_t)tokens * heads <= (1u << 30);
+}
+
+template <class E, int DP, int RT, bool PAD>
+int launch_chunk(const ChunkArgs& a, hipStream_t st) {
+  const auto kernel = k_chunk_attention<E, DP, RT, PAD>;
+  if (Tile<DP>::kBytes > 64 * 1024 &&
+      hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                          (int)Tile<DP>::kBytes) != hipSuccess)
+    return DGT_E_HIP;
+  hipLaunchKernelGGL(kernel, dim3(kCUs), dim3(256), Tile<DP>::kBytes, st, a);
+  if (int rc = launched()) return rc;
+  hipLaunchKernelGGL((k_chunk_join<E, DP, RT>), dim3(4 * kCUs), dim3(256), 0, st, a);
+  return launched();
+}
+
+template <class E>
+int launch_chunk(const ChunkArgs& a, uint32_t dp, hipStream_t st) {
+  const uint32_t lds = 2 * a.requests * 4;  // 64 KB at most
+  if (lds > 63 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_chunk_plan),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+    return DGT_E_HIP;
+  hipLaunchKernelGGL(k_chunk_plan, dim3(1), dim3(kPlanThreads), lds, st, a);
+  if (int rc = launched()) return rc;
+  const bool pad = a.dim != dp;
+  switch (dp) {
+    case 64: return pad ? launch_chunk<E, 64, 2, true>(a, st) : launch_chunk<E, 64, 2, false>(a, st);
+    case 128: return pad ? launch_chunk<E, 128, 2, true>(a, st) : launch_chunk<E, 128, 2, false>(a, st);
+  }
+  return pad ? launch_chunk<E, 256, 1, true>(a, st) : launch_chunk<E, 256, 1, false>(a, st);
+}
+
+}  // namespace
+}  // namespace serve
+}  // namespace dgt
+
+using namespace dgt::serve;
+
+extern "C" {
+
+size_t dgt_chunk_attention_workspace(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                                     uint32_t requests) {
+  if (!chunk_shape_ok(tokens, heads, kv_heads, dim, requests)) return 0;
+  return plan_chunk(heads, kv_heads, dim, requests).ws_bytes;
+}
+
+int dgt_chunk_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t q_head,
+                        const void* d_k_cache, const void* d_v_cache, uint32_t blocks, uint32_t block,
+                        const int32_t* d_table, uint32_t width, const int32_t* d_ctx, const int32_t* d_cu,
+                        uint32_t requests, uint32_t tokens, uint32_t heads, uint32_t kv_heads,
+                        uint32_t dim, float scale, void* d_out, uint64_t out_row, uint64_t out_head,
+                        void* d_ws, size_t ws_bytes, void* stream) {
+  if (type != DGT_ELT_BF16 && type != DGT_ELT_F16) return DGT_E_UNSUPPORTED;
+  if (!chunk_shape_ok(tokens, heads, kv_heads, dim, requests) || !block_ok(block) ||
+      !pool_ok(blocks, block) || (uint64_t)width * block > 0x7FFFFFFFull)
+    return DGT_E_SHAPE;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return DGT_E_ARG;
+  if (tokens == 0 || requests == 0) return DGT_OK;
+  if (!d_q || !d_out || !d_cu || !d_ctx || !d_ws) return DGT_E_ARG;
+  if ((width && !d_table) || (blocks && (!d_k_cache || !d_v_cache))) return DGT_E_ARG;
+  if (tokens == 1) q_row = out_row = 0;  // one row, or one head, has no stride
+  if (heads == 1) q_head = out_head = 0;
+  if (!aligned(d_q, 16) || !aligned(d_k_cache, 16) || !aligned(d_v_cache, 16) || !aligned(d_out, 4) ||
+      !aligned(d_ws, 256) || q_row % 8 || q_head % 8 || out_row % 2 || out_head % 2)
+    return DGT_E_ARG;
+  // (a page's bytes are counted in 32 bits)
+  if (blocks == 0 || (uint64_t)kv_heads * block * dim * 2 >= (1ull << 32)) return DGT_E_SHAPE;
+  const ChunkPlan p = plan_chunk(heads, kv_heads, dim, requests);
+  if (ws_bytes < p.ws_bytes) return DGT_E_BUFSIZE;
+  ChunkArgs a;
+  a.q = static_cast<const uint16_t*>(d_q);
+  a.kc = static_cast<const uint16_t*>(d_k_cache);
+  a.vc = static_cast<const uint16_t*>(d_v_cache);
+  a.table = d_table;
+  a.ctx = d_ctx;
+  a.cu = d_cu;
+  a.out = static_cast<uint16_t*>(d_out);
+  a.plan = static_cast<uint32_t*>(d_ws);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + p.part_off);
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.out_row = out_row;
+  a.out_head = out_head;
+  a.requests = requests;
+  a.tokens = tokens;
+  a.heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.dim = dim;
+  a.log_block = (uint32_t)__builtin_ctz(block);
+  a.width = width;
+  a.blocks = blocks;
+  a.tile_tokens = p.tile_tokens;
+  a.splits = p.splits;
+  a.scale = scale * 1.4426950408889634f;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return type == DGT_ELT_BF16 ? launch_chunk<Bf16>(a, p.dp, st) : launch_chunk<F16>(a, p.dp, st);
+}
+
+}  // extern "C"

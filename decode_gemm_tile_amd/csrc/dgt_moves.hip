@@ -1,0 +1,507 @@
+// Pages after a step: what is kept of the drafts moves up and the rest goes back, requests
+// that share pages, requests that end.
+#include "dgt_serve.h"
+
+#include <algorithm>
+
+namespace dgt {
+namespace serve {
+namespace {
+
+struct Pool {  // caches of all layers, in 16-bit elements
+  uint16_t *kc, *vc;
+  uint32_t layers, heads, dim, log_block, blocks;
+  __device__ __forceinline__ uint64_t page(uint32_t layer, uint32_t id, uint32_t head) const {
+    return ((((uint64_t)layer * blocks + id) * heads + head) * dim) << log_block;
+  }
+  __device__ __forceinline__ uint32_t block() const { return 1u << log_block; }
+  __device__ __forceinline__ bool holds(uint32_t slot) const { return slot < blocks << log_block; }
+};
+
+// Exclusive sum over a workgroup's threads, in their order; s_sum holds one word a wave.
+template <int THREADS>
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* s_sum, uint32_t* total) {
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t scan = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(scan, d, 64);
+    if (lane >= (uint32_t)d) scan += o;
+  }
+  if (lane == 63) s_sum[wave] = scan;
+  __syncthreads();
+  uint32_t before = scan - v, all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) before += s_sum[w];
+    all += s_sum[w];
+  }
+  __syncthreads();  // s_sum is free again
+  *total = all;
+  return before;
+}
+
+// ----------------------------------------------------------------------- keep
+struct KeepArgs {
+  const int32_t *path, *kept, *ctx, *cu, *slots, *free_head;
+  int32_t *free_list, *table, *lens, *counts;
+  uint32_t requests, tokens, free_len, width, units;
+  Pool pool;
+};
+
+constexpr uint32_t kKeepRows = 16;    // tokens that a workgroup moves at a time
+
+// The first new token of a request that the plan refused has no slot.
+__device__ __forceinline__ uint32_t kept_of(const KeepArgs& a, uint32_t b, uint32_t first, uint32_t count) {
+  if (count == 0 || !a.pool.holds((uint32_t)a.slots[first])) return 0;
+  return min((uint32_t)max(a.kept[b], 0), count);
+}
+
+// Lengths, and the pages past them, by one workgroup: the list's order is the requests'.
+// A column past the kept tokens begins at or behind the cached ones' end, so a new token
+// lies first in it and its slot names the page.
+__device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
+  const uint32_t log = a.pool.log_block, round = a.pool.block() - 1;
+  const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
+  uint32_t total = 0;
+  // twice over the requests: how many pages, then which
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t done = 0;
+    for (uint32_t b0 = 0; b0 < a.requests; b0 += 256) {
+      const uint32_t b = b0 + threadIdx.x;
+      uint32_t first = 0, count = 0, ctx = 0, now = 0, from = 0, to = 0;
+      if (b < a.requests) {
+        request_rows(a.cu, b, a.tokens, &first, &count);
+        ctx = (uint32_t)max(a.ctx[b], 0);
+        const bool held = count && a.pool.holds((uint32_t)a.slots[first]);
+        const uint32_t kept = kept_of(a, b, first, count);
+        now = (uint32_t)min((uint64_t)ctx + kept, (uint64_t)0x7FFFFFFF);
+        from = min((uint32_t)(((uint64_t)now + round) >> log), a.width);
+        to = held ? min((uint32_t)(((uint64_t)ctx + count + round) >> log), a.width) : from;
+      }
+      auto page = [&](uint32_t c) {  // of column c
+        const uint32_t at = max(c << log, ctx) - ctx;
+        const uint32_t slot = at < count ? (uint32_t)a.slots[first + at] : ~0u;
+        return a.pool.holds(slot) ? slot >> log : ~0u;
+      };
+      uint32_t mine = 0;
+      for (uint32_t c = from; c < to; ++c) mine += page(c) != ~0u;
+      uint32_t all;
+      uint32_t at = done + sum_before<256>(mine, s_sum, &all);
+      done += all;
+      if (pass == 0) continue;
+      for (uint32_t c = from; c < to; ++c) {
+        const uint32_t id = page(c);
+        if (id == ~0u) continue;
+        // (there is room for all of them unless the list is not what they came from)
+        if (head + at >= total) a.free_list[head + at - total] = (int32_t)id;
+        a.table[(uint64_t)b * a.width + c] = -1;
+        ++at;
+      }
+      if (b < a.requests) a.lens[b] = (int32_t)now;
+    }
+    total = done;
+  }
+  if (threadIdx.x == 0) {
+    a.counts[0] = (int32_t)(head - min(total, head));
+    a.counts[1] = (int32_t)total;
+  }
+}
+
+// A workgroup moves the kept rows of one request, layer and head, 16 at a time: all of
+// them are read before any is written.  Index i_j >= j rises with j, so a row that a
+// later step reads lies behind every place that this one writes.  Slots are looked up
+// in the plan's list and not in the table, whose columns change at the same time.
+__device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint32_t* s_src, uint32_t* s_dst) {
+  const uint32_t t = threadIdx.x, dim = a.pool.dim, log = a.pool.log_block, in_page = a.pool.block() - 1;
+  const uint32_t per = a.pool.layers * a.pool.heads, b = unit / per, layer = unit % per / a.pool.heads;
+  const uint32_t head = unit % a.pool.heads;
+  uint32_t first, count;
+  request_rows(a.cu, b, a.tokens, &first, &count);
+  const uint32_t kept = kept_of(a, b, first, count);
+  for (uint32_t j0 = 0; j0 < kept; j0 += kKeepRows) {
+    const uint32_t rows = min(kept - j0, kKeepRows);
+    bool moves = false;
+    if (t < rows) {
+      const uint32_t j = j0 + t, i = (uint32_t)a.path[first + j];
+      uint32_t src = ~0u, dst = ~0u;
+      if (i > j && i < count) {
+        src = (uint32_t)a.slots[first + i];
+        dst = (uint32_t)a.slots[first + j];
+      }
+      moves = a.pool.holds(src) && a.pool.holds(dst);
+      s_src[t] = moves ? src : ~0u;
+      s_dst[t] = dst;
+    }
+    if (!__syncthreads_or(moves)) continue;
+    // 16-byte pieces of key rows, a row's side by side; value elements, a value row's side by side
+    const uint32_t pieces = dim / 8;
+    u32x4 k[8];
+#pragma unroll
+    for (uint32_t n = 0; n < 8; ++n) {  // kKeepRows * 1024 / 8 / 256
+      const uint32_t x = t + 256 * n, r = x / pieces;
+      if (r < rows && s_src[r] != ~0u)
+        k[n] = *reinterpret_cast<const u32x4*>(a.pool.kc + a.pool.page(layer, s_src[r] >> log, head) +
+                                               (s_src[r] & in_page) * dim + 8 * (x % pieces));
+    }
+    for (uint32_t d0 = 0; d0 < dim; d0 += 128) {
+      const uint32_t r = t % kKeepRows;
+      const bool on = r < rows && s_src[r] != ~0u;
+      const uint16_t* vs = a.pool.vc + a.pool.page(layer, on ? s_src[r] >> log : 0, head) + (on ? s_src[r] & in_page : 0);
+      uint16_t* vd = a.pool.vc + a.pool.page(layer, on ? s_dst[r] >> log : 0, head) + (on ? s_dst[r] & in_page : 0);
+      uint16_t v[8];
+#pragma unroll
+      for (uint32_t n = 0; n < 8; ++n) {
+        const uint32_t d = d0 + t / kKeepRows + 16 * n;
+        if (on && d < dim) v[n] = vs[(uint64_t)d << log];
+      }
+      __syncthreads();
+#pragma unroll
+      for (uint32_t n = 0; n < 8; ++n) {
+        const uint32_t d = d0 + t / kKeepRows + 16 * n;
+        if (on && d < dim) vd[(uint64_t)d << log] = v[n];
+      }
+    }
+#pragma unroll
+    for (uint32_t n = 0; n < 8; ++n) {
+      const uint32_t x = t + 256 * n, r = x / pieces;
+      if (r < rows && s_src[r] != ~0u)
+        *reinterpret_cast<u32x4*>(a.pool.kc + a.pool.page(layer, s_dst[r] >> log, head) + (s_dst[r] & in_page) * dim +
+                                  8 * (x % pieces)) = k[n];
+    }
+    __syncthreads();  // what was written is behind what the next step reads; s_src is reused
+  }
+}
+
+__global__ __launch_bounds__(256) void k_page_keep(KeepArgs a) {
+  __shared__ uint32_t s_sum[4], s_src[kKeepRows], s_dst[kKeepRows];
+  if (blockIdx.x == 0) {
+    keep_pages(a, s_sum);
+    return;
+  }
+  for (uint32_t unit = blockIdx.x - 1; unit < a.units; unit += gridDim.x - 1) keep_rows(a, unit, s_src, s_dst);
+}
+
+// ----------------------------------------------------------------------- fork
+struct ForkArgs {
+  const int32_t *src, *dst, *free_list, *free_head;
+  int32_t *lens, *table, *shares, *counts;
+  uint32_t forks, requests, width, free_len, parts;
+  Pool pool;
+};
+
+// Every workgroup goes through the list of forks for itself (one is a few loads): s_first
+// gets the first fork of each row, s_rank how many pages the forks before need, or ~0 for
+// a refused one.  Returns the pages taken in all.
+__device__ __forceinline__ uint32_t plan_forks(const ForkArgs& a, uint32_t* s_first, uint32_t* s_rank, uint32_t* s_sum) {
+  const uint32_t t = threadIdx.x, in_page = a.pool.block() - 1;
+  for (uint32_t i = t; i < a.requests; i += 256) s_first[i] = ~0u;
+  __syncthreads();
+  for (uint32_t i = t; i < a.forks; i += 256) {
+    const uint32_t dst = (uint32_t)a.dst[i];
+    if (dst < a.requests) atomicMin(&s_first[dst], i);  // the least of them, in any order
+  }
+  __syncthreads();
+  const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len), left = a.free_len - head;
+  uint32_t taken = 0;
+  for (uint32_t i0 = 0; i0 < a.forks; i0 += 256) {
+    const uint32_t i = i0 + t;
+    bool sound = false, need = false;
+    if (i < a.forks) {
+      const uint32_t src = (uint32_t)a.src[i], dst = (uint32_t)a.dst[i];
+      if (src < a.requests && dst < a.requests && s_first[dst] == i) {
+        const int32_t len = a.lens[src];
+        sound = len > 0 && a.lens[dst] <= 0 && ((uint64_t)len + in_page) >> a.pool.log_block <= a.width;
+        need = sound && (len & in_page);
+      }
+    }
+    uint32_t all;
+    const uint32_t rank = taken + sum_before<256>(need, s_sum, &all);
+    taken += all;
+    if (i < a.forks) s_rank[i] = sound && (!need || rank < left) ? rank : ~0u;
+  }
+  __syncthreads();
+  return min(taken, left);
+}
+
+// Part 0 of a fork writes the row of the table and counts the shares; every part copies its
+// share of the last page's pieces in all layers and heads: key rows up to the length,
+// values in pieces of 8 tokens.
+__global__ __launch_bounds__(256) void k_page_fork(ForkArgs a) {
+  extern __shared__ uint32_t lds[];
+  __shared__ uint32_t s_sum[4];
+  uint32_t *s_first = lds, *s_rank = lds + a.requests;
+  plan_forks(a, s_first, s_rank, s_sum);
+  const uint32_t t = threadIdx.x, log = a.pool.log_block, dim = a.pool.dim;
+  const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
+  for (uint32_t unit = blockIdx.x; unit < a.forks * a.parts; unit += gridDim.x) {
+    const uint32_t i = unit / a.parts, part = unit % a.parts, rank = s_rank[i];
+    if (rank == ~0u) continue;
+    const uint32_t src = (uint32_t)a.src[i], dst = (uint32_t)a.dst[i], len = (uint32_t)a.lens[src];
+    const uint32_t full = len >> log, rest = len & (a.pool.block() - 1);
+    const int32_t* from = a.table + (uint64_t)src * a.width;
+    const uint32_t fresh = rest ? (uint32_t)a.free_list[head + rank] : ~0u;
+    if (part == 0) {
+      int32_t* to = a.table + (uint64_t)dst * a.width;
+      for (uint32_t c = t; c < full; c += 256) {
+        const uint32_t id = (uint32_t)from[c];
+        to[c] = (int32_t)id;
+        if (id < a.pool.blocks) atomicAdd(a.shares + id, 1);
+      }
+      if (t == 0 && rest) to[full] = (int32_t)fresh;
+    }
+    if (!rest) continue;
+    const uint32_t old = (uint32_t)from[full];
+    if (old >= a.pool.blocks || fresh >= a.pool.blocks || old == fresh) continue;
+    const uint32_t k_pieces = rest * dim / 8, v_row = (rest + 7) / 8, v_pieces = v_row * dim;
+    const uint32_t in_row = a.pool.block() / 8, each = k_pieces + v_pieces;
+    const uint32_t heads = a.pool.layers * a.pool.heads;
+    for (uint32_t lh = part; lh < heads; lh += a.parts) {
+      const uint64_t x = a.pool.page(lh / a.pool.heads, old, lh % a.pool.heads);
+      const uint64_t y = a.pool.page(lh / a.pool.heads, fresh, lh % a.pool.heads);
+      const u32x4 *kx = reinterpret_cast<const u32x4*>(a.pool.kc + x), *vx = reinterpret_cast<const u32x4*>(a.pool.vc + x);
+      u32x4 *ky = reinterpret_cast<u32x4*>(a.pool.kc + y), *vy = reinterpret_cast<u32x4*>(a.pool.vc + y);
+      auto value_at = [&](uint32_t p) { return p / v_row * in_row + p % v_row; };
+      for (uint32_t p0 = t; p0 < each; p0 += 256 * 4) {
+        u32x4 v[4];
+#pragma unroll
+        for (uint32_t n = 0; n < 4; ++n) {
+          const uint32_t p = p0 + 256 * n;
+          if (p < each) v[n] = p < k_pieces ? kx[p] : vx[value_at(p - k_pieces)];
+        }
+#pragma unroll
+        for (uint32_t n = 0; n < 4; ++n) {
+          const uint32_t p = p0 + 256 * n;
+          if (p < k_pieces) ky[p] = v[n];
+          else if (p < each) vy[value_at(p - k_pieces)] = v[n];
+        }
+      }
+    }
+  }
+}
+
+// Lengths and the head change in a launch of their own, after every workgroup of the first
+// has read them.
+__global__ __launch_bounds__(256) void k_fork_counts(ForkArgs a) {
+  extern __shared__ uint32_t lds[];
+  __shared__ uint32_t s_sum[4], s_refused;
+  uint32_t *s_first = lds, *s_rank = lds + a.requests;
+  if (threadIdx.x == 0) s_refused = 0;
+  const uint32_t taken = plan_forks(a, s_first, s_rank, s_sum);
+  const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
+  uint32_t refused = 0;
+  for (uint32_t i = threadIdx.x; i < a.forks; i += 256) {
+    // (a source is not empty and a destination is, so none of these is read here again)
+    if (s_rank[i] != ~0u) a.lens[a.dst[i]] = a.lens[a.src[i]];
+    else ++refused;
+  }
+  if (refused) atomicAdd(&s_refused, refused);  // whole numbers: any order gives the same
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.counts[0] = (int32_t)(head + taken);
+    a.counts[1] = (int32_t)s_refused;
+  }
+}
+
+// ----------------------------------------------------------------------- free
+struct FreeArgs {
+  const int32_t *rows, *free_head;
+  int32_t *lens, *table, *free_list, *shares, *counts;
+  uint32_t* bits;  // of the pages that go back
+  uint32_t count, requests, width, free_len, log_block, blocks, words, parts;
+};
+
+// A page loses a holder for each row that ends; the one that finds none left marks it.
+__global__ __launch_bounds__(256) void k_page_free(FreeArgs a) {
+  const uint32_t t = threadIdx.x;
+  for (uint32_t unit = blockIdx.x; unit < a.count * a.parts; unit += gridDim.x) {
+    const uint32_t i = unit / a.parts, part = unit % a.parts, row = (uint32_t)a.rows[i];
+    if (row >= a.requests) continue;
+    bool again = false;  // a row that was named before
+    for (uint32_t j = t; j < i; j += 256) again |= (uint32_t)a.rows[j] == row;
+    if (__syncthreads_or(again)) continue;
+    const uint32_t len = (uint32_t)max(a.lens[row], 0);
+    const uint32_t pages = min((uint32_t)(((uint64_t)len + (1u << a.log_block) - 1) >> a.log_block), a.width);
+    for (uint32_t c = t + 256 * part; c < pages; c += 256 * a.parts) {
+      int32_t* at = a.table + (uint64_t)row * a.width + c;
+      const uint32_t id = (uint32_t)*at;
+      *at = -1;
+      if (id < a.blocks && atomicSub(a.shares + id, 1) <= 0) atomicOr(a.bits + id / 32, 1u << id % 32);
+    }
+  }
+}
+
+// One workgroup writes the marked pages into the list, in the order of their ids, and
+// clears the marks.
+constexpr uint32_t kCollect = 1024;
+__global__ __launch_bounds__(kCollect) void k_free_collect(FreeArgs a) {
+  __shared__ uint32_t s_sum[kCollect / 64];
+  const uint32_t t = threadIdx.x;
+  const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
+  uint32_t total = 0;
+  for (uint32_t w = t; w < a.words; w += kCollect) total += __popc(a.bits[w]);
+  sum_before<kCollect>(total, s_sum, &total);
+  uint32_t done = 0;
+  for (uint32_t w0 = 0; w0 < a.words; w0 += kCollect) {
+    const uint32_t w = w0 + t;
+    uint32_t bits = w < a.words ? a.bits[w] : 0, all;
+    uint32_t at = done + sum_before<kCollect>(__popc(bits), s_sum, &all);
+    done += all;
+    if (bits) a.bits[w] = 0;
+    for (; bits; bits &= bits - 1, ++at) {
+      const uint32_t id = 32 * w + (uint32_t)__builtin_ctz(bits);
+      a.shares[id] = 0;
+      if (head + at >= total) a.free_list[head + at - total] = (int32_t)id;
+    }
+  }
+  for (uint32_t i = t; i < a.count; i += kCollect)
+    if ((uint32_t)a.rows[i] < a.requests) a.lens[a.rows[i]] = 0;
+  __syncthreads();
+  if (t == 0) {
+    a.counts[0] = (int32_t)(head - min(total, head));
+    a.counts[1] = (int32_t)total;
+  }
+}
+
+bool caches_ok(uint32_t layers, uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block) {
+  return block_ok(block) && pool_ok(blocks, block) && layers >= 1 && layers <= 4096 && heads >= 1 && heads <= 65535 &&
+         dim >= 8 && dim % 8 == 0 && dim <= 1024;
+}
+
+bool table_ok(uint32_t requests, uint32_t width, uint32_t free_len, uint32_t block) {
+  return requests <= kMaxRequests && free_len <= (1u << 30) && (uint64_t)width * block <= 0x7FFFFFFFull;
+}
+
+Pool make_pool(void* k, void* v, uint32_t layers, uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block) {
+  return Pool{static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), layers, heads, dim, (uint32_t)__builtin_ctz(block),
+              blocks};
+}
+
+}  // namespace
+}  // namespace serve
+}  // namespace dgt
+
+using namespace dgt::serve;
+
+extern "C" {
+
+int dgt_page_keep(const int32_t* d_path, const int32_t* d_kept, const int32_t* d_ctx, const int32_t* d_cu,
+                  const int32_t* d_slots, uint32_t requests, uint32_t tokens, int32_t* d_free,
+                  uint32_t free_len, const int32_t* d_free_head, int32_t* d_table, uint32_t width,
+                  uint32_t layers, uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block,
+                  void* d_k_cache, void* d_v_cache, int32_t* d_lens, int32_t* d_counts, void* stream) {
+  if (!caches_ok(layers, heads, dim, blocks, block) || !table_ok(requests, width, free_len, block) || tokens > (1u << 28))
+    return DGT_E_SHAPE;
+  if (!d_free_head || !d_counts || (free_len && !d_free)) return DGT_E_ARG;
+  if (requests && (!d_kept || !d_ctx || !d_cu || !d_lens || (width && !d_table))) return DGT_E_ARG;
+  if (tokens && !d_slots) return DGT_E_ARG;
+  if (blocks && (!d_k_cache || !d_v_cache)) return DGT_E_ARG;
+  if (!aligned(d_k_cache, 16) || !aligned(d_v_cache, 16)) return DGT_E_ARG;
+  KeepArgs a;
+  a.path = d_path;
+  a.kept = d_kept;
+  a.ctx = d_ctx;
+  a.cu = d_cu;
+  a.slots = d_slots;
+  a.free_head = d_free_head;
+  a.free_list = d_free;
+  a.table = d_table;
+  a.lens = d_lens;
+  a.counts = d_counts;
+  a.requests = requests;
+  a.tokens = tokens;
+  a.free_len = free_len;
+  a.width = width;
+  a.pool = make_pool(d_k_cache, d_v_cache, layers, heads, dim, blocks, block);
+  // a unit is the rows of one request, layer and head
+  const uint64_t units = d_path && tokens && blocks ? (uint64_t)requests * layers * heads : 0;
+  if (units > 0xFFFFFFFFull - 64 * kCUs) return DGT_E_SHAPE;
+  a.units = (uint32_t)units;
+  hipLaunchKernelGGL(k_page_keep, dim3(1 + (uint32_t)std::min<uint64_t>(units, 16 * kCUs)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), a);
+  return launched();
+}
+
+int dgt_page_fork(const int32_t* d_src, const int32_t* d_dst, uint32_t forks, int32_t* d_lens,
+                  int32_t* d_table, uint32_t requests, uint32_t width, const int32_t* d_free,
+                  uint32_t free_len, const int32_t* d_free_head, int32_t* d_shares, uint32_t layers,
+                  uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block, void* d_k_cache,
+                  void* d_v_cache, int32_t* d_counts, void* stream) {
+  if (!caches_ok(layers, heads, dim, blocks, block) || !table_ok(requests, width, free_len, block) || forks > kMaxRequests)
+    return DGT_E_SHAPE;
+  if (!d_free_head || !d_counts || (free_len && !d_free)) return DGT_E_ARG;
+  if (forks && (!d_src || !d_dst)) return DGT_E_ARG;
+  if (requests && (!d_lens || (width && !d_table))) return DGT_E_ARG;
+  if (blocks && (!d_k_cache || !d_v_cache || !d_shares)) return DGT_E_ARG;
+  if (!aligned(d_k_cache, 16) || !aligned(d_v_cache, 16)) return DGT_E_ARG;
+  ForkArgs a;
+  a.src = d_src;
+  a.dst = d_dst;
+  a.free_list = d_free;
+  a.free_head = d_free_head;
+  a.lens = d_lens;
+  a.table = d_table;
+  a.shares = d_shares;
+  a.counts = d_counts;
+  a.forks = forks;
+  a.requests = requests;
+  a.width = width;
+  a.free_len = free_len;
+  a.pool = make_pool(d_k_cache, d_v_cache, layers, heads, dim, blocks, block);
+  // parts of a fork, so that a few forks fill the card; a part is at least a head of a layer
+  a.parts = std::min(layers * heads, std::max(4 * kCUs / std::max(forks, 1u), 1u));
+  const uint32_t lds = 4 * (requests + forks);
+  if (lds > 63 * 1024 &&  // with what the kernels have besides, more than the 64 KB of a plain launch
+      (hipFuncSetAttribute(reinterpret_cast<const void*>(k_page_fork), hipFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)lds) != hipSuccess ||
+       hipFuncSetAttribute(reinterpret_cast<const void*>(k_fork_counts), hipFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)lds) != hipSuccess))
+    return DGT_E_HIP;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (forks) {
+    hipLaunchKernelGGL(k_page_fork, dim3(std::min(forks * a.parts, 8 * kCUs)), dim3(256), lds, st, a);
+    if (int rc = launched()) return rc;
+  }
+  hipLaunchKernelGGL(k_fork_counts, dim3(1), dim3(256), lds, st, a);
+  return launched();
+}
+
+size_t dgt_page_free_workspace(uint32_t blocks) { return ((size_t)blocks + 31) / 32 * 4 + 4; }
+
+int dgt_page_free(const int32_t* d_rows, uint32_t count, int32_t* d_lens, int32_t* d_table,
+                  uint32_t requests, uint32_t width, int32_t* d_free, uint32_t free_len,
+                  const int32_t* d_free_head, int32_t* d_shares, uint32_t blocks, uint32_t block,
+                  int32_t* d_counts, void* d_ws, size_t ws_bytes, void* stream) {
+  if (!block_ok(block) || !pool_ok(blocks, block) || !table_ok(requests, width, free_len, block) || count > kMaxRequests)
+    return DGT_E_SHAPE;
+  if (!d_free_head || !d_counts || (free_len && !d_free) || (count && !d_rows)) return DGT_E_ARG;
+  if (requests && (!d_lens || (width && !d_table))) return DGT_E_ARG;
+  if ((blocks && !d_shares) || !d_ws || !aligned(d_ws, 4)) return DGT_E_ARG;
+  if (ws_bytes < dgt_page_free_workspace(blocks)) return DGT_E_BUFSIZE;
+  FreeArgs a;
+  a.rows = d_rows;
+  a.free_head = d_free_head;
+  a.lens = d_lens;
+  a.table = d_table;
+  a.free_list = d_free;
+  a.shares = d_shares;
+  a.counts = d_counts;
+  a.bits = static_cast<uint32_t*>(d_ws);
+  a.count = count;
+  a.requests = requests;
+  a.width = width;
+  a.free_len = free_len;
+  a.log_block = (uint32_t)__builtin_ctz(block);
+  a.blocks = blocks;
+  a.words = (blocks + 31) / 32;
+  a.parts = std::max(1u, std::min((width + 255) / 256, 2 * kCUs / std::max(count, 1u)));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (count) {
+    hipLaunchKernelGGL(k_page_free, dim3(std::min(count * a.parts, 8 * kCUs)), dim3(256), 0, st, a);
+    if (int rc = launched()) return rc;
+  }
+  hipLaunchKernelGGL(k_free_collect, dim3(1), dim3(kCollect), 0, st, a);
+  return launched();
+}
+
+}  // extern "C"

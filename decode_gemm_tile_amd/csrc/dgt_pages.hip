@@ -236,34 +236,6 @@ struct StoreArgs {
   bool wide;  // rows of k and v are 16-byte aligned
 };
 
-constexpr uint32_t kStoreRows = 64, kStoreDims = 128;  // a workgroup's tile; longer heads take several
-constexpr uint32_t kStoreLine = kStoreRows + 2;        // elements of a value row in LDS
-
-// Eight elements of a source row in the cache's type.
-template <typename E, typename S>
-__device__ __forceinline__ u32x4 load8(const S* p, bool wide) {
-  if constexpr (sizeof(S) == 2) {
-    if (wide) return *reinterpret_cast<const u32x4*>(p);
-    u32x4 o;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = p[2 * j] | (uint32_t)p[2 * j + 1] << 16;
-    return o;
-  } else {
-    floatx4 a, b;
-    if (wide) {
-      a = *reinterpret_cast<const floatx4*>(p);
-      b = *reinterpret_cast<const floatx4*>(p + 4);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j] = p[j];
-        b[j] = p[4 + j];
-      }
-    }
-    return u32x4{E::pack2(a[0], a[1]), E::pack2(a[2], a[3]), E::pack2(b[0], b[1]), E::pack2(b[2], b[3])};
-  }
-}
-
 template <typename E, typename S>
 __global__ __launch_bounds__(256) void k_kv_store(StoreArgs a) {
   __shared__ uint32_t s_slot[kStoreRows], s_head[kStoreRows], s_heads;
@@ -272,15 +244,8 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreArgs a) {
   const uint32_t d0 = blockIdx.z * kStoreDims, dims = min(a.dim - d0, kStoreDims);
   const uint32_t rows = min(a.tokens - t0, kStoreRows), block = 1u << a.log_block;
   if (t < 64) {
-    uint32_t slot = t < rows ? (uint32_t)a.slots[t0 + t] : ~0u;
-    if (slot >= a.blocks << a.log_block) slot = ~0u;
-    s_slot[t] = slot;
-    // tokens that begin a group: skipped ones begin none
-    const uint32_t last = (uint32_t)__shfl_up((int)slot, 1, 64);
-    const bool begins = slot != ~0u && (t == 0 || slot != last + 1 || last == ~0u || slot % 8 == 0);
-    const uint64_t all = __ballot(begins);
-    if (begins) s_head[__popcll(all & ((1ull << t) - 1))] = t;
-    if (t == 0) s_heads = (uint32_t)__popcll(all);
+    const uint32_t slot = t < rows ? (uint32_t)a.slots[t0 + t] : ~0u;
+    slot_groups(slot < a.blocks << a.log_block ? slot : ~0u, s_slot, s_head, &s_heads);
   }
   __syncthreads();
   const S* k = static_cast<const S*>(a.k) + (int64_t)h * a.k_head + d0;
@@ -311,26 +276,7 @@ __global__ __launch_bounds__(256) void k_kv_store(StoreArgs a) {
     }
   }
   __syncthreads();
-  const uint32_t heads = s_heads;
-  // Two groups side by side, then the next value row, so that neighbours in memory go
-  // to neighbouring lanes.
-  for (uint32_t i = t; i < dims * (heads + (heads & 1)); i += 256) {
-    const uint32_t two = i / (2 * dims), d = i / 2 % dims, group = 2 * two + (i & 1);
-    if (group >= heads) continue;
-    const uint32_t r0 = s_head[group], slot = s_slot[r0];
-    uint16_t* to = a.vc + (((uint64_t)(slot >> a.log_block) * a.heads + h) * a.dim + d0 + d) * block + (slot & (block - 1));
-    const uint16_t* from = s_v + d * kStoreLine + r0;
-    uint32_t n = 1;  // tokens of the group
-    while (n < 8 - slot % 8 && r0 + n < kStoreRows && s_slot[r0 + n] == slot + n) ++n;
-    if (n == 8) {
-      u32x4 o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = from[2 * j] | (uint32_t)from[2 * j + 1] << 16;
-      *reinterpret_cast<u32x4*>(to) = o;
-    } else {
-      for (uint32_t j = 0; j < n; ++j) to[j] = from[j];
-    }
-  }
+  write_values(a.vc + (uint64_t)h * a.dim * block, a.heads, a.dim, d0, dims, a.log_block, s_v, s_slot, s_head, s_heads);
 }
 
 }  // namespace

@@ -99,6 +99,75 @@ __device__ __forceinline__ uint32_t chunk_request(const int32_t* cu, uint32_t co
   return lo;
 }
 
+// ------------------------------------------------- new tokens into the cache's pages
+constexpr uint32_t kStoreRows = 64, kStoreDims = 128;  // a workgroup's tile; longer heads take several
+constexpr uint32_t kStoreLine = kStoreRows + 2;        // elements of a value row in LDS
+
+// Eight elements of a source row in the cache's type.
+template <typename E, typename S>
+__device__ __forceinline__ u32x4 load8(const S* p, bool wide) {
+  if constexpr (sizeof(S) == 2) {
+    if (wide) return *reinterpret_cast<const u32x4*>(p);
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = p[2 * j] | (uint32_t)p[2 * j + 1] << 16;
+    return o;
+  } else {
+    floatx4 a, b;
+    if (wide) {
+      a = *reinterpret_cast<const floatx4*>(p);
+      b = *reinterpret_cast<const floatx4*>(p + 4);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[j] = p[j];
+        b[j] = p[4 + j];
+      }
+    }
+    return u32x4{E::pack2(a[0], a[1]), E::pack2(a[2], a[3]), E::pack2(b[0], b[1]), E::pack2(b[2], b[3])};
+  }
+}
+
+// Tokens of a tile whose slots follow one another within 8 aligned slots make a group: the
+// wave's lanes hold a slot each (~0: no token, or one that is skipped); s_head gets the
+// tokens that begin a group.
+__device__ __forceinline__ void slot_groups(uint32_t slot, uint32_t* s_slot, uint32_t* s_head, uint32_t* s_heads) {
+  const uint32_t t = threadIdx.x;
+  s_slot[t] = slot;
+  const uint32_t last = (uint32_t)__shfl_up((int)slot, 1, 64);
+  const bool begins = slot != ~0u && (t == 0 || slot != last + 1 || last == ~0u || slot % 8 == 0);
+  const uint64_t all = __ballot(begins);
+  if (begins) s_head[__popcll(all & ((1ull << t) - 1))] = t;
+  if (t == 0) *s_heads = (uint32_t)__popcll(all);
+}
+
+// Writes a tile's values, turned in LDS (s_v: kStoreLine elements a value row), into the
+// pages of one head; vc points at the head's first page.
+__device__ __forceinline__ void write_values(uint16_t* vc, uint32_t page_heads, uint32_t dim, uint32_t d0, uint32_t dims,
+                                             uint32_t log_block, const uint16_t* s_v, const uint32_t* s_slot,
+                                             const uint32_t* s_head, uint32_t heads) {
+  const uint32_t block = 1u << log_block;
+  // Two groups side by side, then the next value row, so that neighbours in memory go
+  // to neighbouring lanes.
+  for (uint32_t i = threadIdx.x; i < dims * (heads + (heads & 1)); i += 256) {
+    const uint32_t two = i / (2 * dims), d = i / 2 % dims, group = 2 * two + (i & 1);
+    if (group >= heads) continue;
+    const uint32_t r0 = s_head[group], slot = s_slot[r0];
+    uint16_t* to = vc + ((uint64_t)(slot >> log_block) * page_heads * dim + d0 + d) * block + (slot & (block - 1));
+    const uint16_t* from = s_v + d * kStoreLine + r0;
+    uint32_t n = 1;  // tokens of the group
+    while (n < 8 - slot % 8 && r0 + n < kStoreRows && s_slot[r0 + n] == slot + n) ++n;
+    if (n == 8) {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = from[2 * j] | (uint32_t)from[2 * j + 1] << 16;
+      *reinterpret_cast<u32x4*>(to) = o;
+    } else {
+      for (uint32_t j = 0; j < n; ++j) to[j] = from[j];
+    }
+  }
+}
+
 // Keeps what is computed from v inside the loop it stands in: the rare paths'
 // addresses would otherwise be formed ahead of all loops and hold registers there.
 __device__ __forceinline__ void keep_here(uint32_t& v) { asm volatile("" : "+v"(v)); }

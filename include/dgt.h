@@ -360,6 +360,144 @@ int dgt_lora_add(const float* d_y, uint64_t y_row, const uint16_t* d_x, uint64_t
                  uint32_t n, uint32_t k, uint32_t rank, float* d_out, uint64_t out_row, void* d_ws,
                  size_t ws_bytes, void* stream);
 
+/* Queries, keys and values of the new tokens out of the projection's rows: norms of
+ * queries and keys for each head and the rotation by position in one pass, the
+ * queries into 16-bit rows for the attention, keys and values into the paged cache.
+ *   x^ = w x / sqrt(mean(x^2) + eps) over the dim elements of a head (without a
+ *        weight array x^ = x);
+ *   the first 2 * pairs elements of x^ are turned in pairs by the angle
+ *        a_i = position * freqs[i]:  (x, y) -> (x cos a - y sin a, y cos a + x sin a);
+ *        pairs are (i, i + pairs), or (2 i, 2 i + 1) with interleaved != 0.
+ * All in fp32 (angles in fp64), rounded once to nearest even; values are only rounded.
+ *   d_q [tokens, heads, dim], d_k, d_v [tokens, kv_heads, dim] of type `source`: F32,
+ *          or the type of the cache; element strides per row and head, elements of a
+ *          head contiguous.
+ *   d_positions: int32[tokens]; rows with a negative one are skipped altogether.
+ *   d_slots: int32[tokens]; keys and values of slots outside the pool are skipped (the
+ *          queries are not).  Two rows with one slot leave it with either's values.
+ *   d_freqs: double[pairs], radians a position; pairs <= dim / 2, 0 for no rotation.
+ *   d_q_weight, d_k_weight: float[dim] or NULL.  eps >= 0.
+ *   type: BF16 or F16, of d_q_out and the pages.  d_q_out [tokens, heads, dim], strides
+ *          multiples of 8; it does not overlap an input.
+ * dim: a multiple of 8 up to 256.  d_q_out and the pages are 16-byte aligned.
+ * Errors: E_ARG, E_SHAPE, E_UNSUPPORTED, E_HIP. */
+int dgt_rope_store(const void* d_q, const void* d_k, const void* d_v, uint32_t source, int64_t q_row,
+                   int64_t q_head, int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
+                   const int32_t* d_positions, const int32_t* d_slots, uint32_t tokens, uint32_t heads,
+                   uint32_t kv_heads, uint32_t dim, const double* d_freqs, uint32_t pairs,
+                   uint32_t interleaved, const float* d_q_weight, const float* d_k_weight, float eps,
+                   uint32_t type, void* d_q_out, int64_t out_row, int64_t out_head, void* d_k_cache,
+                   void* d_v_cache, uint32_t blocks, uint32_t block, void* stream);
+
+/* Attention of a chunk of new tokens (a prompt or a part of one) over cached and new
+ * keys: what dgt_tree_attention computes without a mask, with its layouts and the
+ * same values up to rounding, made for many new tokens a request: tiles of rows end at
+ * their own last key, and long ones are split over the keys.
+ *   d_ws: dgt_chunk_attention_workspace(...) bytes, any contents.
+ * Three launches; the order of all sums is fixed by the lengths and shapes.
+ * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED, E_HIP. */
+size_t dgt_chunk_attention_workspace(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim,
+                                     uint32_t requests);
+int dgt_chunk_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t q_head,
+                        const void* d_k_cache, const void* d_v_cache, uint32_t blocks, uint32_t block,
+                        const int32_t* d_table, uint32_t width, const int32_t* d_ctx, const int32_t* d_cu,
+                        uint32_t requests, uint32_t tokens, uint32_t heads, uint32_t kv_heads,
+                        uint32_t dim, float scale, void* d_out, uint64_t out_row, uint64_t out_head,
+                        void* d_ws, size_t ws_bytes, void* stream);
+
+/* Verification of drafted tokens: which of them the target's probabilities accept,
+ * and the token that follows, so that what comes out is distributed as the target's
+ * own samples are.  Row 0 of a request is a token that is decided already; the others
+ * are drafted, row i with token d_draft[i] to follow row parent(i) (d_parents as for
+ * dgt_page_plan; NULL: a chain).  Rows whose way up does not end in row 0 are never
+ * accepted.  At the path's end e (at first row 0), with p = softmax(logits[e] / T):
+ *   the children of e are looked at in the order of their rows.  Without draft
+ *   probabilities the drafts are taken as given: child i is accepted if
+ *   u_i * Z < p(x_i), Z = 1 - the sum of p over the tokens of e refused so far; a token
+ *   refused once is refused again.  With them (chains only): accepted if
+ *   u_i * q(x_i) < p(x_i), q = d_probs[e].  The first accepted child becomes the end.
+ *   With no child left the next token is the first v whose running sum of r passes
+ *   s * sum(r): r = p without the refused tokens, or max(p - q, 0) after a refusal.
+ * T = d_temperature[b] (NULL: 1); T <= 0 (or not a number): a child is accepted if its
+ * token is the row's largest logit's (the first of equals), and so is the next token.
+ * Sums over a vocabulary are fp64, and so are the exponentials in them.
+ *   d_logits: [tokens, vocab] of type `type` (F32, BF16, F16), row stride in elements;
+ *          -inf excludes a token.  A row with a NaN or +inf, or of -inf alone, ends the
+ *          path, and the next token is -1.
+ *   d_draft: int32[tokens]; ids outside the vocabulary are refused.
+ *   d_probs: NULL or float[tokens, vocab], row stride given: row e is what the token
+ *          after row e was drawn from.  Values that are negative or NaN count as 0.
+ *   d_accept: float[tokens], u of each row, in [0, 1); row 0's is not used.
+ *   d_sample: float[requests], s, in [0, 1).
+ *   d_path: int32[tokens]: the accepted rows as indexes within the request, row 0 first,
+ *          then -1 to the request's end; rows past cu[requests] are not written.
+ *   d_accepted: int32[requests], how many (0 for a request of no rows).
+ *   d_next: int32[requests] (-1 for a request of no rows).
+ *   d_ws: dgt_verify_workspace(...) bytes, any contents.
+ * vocab <= 2^22; tokens * vocab may pass 2^32.
+ * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED (draft probabilities of a tree), E_HIP. */
+size_t dgt_verify_workspace(uint32_t tokens, uint32_t vocab, uint32_t requests);
+int dgt_verify(uint32_t type, const void* d_logits, uint64_t logits_row, const int32_t* d_draft,
+               const float* d_probs, uint64_t probs_row, const int32_t* d_parents, const int32_t* d_cu,
+               const float* d_temperature, const float* d_accept, const float* d_sample,
+               uint32_t requests, uint32_t tokens, uint32_t vocab, int32_t* d_path,
+               int32_t* d_accepted, int32_t* d_next, void* d_ws, size_t ws_bytes, void* stream);
+
+/* Pages of a cache: what a step keeps, requests that share pages, requests that end.
+ * Caches here may hold several layers, [layers, blocks, ...] with the pages of each as
+ * above; a page id means the same page in all of them.  A free list is int32[free_len],
+ * its free ids from `head` on; pages go back in front of it.  d_free_head is read;
+ * d_counts[0] is the new head (d_free_head may lie in d_counts).  Nothing else overlaps
+ * but where it is said.  Elements are 16 bits and are copied bit for bit. */
+
+/* After a step: of request b the first d_kept[b] rows of its path are kept (cut to its new
+ * tokens).  Their keys and values move to the places of its first new tokens, in all
+ * layers; its length becomes ctx[b] + kept; pages past that length go back to the list,
+ * request by request, and their columns of the table become -1.
+ *   d_path: int32[tokens] as dgt_verify writes it: row cu[b] + j holds the index, within
+ *          the request, of the j-th kept row; or NULL: the first rows are kept.  The
+ *          indexes rise; where one is out of range, or below j, the j-th place is left as it is.
+ *   d_slots: int32[tokens], the step's slots (dgt_page_plan).  A request whose first new
+ *          token has no slot (the plan refused it) keeps nothing and returns nothing.
+ *   d_lens: int32[requests], the new lengths; may be d_ctx.
+ *   d_counts: int32[2]: the list's new head, the pages that went back.
+ * Errors: E_ARG, E_SHAPE, E_HIP. */
+int dgt_page_keep(const int32_t* d_path, const int32_t* d_kept, const int32_t* d_ctx, const int32_t* d_cu,
+                  const int32_t* d_slots, uint32_t requests, uint32_t tokens, int32_t* d_free,
+                  uint32_t free_len, const int32_t* d_free_head, int32_t* d_table, uint32_t width,
+                  uint32_t layers, uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block,
+                  void* d_k_cache, void* d_v_cache, int32_t* d_lens, int32_t* d_counts, void* stream);
+
+/* Fork: row dst[i] of the table becomes a request that holds what row src[i] holds.  Full
+ * pages are shared; of a last page that is not full a copy is made, into a page of the
+ * free list.  Both requests can then grow independently.
+ *   d_shares: int32[blocks], how many requests hold a page besides the first; zero for
+ *          pages that the plan hands out.
+ *   d_lens: int32[requests]; dst[i] must be empty (length 0) and gets src[i]'s length.
+ * Fork i is refused, and changes nothing, if src or dst is out of range, src is empty or
+ * its pages do not fit the table, dst is not empty, an earlier i names the same dst, or the
+ * list has no page left for it.
+ *   d_counts: int32[2]: the list's new head, the forks that were refused.
+ * forks and requests are at most 8192.  Errors: E_ARG, E_SHAPE, E_HIP. */
+int dgt_page_fork(const int32_t* d_src, const int32_t* d_dst, uint32_t forks, int32_t* d_lens,
+                  int32_t* d_table, uint32_t requests, uint32_t width, const int32_t* d_free,
+                  uint32_t free_len, const int32_t* d_free_head, int32_t* d_shares, uint32_t layers,
+                  uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block, void* d_k_cache,
+                  void* d_v_cache, int32_t* d_counts, void* stream);
+
+/* End of requests: the pages of rows d_rows lose a holder, and those that nobody else holds
+ * go back to the list, in the order of their ids.  Their lengths become 0, their columns
+ * of the table -1.  Rows out of range or named before are passed over.
+ *   d_counts: int32[2]: the list's new head, the pages that went back.
+ *   d_ws: dgt_page_free_workspace(blocks) bytes, zero-filled before its first use; every
+ *          call leaves it ready for the next (on one stream).
+ * count and requests are at most 8192.  Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_HIP. */
+size_t dgt_page_free_workspace(uint32_t blocks);
+int dgt_page_free(const int32_t* d_rows, uint32_t count, int32_t* d_lens, int32_t* d_table,
+                  uint32_t requests, uint32_t width, int32_t* d_free, uint32_t free_len,
+                  const int32_t* d_free_head, int32_t* d_shares, uint32_t blocks, uint32_t block,
+                  int32_t* d_counts, void* d_ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

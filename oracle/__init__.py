@@ -35,7 +35,8 @@ Module map
   blob      compressed-layer byte format writer / reader             (pinned)
   numerics  bf16 / e4m3 casts, int4 dequant, fp8 activation quant    (pinned)
   gemm      fp64 reference GEMM Y = X W^T                            (pinned)
-  serving   page plan, cache store, tree attention, adapters         (pinned)
+  serving   page plan, cache store, attention, adapters, rotation,
+            verification of drafts, page moves and forks             (pinned)
 
 Every function is pinned by a ``-m "not gpu"`` test in ``tests/test_oracle_*``
 against closed forms, brute force, library routines or hand-worked golden
