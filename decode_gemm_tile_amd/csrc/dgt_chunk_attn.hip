@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace dgt {
 namespace serve {
@@ -34,7 +35,7 @@ struct ChunkArgs {
   float scale;                   // times log2(e)
 };
 
-constexpr uint32_t kWaves = 4, kKeys = 64, kDies = 8;
+constexpr uint32_t kKeys = 64, kDies = 8;  // keys that pieces are counted in
 constexpr uint32_t kMostParts = 1024;  // of all tiles together
 
 // What k_chunk_plan leaves in the workspace, in words.
@@ -43,6 +44,7 @@ struct Plan {
   static constexpr uint32_t kPiece = 128;      // keys of a piece, a multiple of kKeys
   static constexpr uint32_t kItems = 129;      // in all
   static constexpr uint32_t kCut = 130;        // items among which those of cut tiles are
+  static constexpr uint32_t kZeros = 144;      // 16 bytes
   static constexpr uint32_t kOrder = 160;      // [requests]: request number, longest first
   static __host__ __device__ constexpr uint32_t item0(uint32_t requests) { return kOrder + requests; }  // [requests], first item
   static __host__ __device__ constexpr uint32_t part0(uint32_t requests) { return kOrder + 2 * requests; }  // [requests], first part
@@ -188,6 +190,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
     parts = bp;
   }
   if (t < kDies) a.plan[Plan::kQueue + 16 * t] = 0;
+  if (t < 4) a.plan[Plan::kZeros + t] = 0;
   if (t == 0) {
     a.plan[Plan::kPiece] = piece;
     a.plan[Plan::kItems] = sound ? items : 0;
@@ -239,20 +242,24 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, uint32_t x, uint32_t
   return it;
 }
 
-// A tile of keys and values in LDS, in 16-byte pieces, permuted so that 16 neighbouring
-// rows of an operand read lie on different banks.
-template <int DP>
+// A tile of keys and values in LDS, in 16-byte pieces: rows of keys, then rows of values
+// (a page holds them transposed).  Piece p of a row lies at p with some bits flipped by the
+// row's number, so that 16 neighbouring rows of an operand read lie on different banks.
+// Four tiles: one is multiplied by one half of the waves, the one before by the other,
+// and two are on their way.
+template <int DP, int WAVES>
 struct Tile {
+  static constexpr uint32_t kThreads = 64 * WAVES;
+  static constexpr uint32_t kKeys = DP == 256 ? 32 : 64, kGroups = kKeys / 8;
   static constexpr uint32_t kKPieces = DP / 8, kVPieces = kKeys / 8;  // of a row
   static constexpr uint32_t kPieces = kKeys * kKPieces;               // keys or values
-  static constexpr uint32_t kEach = kPieces / 256;                    // a thread
-  static constexpr uint32_t kBytes = 2 * 2 * kPieces * 16;
-  static __device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t piece) {
-    return row * kKPieces + (piece ^ (kKPieces >= 16 ? row & 15 : (row >> 1) & 7));
-  }
-  static __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) {
-    return row * kVPieces + (piece ^ ((row >> 1) & 7));
-  }
+  static constexpr uint32_t kEach = kPieces / kThreads;               // a thread
+  static constexpr uint32_t kBuffers = 4;
+  static constexpr uint32_t kBytes = kBuffers * 2 * kPieces * 16;
+  static __device__ __forceinline__ uint32_t k_flip(uint32_t row) { return kKPieces >= 16 ? row & 15 : (row >> 1) & 7; }
+  static __device__ __forceinline__ uint32_t v_flip(uint32_t row) { return kVPieces == 8 ? (row >> 1) & 7 : (row >> 2) & 3; }
+  static __device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t piece) { return row * kKPieces + (piece ^ k_flip(row)); }
+  static __device__ __forceinline__ uint32_t v_at(uint32_t row, uint32_t piece) { return row * kVPieces + (piece ^ v_flip(row)); }
 };
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
@@ -283,45 +290,78 @@ __device__ __forceinline__ float half_sum(float v) {
 // 16-bit weights up to 2^kSlack lose nothing by it.
 constexpr float kSlack = 8.f;
 
-template <int DP, int RT>
+template <int DP, int RT, int WAVES>
 struct PartOf {  // ref[rows], l[rows], then the outputs in the order of the lanes that hold them
-  static constexpr uint32_t kRows = kWaves * 32 * RT;
+  static constexpr uint32_t kRows = WAVES * 32 * RT;
   static constexpr uint32_t kFloats = kRows * (DP + 2);
 };
 
-template <class E, int DP, int RT, bool PAD>
-__global__ __launch_bounds__(256, 1) void k_chunk_attention(ChunkArgs a) {
-  using T = Tile<DP>;
-  using P = PartOf<DP, RT>;
-  constexpr int KS = DP / 16, DT = DP / 32;
+// 16 bytes a lane from memory into LDS, lane after lane from `to` (the same for all lanes of
+// the wave) on.  The compiler does not know that it is under way: loads_wait<n> waits until no
+// more than the last n of the wave's loads are.  (The compiler's own waits for its loads count
+// these too, and so wait longer than they need.)
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void loads_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// What the threads of a workgroup have written to LDS is there for all of them; loads from
+// memory stay under way (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <class E, int DP, int RT, int WAVES, bool PAD>
+__global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) {
+  using T = Tile<DP, WAVES>;
+  using P = PartOf<DP, RT, WAVES>;
+  constexpr int KS = DP / 16, DT = DP / 32, NH = T::kKeys / 32;
   extern __shared__ u32x4 lds[];
-  u32x4* s_k = lds;                   // [2][kPieces]
-  u32x4* s_v = lds + 2 * T::kPieces;  // [2][kPieces]
+  u32x4* s_k = lds;                               // [kBuffers][kPieces]
+  u32x4* s_v = lds + T::kBuffers * T::kPieces;    // [kBuffers][kPieces]
   __shared__ uint32_t s_item;
   const uint32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const uint32_t half = lane >> 5, l32 = lane & 31;
+  const uint32_t group = wave >> 2;
   const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
   const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
   const uint32_t page_bytes = (uint32_t)(2 * page_len) * a.heads;
   const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kItems];
 
-  // Pieces of a page's value row that lie in one tile, as a power of two.  Piece x of a tile
-  // of values in the order of memory: page by page, value row by row.
-  const uint32_t log_vp = min(a.log_block, 6u) - 3;
-  const uint32_t log_part = log_vp + (uint32_t)__builtin_ctz(DP);
-  const uint32_t k_lane = 2 * ((lane / T::kKPieces) * dim + 8 * (lane % T::kKPieces));
-  const uint32_t v_lane = 2 * (((lane >> log_vp) << a.log_block) + 8 * (lane & ((1u << log_vp) - 1)));
+  // A wave's load fills 64 neighbouring pieces in LDS, so a lane asks for the piece that
+  // belongs at its place.  Of the wave's first load: the lane's row and piece of it.  (Later
+  // loads are some rows on; kinds of flips repeat with them, but for keys of 256 elements,
+  // where bit 3 changes.)
+  const uint32_t k_row = (64 * wave + lane) / T::kKPieces, k_piece = lane % T::kKPieces ^ T::k_flip(k_row);
+  const uint32_t v_row = (64 * wave + lane) / T::kVPieces, v_piece = lane % T::kVPieces ^ T::v_flip(v_row);
+  constexpr uint32_t kRowStep = T::kThreads / T::kKPieces, vRowStep = T::kThreads / T::kVPieces;
+  static_assert(T::kVPieces == 8 ? vRowStep % 16 == 0 : vRowStep % 16 == 0, "values: the same flips in all loads");
+  static_assert(T::kKPieces == 16 ? kRowStep % 16 == 0 : T::kKPieces == 8 ? kRowStep % 16 == 0 : kRowStep == 8, "keys");
+  const uint32_t k_lane = 2 * (lane / T::kKPieces) * dim;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  const uint8_t* zeros = reinterpret_cast<const uint8_t*>(a.plan + Plan::kZeros);  // what lies past dim
 
   uint32_t queue = blockIdx.x % kDies, tried = 0;
+  auto draw = [&] { return __hip_atomic_fetch_add(a.plan + Plan::kQueue + 16 * queue, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  uint32_t drawn = t == 0 ? draw() : 0;
   for (;;) {
     if (t == 0) {
       uint32_t x = ~0u;
-      for (; tried < kDies; ++tried, queue = (queue + 1) % kDies) {
-        const uint32_t n = __hip_atomic_fetch_add(a.plan + Plan::kQueue + 16 * queue, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (n < (items + kDies - 1 - queue) / kDies) {
-          x = n * kDies + queue;
+      while (tried < kDies) {
+        if (drawn < (items + kDies - 1 - queue) / kDies) {
+          x = drawn * kDies + queue;
           break;
         }
+        queue = (queue + 1) % kDies;  // this die's is empty: help the next
+        if (++tried < kDies) drawn = draw();
       }
       s_item = x;
     }
@@ -329,6 +369,7 @@ __global__ __launch_bounds__(256, 1) void k_chunk_attention(ChunkArgs a) {
     const uint32_t x = __builtin_amdgcn_readfirstlane(s_item);
     __syncthreads();
     if (x == ~0u) break;
+    if (t == 0) drawn = draw();  // the next item's number is on its way while this one is worked on
     const Item it = item_of(a, x, piece, P::kRows);
     // (a piece past the tile's keys; a tile of no keys at all still has rows to write)
     if (it.k0 >= it.k1 && it.piece) continue;
@@ -353,181 +394,163 @@ __global__ __launch_bounds__(256, 1) void k_chunk_attention(ChunkArgs a) {
     const uint32_t all_see = min(it.c.ctx + it.token + 1, it.c.keys);  // keys that every row sees
     floatx16 o[RT][DT];
     float ref[RT], l[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      ref[i] = -INFINITY;
-      l[i] = 0.f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[i][d] = floatx16{};
-    }
 
     const int32_t* pages = a.table + (uint64_t)it.b * a.width;
     const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.kc + it.head * page_len);
     const uint8_t* values = reinterpret_cast<const uint8_t*>(a.vc + it.head * page_len);
-    // Pages of a tile's groups of 8 keys, one a lane (repeating), ~0 where the group does not
-    // exist; `absent` has a bit for each such group.
-    auto tile_pages = [&](uint32_t kb) {
-      const uint32_t key = kb + 8 * (lane % 8);
-      const uint32_t page = key < it.k1 ? (uint32_t)pages[key >> a.log_block] : ~0u;
-      return page < a.blocks ? page : ~0u;
+    // Pages of the groups of 8 keys of kSpan tiles, one a lane.  A table entry is looked at
+    // kSpan tiles after it was asked for: waiting for it in each tile was a third of the
+    // kernel's time.
+    constexpr uint32_t kSpan = 64 / T::kGroups;
+    auto key_of = [&](uint32_t n) { return it.k0 + n * T::kKeys + 8 * lane; };
+    auto ask = [&](uint32_t n) { return (uint32_t)pages[min(key_of(n), it.k1 - 1) >> a.log_block]; };
+    uint32_t coming = 0, have = 0;  // entries asked for, and pages in hand
+    uint64_t gone = 0;              // a bit for each group in hand that does not exist
+    // Sets tile n on its way into its buffer; where a group does not exist, page 0 is read
+    // instead.  A wave's keys of one load lie in one group, so their page is a scalar.
+    auto load = [&](uint32_t n) {
+      const uint32_t in = n % kSpan * T::kGroups;
+      if (in == 0) {
+        const bool off = coming >= a.blocks || key_of(n) >= it.k1;
+        gone = __ballot(off);
+        have = off ? 0u : coming;
+        coming = ask(n + kSpan);
+      }
+      const uint32_t inside = (it.k0 + n * T::kKeys) & in_page;  // where the tile begins in a page longer than it
+      const uint32_t to = lds0 + (n % T::kBuffers) * T::kPieces * 16 + wave * 1024;
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) {
+        const uint32_t row = 64 * wave / T::kKPieces + kRowStep * j, p = k_piece ^ (T::kKPieces == 32 ? 8 * (j & 1) : 0);
+        const uint8_t* from = keys + (uint64_t)__builtin_amdgcn_readlane(have, in + row / 8) * page_bytes +
+                              (inside + (row & in_page)) * (2 * dim);
+        // (every wave makes the same number of loads: waits count them)
+        if constexpr (PAD) load_to_lds(8 * p < dim ? from + k_lane + 16 * p : zeros, to + T::kThreads * 16 * j);
+        else load_to_lds(from, k_lane + 16 * p, to + T::kThreads * 16 * j);
+      }
+      const uint64_t page = (uint32_t)__shfl((int)have, in + v_piece, 64);
+      const uint8_t* from = values + page * page_bytes + 2 * ((v_row << a.log_block) + inside + (8 * v_piece & in_page));
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) {
+        const uint8_t* row = from + j * ((uint64_t)(2 * vRowStep) << a.log_block);
+        load_to_lds(!PAD || v_row + vRowStep * j < dim ? row : zeros, to + (T::kBuffers * T::kPieces + T::kThreads * j) * 16);
+      }
+      return (uint32_t)(gone >> in) & ((1u << T::kGroups) - 1);
     };
-    u32x4 rk[T::kEach], rv[T::kEach];
-    uint32_t absent = 0, coming = tile_pages(it.k0);
-    // A wave's pieces of one load lie in one page, so the page is a scalar; where a group
-    // does not exist, page 0 is read instead.
-    auto load = [&](uint32_t kb) {
-      absent = (uint32_t)__ballot(coming == ~0u) & 0xFFu;
-      const uint32_t pages_now = coming == ~0u ? 0u : coming;
-      coming = tile_pages(kb + kKeys);
-      const uint32_t inside = kb & in_page;  // where the tile begins in a page longer than it
-#pragma unroll
+    constexpr int kLoads = 2 * T::kEach;  // of a wave and tile
+    // Some row does not see all of tile n, or a page is missing.
+    auto edge = [&](uint32_t n, uint32_t absent) { return it.k0 + (n + 1) * T::kKeys > all_see || absent; };
+    // Such a tile, once it is there: values of keys that do not exist become zero, and one
+    // that is not finite is noted, for a weight of zero times it is not zero.
+    auto mend = [&](uint32_t n, uint32_t absent) {
+      bool odd = false;
       for (uint32_t j = 0; j < T::kEach; ++j) {
-        const uint32_t row = (64 * wave + 256 * j) / T::kKPieces;
-        const uint8_t* from = keys + (uint64_t)__builtin_amdgcn_readlane(pages_now, row / 8) * page_bytes;
-        const uint32_t at = (inside + (row & in_page)) * (2 * dim) + k_lane;
-        rk[j] = !PAD || 8 * (t % T::kKPieces) < dim ? *reinterpret_cast<const u32x4*>(from + at) : u32x4{};
-      }
+        if (PAD && v_row + vRowStep * j >= dim) continue;
+        u32x4* at = s_v + (n % T::kBuffers) * T::kPieces + t + T::kThreads * j;
+        u32x4 v = *at;
+        const uint32_t key = it.k0 + n * T::kKeys + 8 * v_piece;
+        const uint32_t real = (absent >> v_piece) & 1 || key >= it.k1 ? 0u : min(it.k1 - key, 8u);
 #pragma unroll
-      for (uint32_t j = 0; j < T::kEach; ++j) {
-        const uint32_t x_w = 64 * wave + 256 * j, part = x_w >> log_part;
-        const uint32_t y_w = x_w & ((1u << log_part) - 1);  // the wave's first piece within the part
-        const uint8_t* from = values + (uint64_t)__builtin_amdgcn_readlane(pages_now, part << log_vp) * page_bytes;
-        const uint32_t at = 2 * (((y_w >> log_vp) << a.log_block) + inside) + v_lane;
-        rv[j] = !PAD || (y_w + lane) >> log_vp < dim ? *reinterpret_cast<const u32x4*>(from + at) : u32x4{};
-      }
-    };
-    // Values of keys that do not exist become zero, and one that is not finite is noted
-    // where some row does not see it: a weight of zero times it is not zero.
-    bool odd = false;
-    auto store = [&](uint32_t kb, uint32_t buf) {
-      const bool edge = kb + kKeys > all_see || absent;
-      odd = false;
-#pragma unroll
-      for (uint32_t j = 0; j < T::kEach; ++j) {
-        const uint32_t x = t + 256 * j;
-        s_k[buf * T::kPieces + T::k_at(x / T::kKPieces, x % T::kKPieces)] = rk[j];
-      }
-#pragma unroll
-      for (uint32_t j = 0; j < T::kEach; ++j) {
-        const uint32_t x = t + 256 * j, row = (x & ((DP << log_vp) - 1)) >> log_vp;
-        const uint32_t p = (x >> log_part << log_vp) + (x & ((1u << log_vp) - 1));
-        if (edge) {
-          const uint32_t key = kb + 8 * p;
-          const uint32_t real = (absent >> p) & 1 || key >= it.k1 ? 0u : min(it.k1 - key, 8u);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t v = rv[j][w];
-            v = real <= 2u * w ? 0u : real == 2u * w + 1 ? v & 0xFFFFu : v;
-            rv[j][w] = v;
-            odd |= !E::finite2(v);
-          }
+        for (int w = 0; w < 4; ++w) {
+          v[w] = real <= 2u * w ? 0u : real == 2u * w + 1 ? v[w] & 0xFFFFu : v[w];
+          odd |= !E::finite2(v[w]);
         }
-        s_v[buf * T::kPieces + T::v_at(row, p)] = rv[j];
+        *at = v;
       }
-      if (edge) odd = __syncthreads_or(odd);
-      else __syncthreads();
+      return __syncthreads_or(odd);
     };
 
-    if (it.k0 < it.k1) {
-      load(it.k0);
-      store(it.k0, 0);
-    }
-    uint32_t buf = 0;
-    for (uint32_t kb = it.k0; kb < it.k1; kb += kKeys, buf ^= 1) {
-      const bool more = kb + kKeys < it.k1, odd_now = odd;
-      const uint32_t absent_now = absent;
-      if (more) load(kb + kKeys);
-      if (works) {
-        const u32x4* bk = s_k + buf * T::kPieces;
-        const u32x4* bv = s_v + buf * T::kPieces;
-        floatx16 s[RT][2];
+    // The plain loop gives up at the first such value, and the slow one begins again.
+    //
+    // Waves w and w + 4 share a SIMD: while one is at its products, the other is at its
+    // weights, and a barrier after each keeps it so.  (Left to themselves both did the same
+    // at a time.)  In step 2 n the first half of the waves add the values of tile n - 1 and
+    // multiply the keys of tile n, in step 2 n + 1 they turn scores into weights and set a
+    // tile on its way; the second half is a step behind, and a tile ahead with its loads.
+    // Tile n + 1 is there for all after step 2 n + 1.
+    auto run = [&](auto slow) {
+      constexpr bool kSlow = decltype(slow)::value;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // row of the operand to key: bits 2 and 3 change places
-          const uint32_t key = 32 * h + ((l32 & 19) | ((l32 & 4) << 1) | ((l32 & 8) >> 1));
+      for (int i = 0; i < RT; ++i) {
+        ref[i] = -INFINITY;
+        l[i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < RT; ++i) s[i][h] = floatx16{};
+        for (int d = 0; d < DT; ++d) o[i][d] = floatx16{};
+      }
+      const uint32_t tiles = it.k0 < it.k1 ? (it.k1 - it.k0 + T::kKeys - 1) / T::kKeys : 0;
+      if (tiles == 0) return true;
+      coming = ask(0);
+      // bits of the missing groups of the tile at the products, and of those after it
+      uint32_t absent = load(0), absent1 = 0, absent2 = 0, ahead = 1;
+      if (ahead < tiles) absent1 = load(ahead++);
+      if (group && ahead < tiles) absent2 = load(ahead++);
+      if (ahead == 3) loads_wait<2 * kLoads>();
+      else if (ahead == 2) loads_wait<kLoads>();
+      else loads_wait<0>();
+      lds_barrier();
+      if (edge(0, absent) && mend(0, absent) && !kSlow) return false;
+
+      floatx16 s[RT][NH];
+      u32x4 p[RT][2 * NH];
+      // Operands are read a step of four ahead of the products that take them.  Pieces 2 x on
+      // from the first lie at its place with 2 x flipped, whatever the row: one register
+      // addresses them all (with one each, some were kept in memory, and fetching those
+      // waited for all loads of the next tile).  Row of the operand to key: bits 2 and 3
+      // change places.
+      const uint32_t k_first = T::k_at((l32 & 19) | ((l32 & 4) << 1) | ((l32 & 8) >> 1), half);
+      const uint32_t v_first = T::v_at(l32, half);
+      constexpr int kStep = 4, NK = NH * KS / kStep, NV = 2 * NH * DT / kStep;
+      u32x4 kf[2][kStep], vf[2][kStep];
+      auto read_keys = [&](uint32_t buf, int i) {
 #pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            const u32x4 kf = bk[T::k_at(key, 2 * x + half)];
-#pragma unroll
-            for (int i = 0; i < RT; ++i) s[i][h] = mfma32<E>(kf, q[i][x], s[i][h]);
-          }
+        for (int e = 0; e < kStep; ++e) {
+          const int h = (kStep * i + e) / KS, x = (kStep * i + e) % KS;
+          kf[i & 1][e] = s_k[((buf * T::kPieces + k_first) ^ 2 * x) + 32 * h * T::kKPieces];
         }
-        // a lane's scores: keys kb + 32 h + 16 g + 8 half + e are element 8 g + e
-        if (kb + kKeys > all_see || absent_now) {
+      };
+      auto read_values = [&](uint32_t buf, int i) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+        for (int e = 0; e < kStep; ++e) {
+          const int g = (kStep * i + e) / DT, d = (kStep * i + e) % DT;
+          vf[i & 1][e] = s_v[((buf * T::kPieces + v_first) ^ 2 * g) + 32 * d * T::kVPieces];
+        }
+      };
+      // o += the weighted values of the tile in buffer `buf`, whose first operands are in hand;
+      // `then`: the buffer whose keys come next
+      auto add_values = [&](uint32_t buf, uint32_t then) {
+        if constexpr (!kSlow) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const uint32_t key = kb + 16 * g + 8 * half;
-              const uint32_t n = (absent_now >> (2 * g + half)) & 1 || key >= sees[i] ? 0u : min(sees[i] - key, 8u);
+          for (int n = 0; n < NV; ++n) {
+            if (n + 1 < NV) read_values(buf, n + 1);
+            else read_keys(then, 0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-              for (uint32_t e = 0; e < 8; ++e)
-                if (e >= n) s[i][g >> 1][8 * (g & 1) + e] = -INFINITY;
+            for (int e = 0; e < kStep; ++e) {
+              const int g = (kStep * n + e) / DT, d = (kStep * n + e) % DT;
+#pragma unroll
+              for (int i = 0; i < RT; ++i) o[i][d] = mfma32<E>(vf[n & 1][e], p[i][g], o[i][d]);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          float top = s[i][0][0];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(top, s[i][h][e]), s[i][h][e + 1]);
-          top = half_max(top) * a.scale;
-          if (__any(top > ref[i] + kSlack)) {
-            const float now = fmaxf(ref[i], top);
-            const float keep = ref[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[i] - now);
-            ref[i] = now;
-            l[i] *= keep;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[i][d] *= keep;
+            __builtin_amdgcn_sched_barrier(0);
           }
-          const float base = ref[i] == -INFINITY ? 0.f : ref[i];  // nothing seen: the weights are 2^-inf = 0
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[i][h][e] = __builtin_amdgcn_exp2f(fmaf(s[i][h][e], a.scale, -base));
-        }
-        if (!odd_now) {
-          u32x4 p[RT][4];
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                p[i][g][w] = E::pack2(s[i][g >> 1][8 * (g & 1) + 2 * w], s[i][g >> 1][8 * (g & 1) + 2 * w + 1]);
-                l[i] = E::add2(p[i][g][w], l[i]);
-              }
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const u32x4 vf = bv[T::v_at(32 * d + l32, 2 * g + half)];
-#pragma unroll
-              for (int i = 0; i < RT; ++i) o[i][d] = mfma32<E>(vf, p[i][g], o[i][d]);
-            }
         } else {
           // key by key, leaving out those of weight zero
-          const uint16_t* value = reinterpret_cast<const uint16_t*>(bv);
+          const uint16_t* value = reinterpret_cast<const uint16_t*>(s_v + buf * T::kPieces);
 #pragma unroll
           for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
               for (int e = 0; e < 16; ++e) l[i] += s[i][h][e];
 #pragma unroll 1
-          for (uint32_t x = 0; x < kKeys; ++x) {
+          for (uint32_t x = 0; x < T::kKeys; ++x) {
             uint32_t h_now = half;
             keep_here(h_now);
-            float p[RT];
+            float w[RT];
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-              p[i] = 0.f;
+              w[i] = 0.f;
 #pragma unroll
-              for (uint32_t e = 0; e < 32; ++e) p[i] = (x >> 4) * 8 + (x & 7) == e ? s[i][e >> 4][e & 15] : p[i];
-              p[i] = __shfl(p[i], ((x >> 3) & 1) * 32 + l32, 64);
+              for (uint32_t e = 0; e < 16 * NH; ++e) w[i] = (x >> 4) * 8 + (x & 7) == e ? s[i][e >> 4][e & 15] : w[i];
+              w[i] = __shfl(w[i], ((x >> 3) & 1) * 32 + l32, 64);
             }
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -536,12 +559,115 @@ __global__ __launch_bounds__(256, 1) void k_chunk_attention(ChunkArgs a) {
                 const float v = E::up(value[T::v_at(32 * d + (e & 3) + 4 * h_now + 8 * (e >> 2), x >> 3) * 8 + (x & 7)]);
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
-                  if (p[i] != 0.f) o[i][d][e] = fmaf(p[i], v, o[i][d][e]);
+                  if (w[i] != 0.f) o[i][d][e] = fmaf(w[i], v, o[i][d][e]);
               }
           }
         }
+      };
+
+      if (group) lds_barrier();
+      // after step 2 n + 1: waits for tile n + 1, all but the loads of the tile after it
+      auto arrive = [&](uint32_t n, uint32_t absent) {
+        if (ahead > n + 2) loads_wait<kLoads>();
+        else loads_wait<0>();
+        lds_barrier();
+        return n + 1 < tiles && edge(n + 1, absent) && mend(n + 1, absent) && !kSlow;
+      };
+      // scores of the tile in buffer `buf`, whose first operands are in hand
+      auto multiply = [&](uint32_t buf) {
+#pragma unroll
+        for (int m = 0; m < NK; ++m) {
+          if (m + 1 < NK) read_keys(buf, m + 1);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int e = 0; e < kStep; ++e) {
+            const int h = (kStep * m + e) / KS, x = (kStep * m + e) % KS;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) s[i][h] = mfma32<E>(kf[m & 1][e], q[i][x], x ? s[i][h] : floatx16{});
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if (works) {
+        read_keys(0, 0);
+        multiply(0);
       }
-      if (more) store(kb + kKeys, buf ^ 1);
+      for (uint32_t n = 0;; ++n) {
+        if (!group) lds_barrier();
+        else if (arrive(n, absent1)) return false;
+
+        const uint32_t kb = it.k0 + n * T::kKeys, buf = n % T::kBuffers, then = (n + 1) % T::kBuffers;
+        const uint32_t absent_now = absent;
+        absent = absent1;
+        absent1 = absent2;
+        if (ahead < tiles) {
+          const uint32_t x = load(ahead++);
+          (group ? absent2 : absent1) = x;
+        }
+        if (works) {
+          // a lane's scores: keys kb + 16 g + 8 half + e are element 8 (g & 1) + e of s[g / 2]
+          if (kb + T::kKeys > all_see || absent_now) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+              for (int g = 0; g < 2 * NH; ++g) {
+                const uint32_t key = kb + 16 * g + 8 * half;
+                const uint32_t seen = (absent_now >> (2 * g + half)) & 1 || key >= sees[i] ? 0u : min(sees[i] - key, 8u);
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e)
+                  if (e >= seen) s[i][g >> 1][8 * (g & 1) + e] = -INFINITY;
+              }
+          }
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            float top = s[i][0][0];
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(top, s[i][h][e]), s[i][h][e + 1]);
+            top = half_max(top) * a.scale;
+            if (__any(top > ref[i] + kSlack)) {
+              const float now = fmaxf(ref[i], top);
+              const float keep = ref[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[i] - now);
+              ref[i] = now;
+              l[i] *= keep;
+#pragma unroll
+              for (int d = 0; d < DT; ++d) o[i][d] *= keep;
+            }
+            const float base = ref[i] == -INFINITY ? 0.f : ref[i];  // nothing seen: the weights are 2^-inf = 0
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[i][h][e] = __builtin_amdgcn_exp2f(fmaf(s[i][h][e], a.scale, -base));
+            if constexpr (!kSlow) {
+#pragma unroll
+              for (int g = 0; g < 2 * NH; ++g)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  p[i][g][w] = E::pack2(s[i][g >> 1][8 * (g & 1) + 2 * w], s[i][g >> 1][8 * (g & 1) + 2 * w + 1]);
+                  l[i] = E::add2(p[i][g][w], l[i]);
+                }
+            }
+          }
+          if (!kSlow) read_values(buf, 0);
+        }
+        if (group) lds_barrier();
+        else if (arrive(n, absent)) return false;
+
+        if (works) add_values(buf, then);
+        if (n + 1 == tiles) break;
+        if (works) {
+          if (kSlow) read_keys(then, 0);
+          multiply(then);
+        }
+      }
+      if (!group) lds_barrier();
+      return true;
+    };
+    if (!run(std::false_type{})) {
+      loads_wait<0>();
+      __syncthreads();  // the buffers are refilled
+      run(std::true_type{});
     }
 
     const bool whole = it.keys <= piece;
@@ -586,9 +712,9 @@ __global__ __launch_bounds__(256, 1) void k_chunk_attention(ChunkArgs a) {
 
 // Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes
 // some rows of a tile, a thread four outputs of a row.
-template <class E, int DP, int RT>
+template <class E, int DP, int RT, int WAVES>
 __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
-  using P = PartOf<DP, RT>;
+  using P = PartOf<DP, RT, WAVES>;
   constexpr uint32_t kFours = DP / 4, kRowsEach = 256 / kFours, kSteps = P::kRows / kRowsEach;
   const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kCut], t = threadIdx.x;
   for (uint64_t unit = blockIdx.x; unit < (uint64_t)items * kSteps; unit += gridDim.x) {
@@ -642,16 +768,17 @@ bool chunk_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t
          (uint64_t)tokens * heads <= (1u << 30);
 }
 
-template <class E, int DP, int RT, bool PAD>
+template <class E, int DP, int RT, int WAVES, bool PAD>
 int launch_chunk(const ChunkArgs& a, hipStream_t st) {
-  const auto kernel = k_chunk_attention<E, DP, RT, PAD>;
-  if (Tile<DP>::kBytes > 64 * 1024 &&
+  using T = Tile<DP, WAVES>;
+  const auto kernel = k_chunk_attention<E, DP, RT, WAVES, PAD>;
+  if (T::kBytes > 64 * 1024 &&
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                          (int)Tile<DP>::kBytes) != hipSuccess)
+                          (int)T::kBytes) != hipSuccess)
     return DGT_E_HIP;
-  hipLaunchKernelGGL(kernel, dim3(kCUs), dim3(256), Tile<DP>::kBytes, st, a);
+  hipLaunchKernelGGL(kernel, dim3(kCUs), dim3(64 * WAVES), T::kBytes, st, a);
   if (int rc = launched()) return rc;
-  hipLaunchKernelGGL((k_chunk_join<E, DP, RT>), dim3(4 * kCUs), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_chunk_join<E, DP, RT, WAVES>), dim3(4 * kCUs), dim3(256), 0, st, a);
   return launched();
 }
 
@@ -665,10 +792,10 @@ int launch_chunk(const ChunkArgs& a, uint32_t dp, hipStream_t st) {
   if (int rc = launched()) return rc;
   const bool pad = a.dim != dp;
   switch (dp) {
-    case 64: return pad ? launch_chunk<E, 64, 2, true>(a, st) : launch_chunk<E, 64, 2, false>(a, st);
-    case 128: return pad ? launch_chunk<E, 128, 2, true>(a, st) : launch_chunk<E, 128, 2, false>(a, st);
+    case 64: return pad ? launch_chunk<E, 64, 1, 8, true>(a, st) : launch_chunk<E, 64, 1, 8, false>(a, st);
+    case 128: return pad ? launch_chunk<E, 128, 1, 8, true>(a, st) : launch_chunk<E, 128, 1, 8, false>(a, st);
   }
-  return pad ? launch_chunk<E, 256, 1, true>(a, st) : launch_chunk<E, 256, 1, false>(a, st);
+  return pad ? launch_chunk<E, 256, 1, 4, true>(a, st) : launch_chunk<E, 256, 1, 4, false>(a, st);
 }
 
 }  // namespace

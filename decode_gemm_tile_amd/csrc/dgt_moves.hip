@@ -272,8 +272,20 @@ __global__ __launch_bounds__(256) void k_page_fork(ForkArgs a) {
 #pragma unroll
         for (uint32_t n = 0; n < 4; ++n) {
           const uint32_t p = p0 + 256 * n;
-          if (p < k_pieces) ky[p] = v[n];
-          else if (p < each) vy[value_at(p - k_pieces)] = v[n];
+          if (p >= each) continue;
+          if (p < k_pieces) {
+            ky[p] = v[n];
+            continue;
+          }
+          const uint32_t at = value_at(p - k_pieces), tokens = rest - 8 * ((p - k_pieces) % v_row);
+          if (tokens >= 8) {
+            vy[at] = v[n];
+          } else {  // cells past the length stay as they are
+            uint16_t* one = reinterpret_cast<uint16_t*>(vy + at);
+#pragma unroll
+            for (uint32_t e = 0; e < 7; ++e)
+              if (e < tokens) one[e] = (uint16_t)(v[n][e / 2] >> 16 * (e & 1));
+          }
         }
       }
     }

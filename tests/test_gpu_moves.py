@@ -150,13 +150,11 @@ def _fork(d, src, dst, lens, layers, heads, dim, shares=None, dtype="bfloat16"):
     assert got.tolist() == ref_counts.tolist() and ls.tolist() == ref_lens.tolist()
     assert np.array_equal(table.cpu().numpy(), ref_table) and sh.tolist() == ref_shares.tolist()
     assert free.tolist() == list(d["free"])
-    k0, v0 = _bits(k), _bits(v)
+    k0, v0 = _bits(k).clone(), _bits(v).clone()
     k0, v0 = (x if layers is not None else x[None] for x in (k0, v0))
-    kg, vg = _bits(kd).view(k0.shape).clone(), _bits(vd).view(v0.shape).clone()
     for a, b, n in copies:
-        assert torch.equal(kg[:, b, :, :n], k0[:, a, :, :n]) and torch.equal(vg[:, b, :, :, :n], v0[:, a, :, :, :n])
-        kg[:, b], vg[:, b] = k0[:, b], v0[:, b]  # (what lies past the tokens is nobody's)
-    assert torch.equal(kg, k0) and torch.equal(vg, v0)
+        k0[:, b, :, :n], v0[:, b, :, :, :n] = k0[:, a, :, :n].clone(), v0[:, a, :, :, :n].clone()
+    assert torch.equal(_bits(kd).view(k0.shape), k0) and torch.equal(_bits(vd).view(v0.shape), v0)
     return ref_table, ref_lens, ref_shares, int(ref_counts[0])
 
 
