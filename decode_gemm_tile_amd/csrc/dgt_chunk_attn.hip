@@ -45,97 +45,108 @@ struct Plan {
   static constexpr uint32_t kItems = 129;      // in all
   static constexpr uint32_t kCut = 130;        // items among which those of cut tiles are
   static constexpr uint32_t kZeros = 144;      // 16 bytes
-  static constexpr uint32_t kOrder = 160;      // [requests]: request number, longest first
-  static __host__ __device__ constexpr uint32_t item0(uint32_t requests) { return kOrder + requests; }  // [requests], first item
-  static __host__ __device__ constexpr uint32_t part0(uint32_t requests) { return kOrder + 2 * requests; }  // [requests], first part
-  static __host__ __device__ constexpr uint32_t words(uint32_t requests) { return kOrder + 3 * requests; }
+  static constexpr uint32_t kRecord = 160;     // [requests][kWords], the longest request first
+  static constexpr uint32_t kWords = 8;        // item, part: the first ones; request, first row, rows, cached keys
+  static __host__ __device__ constexpr uint32_t words(uint32_t requests) { return kRecord + kWords * requests; }
 };
 
 struct Chunk {  // one request
   uint32_t first, count, ctx, keys, tiles;
 };
 
+__device__ __forceinline__ void size_chunk(const ChunkArgs& a, Chunk& c) {
+  c.keys = min(c.ctx + c.count, a.width << a.log_block);
+  c.tiles = (c.count + a.tile_tokens - 1) / a.tile_tokens * a.splits;
+}
+
 __device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, uint32_t b) {
   Chunk c;
   request_rows(a.cu, b, a.tokens, &c.first, &c.count);
-  const uint32_t room = a.width << a.log_block;
-  c.ctx = min((uint32_t)max(a.ctx[b], 0), room);
-  c.keys = min(c.ctx + c.count, room);
-  c.tiles = (c.count + a.tile_tokens - 1) / a.tile_tokens * a.splits;
+  c.ctx = min((uint32_t)max(a.ctx[b], 0), a.width << a.log_block);
+  size_chunk(a, c);
   return c;
 }
 
-template <int THREADS>
-__device__ __forceinline__ float sum_all(float v, float* s) {
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m, 64);
-  __syncthreads();
-  if (lane == 0) s[wave] = v;
-  __syncthreads();
-  float all = 0.f;
-  for (int w = 0; w < THREADS / 64; ++w) all += s[w];
-  return all;
-}
-
 // One workgroup: how long pieces are, and the requests' items.  In units of a tile of 64
-// keys, a call takes about its work over the CUs and a last piece; or one piece where no
-// CU gets two; and a part written and read again costs as much as kPart of them.
-constexpr uint32_t kPlanThreads = 256, kMaxSorted = 1024;
+// keys, a call takes one piece where no CU gets two; else its work over the CUs, or a
+// piece if that is more, and half an item, as the longest go first.  A part written and
+// read again costs as much as kPart of them.
+constexpr uint32_t kPlanThreads = 256, kMaxSorted = 1024, kChoices = 32;
 constexpr float kPart = 6.f;
 
+template <class T, class F>
+__device__ __forceinline__ T reduce_all(T v, T* s, F f) {  // over the workgroup, to all threads
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v = f(v, __shfl_xor(v, m, 64));
+  if (lane == 0) s[wave] = v;
+  __syncthreads();
+  v = s[0];
+  for (uint32_t w = 1; w < kPlanThreads / 64; ++w) v = f(v, s[w]);
+  __syncthreads();
+  return v;
+}
+
 __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
-  extern __shared__ uint32_t s_keys[];  // [requests], then [requests] sorted
-  __shared__ float s_sum[kPlanThreads / 64];
-  __shared__ uint32_t s_scan[kPlanThreads / 64];
+  extern __shared__ uint32_t s_keys[];  // [requests] keys, [requests] tiles, [requests] the order
+  uint32_t *s_tiles = s_keys + a.requests, *s_order = s_tiles + a.requests;
+  __shared__ float s_f[kPlanThreads / 64], s_items[kPlanThreads], s_parts[kPlanThreads];
+  __shared__ uint32_t s_u[kPlanThreads / 64], s_v[kPlanThreads / 64];
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
   float work = 0.f, rows = 0.f;
   uint32_t most = 0;
   for (uint32_t b = t; b < a.requests; b += kPlanThreads) {
     const Chunk c = chunk_of(a, b);
     s_keys[b] = c.tiles ? c.keys : 0;
+    s_tiles[b] = c.tiles;
     // (their mean length: the first tiles see half of the new tokens less)
     work += (float)c.tiles * ((float)(c.keys + min(c.ctx, c.keys)) * (0.5f / kKeys) + 1.f);
     rows += (float)c.count;
     most = max(most, s_keys[b]);
   }
-  work = sum_all<kPlanThreads>(work, s_sum) * (float)a.heads;
+  auto add = [](float x, float y) { return x + y; };
+  work = reduce_all(work, s_f, add) * (float)a.heads;
   // Offsets that fall name rows again and again, and no bound on items holds: such a batch
   // is not computed.  (Sums up to 2^24 are exact, and `tokens` is 2^20 at most.)
-  const bool sound = sum_all<kPlanThreads>(rows, s_sum) <= (float)a.tokens;
+  const bool sound = reduce_all(rows, s_f, add) <= (float)a.tokens;
+  most = reduce_all(most, s_u, [](uint32_t x, uint32_t y) { return max(x, y); });
+
+  // Choice i cuts the longest tile into about 1.25^i pieces; 32 choices side by side, each
+  // over the requests in eight strides.
+  const uint32_t units = max((most + kKeys - 1) / kKeys, 1u), choice = t % kChoices;
+  const uint32_t len = max((uint32_t)ceilf((float)units * exp2f(-0.32192809f * (float)choice)), min(units, 2u));
+  float items = 0.f, parts = 0.f;
+  for (uint32_t b = t / kChoices; b < a.requests; b += kPlanThreads / kChoices) {
+    const uint32_t n = (uint32_t)(((uint64_t)s_keys[b] + len * kKeys - 1) / (len * kKeys));
+    items += (float)s_tiles[b] * (float)max(n, 1u);
+    if (n > 1) parts += (float)s_tiles[b] * (float)n;
+  }
+  s_items[t] = items;
+  s_parts[t] = parts;
+  __syncthreads();
+  items = parts = 0.f;
+  for (uint32_t i = choice; i < kPlanThreads; i += kChoices) {
+    items += s_items[i];
+    parts += s_parts[i];
+  }
+  items *= (float)a.heads;
+  parts *= (float)a.heads;
+  float time = items <= (float)kCUs ? (float)len : fmaxf(work / kCUs, (float)len) + 0.5f * work / items;
+  if (parts > 0.f) time += kPart + parts * (kPart / kCUs);
+  if (choice && parts > (float)kMostParts) time = 3.4e38f;
+  uint32_t piece = len;
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, m, 64));
-  __syncthreads();
-  if (lane == 0) s_scan[wave] = most;
-  __syncthreads();
-  for (uint32_t w = 0; w < kPlanThreads / 64; ++w) most = max(most, s_scan[w]);
-  const float longest = ceilf((float)most / kKeys);
-  float best = 3.4e38f;
-  uint32_t piece = max((most + kKeys - 1) / kKeys, 1u);
-  for (uint32_t k = 1; k <= 64; k += k < 4 ? 1 : k / 4) {
-    const uint32_t len = max((uint32_t)ceilf(longest / (float)k), 2u);
-    float items = 0.f, parts = 0.f;
-    for (uint32_t b = t; b < a.requests; b += kPlanThreads) {
-      const Chunk c = chunk_of(a, b);
-      const uint32_t n = (c.keys + len * kKeys - 1) / (len * kKeys);
-      items += (float)c.tiles * (float)max(n, 1u);
-      if (n > 1) parts += (float)c.tiles * (float)n;
-    }
-    items = sum_all<kPlanThreads>(items, s_sum) * (float)a.heads;
-    parts = sum_all<kPlanThreads>(parts, s_sum) * (float)a.heads;
-    if (parts > (float)kMostParts) break;
-    const float share = parts * (kPart / kCUs);
-    const float time = (items <= (float)kCUs ? (float)len : work / kCUs + (float)len) + (parts > 0.f ? kPart + share : 0.f);
-    if (time < best) {
-      best = time;
-      piece = len;
+  for (int m = 1; m < (int)kChoices; m <<= 1) {
+    const float ot = __shfl_xor(time, m, 64);
+    const uint32_t ol = (uint32_t)__shfl_xor((int)piece, m, 64);
+    if (ot < time || (ot == time && ol > piece)) {
+      time = ot;
+      piece = ol;
     }
   }
   piece *= kKeys;
 
   // requests by their longest tile, descending (of equals, the first first)
-  uint32_t* s_order = s_keys + a.requests;
-  __syncthreads();
   for (uint32_t b = t; b < a.requests; b += kPlanThreads) {
     uint32_t rank = b;
     if (a.requests <= kMaxSorted) {
@@ -146,18 +157,18 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
     s_order[rank] = b;
   }
   __syncthreads();
-  uint32_t items = 0, parts = 0;
+  uint32_t item = 0, part = 0;
   for (uint32_t i0 = 0; i0 < a.requests; i0 += kPlanThreads) {
     const uint32_t i = i0 + t;
+    Chunk c = {};
     uint32_t n = 0, p = 0;
     if (i < a.requests) {
-      const Chunk c = chunk_of(a, s_order[i]);
-      const uint32_t pieces = max((c.keys + piece - 1) / piece, 1u);
+      c = chunk_of(a, s_order[i]);
+      const uint32_t pieces = max((uint32_t)(((uint64_t)c.keys + piece - 1) / piece), 1u);
       n = c.tiles * pieces * a.heads;
       p = pieces > 1 ? n : 0;
     }
-    // exclusive sums of both
-    uint32_t sn = n, sp = p;
+    uint32_t sn = n, sp = p;  // running sums of both
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const uint32_t on = __shfl_up(sn, d, 64), op = __shfl_up(sp, d, 64);
@@ -166,36 +177,37 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
         sp += op;
       }
     }
-    __syncthreads();
     if (lane == 63) {
-      s_scan[wave] = sn;
-      s_sum[wave] = __uint_as_float(sp);
+      s_u[wave] = sn;
+      s_v[wave] = sp;
     }
     __syncthreads();
-    uint32_t bn = items, bp = parts;
+    uint32_t bn = item, bp = part;
     for (uint32_t w = 0; w < kPlanThreads / 64; ++w) {
       if (w == wave) {
         sn += bn;
         sp += bp;
       }
-      bn += s_scan[w];
-      bp += __float_as_uint(s_sum[w]);
+      bn += s_u[w];
+      bp += s_v[w];
     }
+    __syncthreads();
     if (i < a.requests) {
-      a.plan[Plan::kOrder + i] = s_order[i];
-      a.plan[Plan::item0(a.requests) + i] = sn - n;
-      a.plan[Plan::part0(a.requests) + i] = sp - p;
+      u32x4* r = reinterpret_cast<u32x4*>(a.plan + Plan::kRecord + Plan::kWords * i);
+      r[0] = u32x4{sn - n, sp - p, s_order[i], c.first};
+      r[1] = u32x4{c.count, c.ctx, 0u, 0u};
     }
-    items = bn;
-    parts = bp;
+    item = bn;
+    part = bp;
   }
-  if (t < kDies) a.plan[Plan::kQueue + 16 * t] = 0;
+  // every workgroup begins with the item of its own number
+  if (t < kDies) a.plan[Plan::kQueue + 16 * t] = kCUs / kDies;
   if (t < 4) a.plan[Plan::kZeros + t] = 0;
   if (t == 0) {
     a.plan[Plan::kPiece] = piece;
-    a.plan[Plan::kItems] = sound ? items : 0;
+    a.plan[Plan::kItems] = sound ? item : 0;
     // cut tiles come first where requests are sorted
-    a.plan[Plan::kCut] = !sound || parts == 0 ? 0 : a.requests <= kMaxSorted ? parts : items;
+    a.plan[Plan::kCut] = !sound || part == 0 ? 0 : a.requests <= kMaxSorted ? part : item;
   }
 }
 
@@ -211,26 +223,28 @@ struct Item {
 // Item x of the call.  Of a request: tiles from the last, which sees most, pieces, heads.
 __device__ __forceinline__ Item item_of(const ChunkArgs& a, uint32_t x, uint32_t piece, uint32_t rows) {
   const uint32_t lane = threadIdx.x & 63;
-  const uint32_t* item0 = a.plan + Plan::item0(a.requests);
+  const uint32_t* records = a.plan + Plan::kRecord;
   uint32_t lo = 0, len = a.requests;
   while (len > 1) {
     const uint32_t step = (len + 63) / 64, at = lane * step;
-    const bool before = lane == 0 || (at < len && item0[lo + at] <= x);
+    const bool before = lane == 0 || (at < len && records[Plan::kWords * (lo + at)] <= x);
     const uint32_t hits = (uint32_t)__popcll(__ballot(before));
     const uint32_t skip = (hits - 1) * step;
     lo += skip;
     len = min(step, len - skip);
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
+  const u32x4* record = reinterpret_cast<const u32x4*>(records + Plan::kWords * (uint32_t)__builtin_amdgcn_readfirstlane(lo));
+  const u32x4 r0 = record[0], r1 = record[1];
   Item it;
-  it.b = a.plan[Plan::kOrder + lo];
-  it.c = chunk_of(a, it.b);
-  it.pieces = max((it.c.keys + piece - 1) / piece, 1u);
-  const uint32_t in = x - item0[lo], rest = in / a.heads;
+  it.b = r0[2];
+  it.c = Chunk{r0[3], r1[0], r1[1], 0, 0};
+  size_chunk(a, it.c);
+  it.pieces = max((uint32_t)(((uint64_t)it.c.keys + piece - 1) / piece), 1u);
+  const uint32_t in = x - r0[0], rest = in / a.heads;
   it.head = in - rest * a.heads;
   it.piece = rest % it.pieces;
   it.tile = it.c.tiles - 1 - rest / it.pieces;
-  it.part = a.plan[Plan::part0(a.requests) + lo] + in;
+  it.part = r0[1] + in;
   const uint32_t split = it.tile % a.splits;
   it.token = it.tile / a.splits * a.tile_tokens;
   it.tokens = min(it.c.count - it.token, a.tile_tokens);
@@ -351,7 +365,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
 
   uint32_t queue = blockIdx.x % kDies, tried = 0;
   auto draw = [&] { return __hip_atomic_fetch_add(a.plan + Plan::kQueue + 16 * queue, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  uint32_t drawn = t == 0 ? draw() : 0;
+  uint32_t drawn = blockIdx.x / kDies;
   for (;;) {
     if (t == 0) {
       uint32_t x = ~0u;
@@ -722,18 +736,31 @@ __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
     if (it.piece || it.keys <= piece) continue;
     const uint32_t r = (uint32_t)(unit % kSteps) * kRowsEach + t / kFours, d = 4 * (t % kFours);
     if (r >= it.rows()) continue;
+    // item numbers of a tile's pieces lie `heads` apart; four are asked for at a time
     float m = -INFINITY, l = 0.f;
     floatx4 o = {};
-    // item numbers of a tile's pieces lie `heads` apart
+    const uint32_t count = (it.keys + piece - 1) / piece;
     const float* part = a.parts + (uint64_t)it.part * P::kFloats;
-    for (uint32_t k = 0; k < it.keys; k += piece, part += (uint64_t)a.heads * P::kFloats) {
-      const float mw = part[r], lw = part[P::kRows + r];
-      const floatx4 ow = *reinterpret_cast<const floatx4*>(part + 2 * P::kRows + r * DP + d);
-      const float now = fmaxf(m, mw), base = now == -INFINITY ? 0.f : now;
-      const float f = __builtin_amdgcn_exp2f(m - base), fw = __builtin_amdgcn_exp2f(mw - base);
-      m = now;
-      l = fmaf(lw, fw, l * f);
-      o = o * f + ow * fw;
+    const uint64_t step = (uint64_t)a.heads * P::kFloats;
+    for (uint32_t k0 = 0; k0 < count; k0 += 4) {
+      float mw[4], lw[4];
+      floatx4 ow[4];
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) {
+        const float* from = part + min(k0 + k, count - 1) * step;
+        mw[k] = from[r];
+        lw[k] = from[P::kRows + r];
+        ow[k] = *reinterpret_cast<const floatx4*>(from + 2 * P::kRows + r * DP + d);
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) {
+        if (k0 + k >= count) break;
+        const float now = fmaxf(m, mw[k]), base = now == -INFINITY ? 0.f : now;
+        const float f = __builtin_amdgcn_exp2f(m - base), fw = __builtin_amdgcn_exp2f(mw[k] - base);
+        m = now;
+        l = fmaf(lw[k], fw, l * f);
+        o = o * f + ow[k] * fw;
+      }
     }
     if (d >= a.dim) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -784,8 +811,8 @@ int launch_chunk(const ChunkArgs& a, hipStream_t st) {
 
 template <class E>
 int launch_chunk(const ChunkArgs& a, uint32_t dp, hipStream_t st) {
-  const uint32_t lds = 2 * a.requests * 4;  // 64 KB at most
-  if (lds > 63 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_chunk_plan),
+  const uint32_t lds = 3 * a.requests * 4;  // 96 KB at most
+  if (lds > 60 * 1024 && hipFuncSetAttribute(reinterpret_cast<const void*>(k_chunk_plan),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
     return DGT_E_HIP;
   hipLaunchKernelGGL(k_chunk_plan, dim3(1), dim3(kPlanThreads), lds, st, a);
