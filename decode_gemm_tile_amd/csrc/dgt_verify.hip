@@ -7,13 +7,32 @@ namespace dgt {
 namespace serve {
 namespace {
 
+// A request's path starts at row 0 and goes down its tree or chain; an end's largest logit
+// and sum of exponentials decide about the drafted tokens that follow it (the sum is fp32:
+// a draft whose number lies within 2^-20 or so of the border may fall either way).  A
+// workgroup looks at one segment of one row.  The last to come for a row that is the path's
+// end decides, and goes on if the row after it is complete too; else whoever completes
+// that one does.  Nobody waits.  Rows come in the order of their index within the request,
+// so a row's turn is mostly after the decisions above it, and one that the path has
+// passed by is not read: of 64 trees of up to 27 nodes, a third is.
+//
+// Then the next token out of the last row: a uniform number falls between two of a
+// vocabulary's running sums, which lie 1 / vocab apart on the average; sums of fp32
+// exponentials, off by 2^-24, would give another token in one of a hundred calls, so
+// this row's weights are formed in fp64, a workgroup a segment, and the request's last
+// workgroup chooses.  Where a chain was refused the weights are max(p - q, 0), p needs
+// the whole row's sum first, and one more launch forms them.
 struct VerifyArgs {
   const void* logits;
   const float *probs, *temperature, *accept, *sample;
   const int32_t *draft, *parents, *cu;
   int32_t *path, *accepted, *next;
-  struct Part* parts;       // [tokens][segs]
-  double* rest;             // [requests][segs], sums of max(p - q, 0)
+  uint64_t* parts;          // [tokens][segs][2], see Part
+  uint32_t* order;          // [tokens][2]: rows in their turn, and their requests
+  uint32_t* counters;       // [tokens]: parts that are there, and one for a row on the path
+  struct State* states;     // [requests]
+  double* sums;             // [requests][segs]: of a last row's weights, then of max(p - q, 0)
+  double* rest;
   struct End* ends;         // [requests]
   uint64_t logits_row, probs_row;
   uint32_t requests, tokens, vocab, segs;
@@ -23,36 +42,63 @@ struct VerifyArgs {
 // A row's vocabulary in segments; a segment of a row is what one workgroup looks at.
 constexpr uint32_t kSeg = 4096, kThreads = 256, kEach = kSeg / kThreads;
 
-struct Part {  // of a segment
-  double sum;  // of exp((l - top) / T)
-  float top;   // the largest logit; NaN if there is a NaN
-  uint32_t at; // its place, the first of equals (within the vocabulary)
+// What is known of a segment: sum of exp((l - top) / T), top (NaN if there is a NaN), the
+// largest logit's place (the first of equals, within the vocabulary).  Parts, counters and
+// states pass between workgroups that may sit on different dies: agent-scope accesses, and a
+// wait for the stores before whatever tells of them.
+struct Part {
+  float sum, top;
+  uint32_t at;
+};
+__device__ __forceinline__ void put(uint64_t* p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint64_t get(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint32_t count_in(uint32_t* p) { return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// A request's path so far: its end's index in the low half (kOver: it is decided), its length.
+struct State {
+  uint64_t path;
+};
+constexpr uint32_t kOver = 0x7FFFFFFF;
+
+enum Mode : uint32_t { kDone, kFromTarget, kFromRest };
+struct End {  // of a path
+  uint32_t mode, row, counter, rest_counter;
+  float top;     // of the row
+  uint32_t at;   // the largest logit's place
+  uint32_t end;  // the row within its request
+  uint32_t lost; // children of it were refused
 };
 
-struct End {  // of a path whose next token comes from max(p - q, 0)
-  double sum;      // of exp((l - top) / T) over the row
-  float top;
-  uint32_t row, counter;  // row: ~0 where there is nothing to do
-};
-
-// 2^z for z <= 0 in fp64: the Taylor series of 2^f on |f| <= 1/2 ends below 2^-37.  A
-// uniform number falls between two of a vocabulary's running sums, which lie 1 / vocab
-// apart: sums of fp32 exponentials, off by 2^-24, would give another token in one of a
-// hundred calls.  Far values are cut at 2^-1100, which is zero.
+// 2^z for z <= 0 in fp64, off by 2^-39: the polynomial of degree 8 that meets 2^f in the nine
+// Chebyshev points of |f| <= 1/2.  z is cut at -1000, whose power is as good as zero; the
+// whole number is read out of the low bits of z + 1.5 * 2^52.
+// (Eight side by side: one after another, each step waits for the one before.)
+template <int N>
+__device__ __forceinline__ void exp2_64(double (&z)[N]) {
+  constexpr double kRound = 6755399441055744.0;
+  constexpr double kC[9] = {1.3255224878668817e-06, 1.5310079402249296e-05, 0.00015403455852453838,
+                            0.0013333450568000645,  0.009618129159402558,   0.05550410941205933,
+                            0.2402265069581299,     0.6931471805459335,     1.0};
+  double f[N], p[N];
+  uint32_t n[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const double cut = fmax(z[e], -1000.0), whole = cut + kRound;
+    n[e] = (uint32_t)__builtin_bit_cast(uint64_t, whole);
+    f[e] = cut - (whole - kRound);
+    p[e] = kC[0];
+  }
+#pragma unroll
+  for (int k = 1; k < 9; ++k)
+#pragma unroll
+    for (int e = 0; e < N; ++e) p[e] = fma(p[e], f[e], kC[k]);
+#pragma unroll
+  for (int e = 0; e < N; ++e) z[e] = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, p[e]) + ((uint64_t)n[e] << 52));
+}
 __device__ __forceinline__ double exp2_64(double z) {
-  z = fmax(z, -1100.0);
-  const double n = __builtin_rint(z), f = z - n;
-  double p = 1.01780860092396997e-7;  // ln(2)^k / k!
-  p = fma(p, f, 1.32154867901443095e-6);
-  p = fma(p, f, 1.52527338040598403e-5);
-  p = fma(p, f, 1.54035303933816099e-4);
-  p = fma(p, f, 1.33335581464284434e-3);
-  p = fma(p, f, 9.61812910762847716e-3);
-  p = fma(p, f, 5.55041086648215800e-2);
-  p = fma(p, f, 2.40226506959100712e-1);
-  p = fma(p, f, 6.93147180559945309e-1);
-  p = fma(p, f, 1.0);
-  return __builtin_ldexp(p, (int)n);
+  double one[1] = {z};
+  exp2_64<1>(one);
+  return one[0];
 }
 
 constexpr double kLog2e = 1.44269504088896340736;
@@ -61,6 +107,7 @@ __device__ __forceinline__ double heat(const VerifyArgs& a, uint32_t b) {
   const float t = a.temperature ? a.temperature[b] : 1.f;
   return t > 0.f ? kLog2e / (double)t : 0.0;
 }
+__device__ __forceinline__ float heat32(double c) { return (float)fmin(c, 3e38); }
 
 template <class E>
 struct Logit {
@@ -95,18 +142,18 @@ __device__ __forceinline__ uint32_t place(uint32_t e) {
   return (e / L::kPiece * kThreads + threadIdx.x) * L::kPiece + e % L::kPiece;
 }
 
-// A segment's elements of a row; past the vocabulary's end -inf.
-template <class L>
-__device__ __forceinline__ void load_segment(const void* base, uint64_t row, uint32_t seg, uint32_t vocab, bool wide,
-                                             float (&x)[kEach]) {
+// A segment's elements at the thread's places; past the vocabulary's end `none`.
+template <class L, class F>
+__device__ __forceinline__ void load_places(const void* base, uint64_t row, uint32_t seg, uint32_t vocab, bool wide, float none,
+                                            F at, float (&x)[kEach]) {
   const typename L::T* p = static_cast<const typename L::T*>(base) + row + (uint64_t)seg * kSeg;
   const uint32_t left = vocab - seg * kSeg;
   if (wide && left >= kSeg) {
 #pragma unroll
-    for (uint32_t e = 0; e < kEach; e += L::kPiece) L::piece(p + place<L>(e), x + e);
+    for (uint32_t e = 0; e < kEach; e += L::kPiece) L::piece(p + at(e), x + e);
   } else {
 #pragma unroll
-    for (uint32_t e = 0; e < kEach; ++e) x[e] = place<L>(e) < left ? L::one(p, place<L>(e)) : -INFINITY;
+    for (uint32_t e = 0; e < kEach; ++e) x[e] = at(e) < left ? L::one(p, at(e)) : none;
   }
 }
 
@@ -123,106 +170,223 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// Largest logit, its place and the sum of exponentials of a segment, to every thread.
-template <class L>
-__device__ __forceinline__ Part segment_part(const float (&x)[kEach], uint32_t seg, double c, float* s_top, uint32_t* s_at,
-                                             double* s_sum) {
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float top = -INFINITY;
-  uint32_t at = 0xFFFFFFFFu;
-  bool odd = false;
-#pragma unroll
-  for (uint32_t e = 0; e < kEach; ++e) {
-    odd |= x[e] != x[e];
-    const bool take = x[e] > top || at == 0xFFFFFFFFu;  // places rise with e
-    top = take ? x[e] : top;
-    at = take ? seg * kSeg + place<L>(e) : at;
-  }
-  top = odd ? -INFINITY : top;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) better(top, at, __shfl_xor(top, m, 64), __shfl_xor(at, m, 64));
-  odd = __any(odd);
-  if (lane == 0) {
-    s_top[wave] = odd ? NAN : top;
-    s_at[wave] = at;
-  }
-  __syncthreads();
-  top = s_top[0];
-  at = s_at[0];
-#pragma unroll
-  for (int w = 1; w < 4; ++w) {
-    odd |= s_top[w] != s_top[w];
-    better(top, at, s_top[w], s_at[w]);
-  }
-  odd |= s_top[0] != s_top[0];
-  double sum = 0.0;
-  if (c > 0.0 && top > -INFINITY && !odd) {
-#pragma unroll
-    for (uint32_t e = 0; e < kEach; ++e) sum += exp2_64(((double)x[e] - (double)top) * c);
-  }
-  sum = wave_sum(sum);
-  if (lane == 0) s_sum[wave] = sum;
-  __syncthreads();
-  return Part{(s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]), odd ? NAN : top, at};
-}
-
-// The request of a row: the last that begins at or before it.
-__device__ __forceinline__ uint32_t row_request(const VerifyArgs& a, uint32_t row) {
-  const uint32_t lane = threadIdx.x & 63;
-  uint32_t lo = 0, len = a.requests;
-  while (len > 1) {
-    const uint32_t step = (len + 63) / 64, at = lane * step;
-    const bool before = lane == 0 || (at < len && (uint32_t)max(a.cu[lo + at], 0) <= row);
-    const uint32_t hits = (uint32_t)__popcll(__ballot(before));
-    const uint32_t skip = (hits - 1) * step;
-    lo += skip;
-    len = min(step, len - skip);
-  }
-  return lo;
-}
-
-// Every segment of every row.
-template <class L>
-__global__ __launch_bounds__(kThreads) void k_verify_parts(VerifyArgs a) {
-  __shared__ float s_top[4];
-  __shared__ uint32_t s_at[4];
-  __shared__ double s_sum[4];
-  const uint32_t row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
-  float x[kEach];
-  load_segment<L>(a.logits, row * a.logits_row, seg, a.vocab, a.wide, x);
-  const uint32_t b = row_request(a, row);
-  uint32_t first, count;
-  request_rows(a.cu, b, a.tokens, &first, &count);
-  if (row - first >= count) return;  // of no request
-  const Part p = segment_part<L>(x, seg, heat(a, b), s_top, s_at, s_sum);
-  if (threadIdx.x == 0) a.parts[(uint64_t)row * a.segs + seg] = p;
-}
-
+// A thread's, a wave's or a workgroup's share of a row.
 struct RowSum {
-  double sum;
-  float top;
-  uint32_t at;
-  bool sound;
+  float sum, top;  // sum of exp((l - top) / T)
+  uint32_t at;     // the largest logit's place
+  bool odd;        // a NaN
+  static __device__ __forceinline__ RowSum none() { return RowSum{0.f, -INFINITY, 0xFFFFFFFFu, false}; }
+  __device__ __forceinline__ void join(float osum, float otop, uint32_t oat, bool oodd, float c) {
+    const float now = fmaxf(top, otop);
+    if (now > -INFINITY)
+      sum = sum * __builtin_amdgcn_exp2f((top - now) * c) + osum * __builtin_amdgcn_exp2f((otop - now) * c);
+    better(top, at, otop, oat);
+    odd |= oodd;
+  }
+  __device__ __forceinline__ void across_wave(float c) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+      join(__shfl_xor(sum, m, 64), __shfl_xor(top, m, 64), __shfl_xor(at, m, 64), __shfl_xor((int)odd, m, 64), c);
+  }
+  // a softmax exists
+  __device__ __forceinline__ bool sound() const { return !odd && top > -INFINITY && top < INFINITY; }
 };
 
-// A row's parts together, by each wave for itself.
-__device__ __forceinline__ RowSum join_row(const Part* parts, uint32_t segs, double c) {
-  const uint32_t lane = threadIdx.x & 63;
-  float top = -INFINITY;
-  uint32_t at = 0xFFFFFFFFu;
-  bool odd = false;
-  for (uint32_t s = lane; s < segs; s += 64) {
-    odd |= parts[s].top != parts[s].top;
-    better(top, at, parts[s].top, parts[s].at);
-  }
+// N elements at places that rise: their largest first, then the sum against it.  (Infinities
+// make sums that are not numbers, but then the row is not sound.)
+template <int N, class F>
+__device__ __forceinline__ void add_elements(RowSum& r, const float (&x)[N], F place, float c) {
+  float top = x[0];
+  uint32_t at = place(0);
+  bool odd = x[0] != x[0];
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) better(top, at, __shfl_xor(top, m, 64), __shfl_xor(at, m, 64));
-  odd = __any(odd) || !(top > -INFINITY && top < INFINITY);
-  double sum = 0.0;
-  if (!odd && c > 0.0)
-    for (uint32_t s = lane; s < segs; s += 64)
-      if (parts[s].sum > 0.0) sum += parts[s].sum * exp2_64(((double)parts[s].top - (double)top) * c);
-  return RowSum{wave_sum(sum), top, at, !odd};
+  for (int e = 1; e < N; ++e) {
+    odd |= x[e] != x[e];
+    const bool take = x[e] > top;
+    top = take ? x[e] : top;
+    at = take ? place(e) : at;
+  }
+  float sum = 0.f;
+  if (c > 0.f && top > -INFINITY)
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum += __builtin_amdgcn_exp2f((x[e] - top) * c);
+  r.join(sum, top, at, odd, c);
+}
+
+// Before all: rows in the order of their index within the request, no counts, paths of row
+// 0 alone.  Offsets that fall have no such order; their rows come as they are.
+__global__ __launch_bounds__(kThreads) void k_verify_begin(VerifyArgs a) {
+  extern __shared__ uint32_t s_cu[];  // [requests + 1]
+  const uint32_t t = threadIdx.x, row = blockIdx.x * kThreads + t;
+  bool falls = false;
+  for (uint32_t b = t; b <= a.requests; b += kThreads) {
+    s_cu[b] = (uint32_t)min(max(a.cu[b], 0), (int)a.tokens);
+    falls |= b < a.requests && a.cu[b] > a.cu[b + 1];
+  }
+  falls = __syncthreads_or(falls);
+  if (row < a.requests) {
+    a.states[row].path = 1ull << 32;
+    a.ends[row].mode = kDone;
+    a.accepted[row] = 0;
+    a.next[row] = -1;
+  }
+  if (row >= a.tokens) return;
+  uint32_t b = 0, hi = a.requests;  // the last request that begins at or before the row
+  while (hi - b > 1) {
+    const uint32_t mid = (b + hi) >> 1;
+    if (s_cu[mid] <= row) b = mid; else hi = mid;
+  }
+  const uint32_t first = s_cu[b], count = max(s_cu[b + 1], first) - first, j = row - first;
+  const bool live = row >= first && j < count;
+  uint32_t turn = row;
+  if (!falls) {
+    if (live) {
+      turn = 0;
+      for (uint32_t o = 0; o < a.requests; ++o) {
+        const uint32_t n = s_cu[o + 1] - s_cu[o];
+        turn += min(n, j) + (o < b && n > j);
+      }
+    } else {  // behind all of them
+      turn = s_cu[a.requests] - s_cu[0] + (row < s_cu[0] ? row : s_cu[0] + row - s_cu[a.requests]);
+    }
+  }
+  reinterpret_cast<uint64_t*>(a.order)[turn] = row | (uint64_t)(live ? b : 0xFFFFFFFFu) << 32;
+  a.counters[row] = live && j == 0;
+  if (live) a.path[row] = j ? -1 : 0;
+}
+
+// The wave decides about row `end` of request b, all parts of which are there, and about
+// those after it as far as theirs are.
+template <class L>
+__device__ __forceinline__ void decide(const VerifyArgs& a, uint32_t b, uint32_t first, uint32_t count, uint32_t end, double c64) {
+  const uint32_t lane = threadIdx.x & 63;
+  const float c = heat32(c64);
+  uint32_t length = (uint32_t)(get(&a.states[b].path) >> 32);
+  for (;;) {
+    const uint64_t at = (uint64_t)first + end;
+    // the first 64 candidates for children, and what is asked about them ahead of the sum
+    const uint32_t last = a.parents ? count : min(count, end + 2);  // a chain has one child
+    float l = 0.f, u = 0.f, q = 1.f;
+    uint32_t x = 0xFFFFFFFFu;
+    auto is_child = [&](uint32_t j) { return a.parents ? a.parents[first + j] == (int32_t)end : j == end + 1; };
+    auto candidate = [&](uint32_t j) {
+      const bool child = j < last && is_child(j);
+      x = child ? (uint32_t)a.draft[first + j] : 0xFFFFFFFFu;
+      if (child) u = a.accept[first + j];
+      if (x < a.vocab) {
+        l = L::one(a.logits, at * a.logits_row + x);
+        if (a.probs) q = fmaxf(a.probs[at * a.probs_row + x], 0.f);  // (a NaN counts as 0)
+      }
+      return __ballot(child);
+    };
+    uint64_t todo = candidate(end + 1 + lane);
+    RowSum row = RowSum::none();
+    for (uint32_t s = lane; s < a.segs; s += 64) {
+      const uint64_t* p = a.parts + 2 * (at * a.segs + s);
+      const uint64_t v = get(p), w = get(p + 1);
+      const float top = __uint_as_float((uint32_t)(v >> 32));
+      row.join(__uint_as_float((uint32_t)v), top, (uint32_t)w, top != top, c);
+    }
+    row.across_wave(c);
+    uint32_t go = 0;
+    bool lost = false;  // a child of the end was refused
+    double left = row.sum;  // of the row's sum, without the refused tokens
+    // children in the order of their rows, 64 candidates at a time
+    for (uint32_t j0 = end + 1; j0 < last && !go && row.sound(); j0 += 64) {
+      if (j0 != end + 1) todo = candidate(j0 + lane);
+      const double e = x < a.vocab && l > -INFINITY ? exp2_64(((double)l - (double)row.top) * c64) : 0.0;
+      while (todo) {
+        const int n = __ffsll((unsigned long long)todo) - 1;
+        todo &= todo - 1;
+        const uint32_t token = __shfl(x, n, 64), node = j0 + (uint32_t)n;
+        const double weight = __shfl(e, n, 64), draw = (double)__shfl(u, n, 64) * (double)__shfl(q, n, 64);
+        bool taken = false;
+        if (c > 0.f) {
+          // a token that an earlier sibling had is refused already
+          bool before = false;
+          if (a.parents && lost && token < a.vocab)
+            for (uint32_t i = end + 1 + lane; i < node; i += 64) before |= is_child(i) && (uint32_t)a.draft[first + i] == token;
+          if (token < a.vocab && !__any(before)) {
+            taken = draw * (a.probs ? (double)row.sum : left) < weight;
+            if (!taken) left -= weight;
+          }
+        } else {
+          taken = token == row.at;
+        }
+        if (taken) {
+          go = node;
+          break;
+        }
+        lost = true;
+      }
+    }
+    if (!go) {
+      if (lane == 0) {
+        put(&a.states[b].path, kOver);
+        a.accepted[b] = (int32_t)length;
+        const bool more = row.sound() && c > 0.f;  // the next token is still to be chosen
+        a.ends[b] = End{!more ? kDone : a.probs && lost ? kFromRest : kFromTarget, first + end, 0, 0, row.top, row.at, end, lost};
+        if (!more) a.next[b] = row.sound() ? (int32_t)row.at : -1;
+      }
+      return;
+    }
+    end = go;
+    uint32_t old = 0;
+    if (lane == 0) {
+      a.path[first + length] = (int32_t)end;
+      put(&a.states[b].path, end | (uint64_t)(length + 1) << 32);
+      __builtin_amdgcn_s_waitcnt(0);
+      old = count_in(a.counters + first + end);
+    }
+    ++length;
+    if (__builtin_amdgcn_readfirstlane(old) != a.segs) return;  // parts of it are still to come
+  }
+}
+
+// One segment of one row.
+template <class L>
+__global__ __launch_bounds__(kThreads) void k_verify_rows(VerifyArgs a) {
+  __shared__ RowSum s_part[kThreads / 64];
+  const uint32_t turn = blockIdx.x / a.segs, seg = blockIdx.x - turn * a.segs, t = threadIdx.x;
+  const uint32_t row = a.order[2 * turn], b = a.order[2 * turn + 1];
+  if (b >= a.requests) return;
+  uint32_t first, count;
+  request_rows(a.cu, b, a.tokens, &first, &count);
+  const uint32_t j = row - first;
+  if (j >= count) return;
+  // On the way down from the path's end?  (An end that is not the latest only means that
+  // less is passed by.)
+  const uint32_t end = (uint32_t)get(&a.states[b].path);
+  if (j < end) return;
+  if (end && a.parents) {
+    uint32_t x = j;
+    while (x > end) {
+      const uint32_t up = (uint32_t)a.parents[first + x];
+      if (up >= x) return;
+      x = up;
+    }
+    if (x < end) return;
+  }
+  const double c64 = heat(a, b);
+  const float c = heat32(c64);
+  float x[kEach];
+  load_places<L>(a.logits, row * a.logits_row, seg, a.vocab, a.wide, -INFINITY, place<L>, x);
+  RowSum r = RowSum::none();
+  add_elements(r, x, [&](uint32_t e) { return seg * kSeg + place<L>(e); }, c);
+  r.across_wave(c);
+  if ((t & 63) == 0) s_part[t >> 6] = r;
+  __syncthreads();
+  if (t >= 64) return;
+  uint32_t old = 0;
+  if (t == 0) {
+    for (uint32_t w = 1; w < kThreads / 64; ++w) r.join(s_part[w].sum, s_part[w].top, s_part[w].at, s_part[w].odd, c);
+    uint64_t* p = a.parts + 2 * ((uint64_t)row * a.segs + seg);
+    put(p, __float_as_uint(r.sum) | (uint64_t)__float_as_uint(r.odd ? NAN : r.top) << 32);
+    put(p + 1, r.at);
+    __builtin_amdgcn_s_waitcnt(0);
+    old = count_in(a.counters + row);
+  }
+  if (__builtin_amdgcn_readfirstlane(old) == a.segs) decide<L>(a, b, first, count, j, c64);
 }
 
 // Exclusive running sum over the workgroup's threads in fp64.
@@ -237,7 +401,6 @@ __device__ __forceinline__ double run_before(double v, double* s_sum, double* to
   if (lane == 63) s_sum[wave] = scan;
   __syncthreads();
   double before = scan - v, all = 0.0;
-  // (scan - v is exact enough for choosing a thread, which then adds for itself)
 #pragma unroll
   for (uint32_t w = 0; w < kThreads / 64; ++w) {
     if (w < wave) before += s_sum[w];
@@ -248,46 +411,52 @@ __device__ __forceinline__ double run_before(double v, double* s_sum, double* to
   return before;
 }
 
-// The first place whose running sum passes `border`, where `before` is the sum of all
-// places before the segment; w holds the segment's weights, kSeg of them.  If rounding
+// The first place of a segment whose running sum passes `border`, where `before` is the
+// sum of all places before it; a thread holds the weights of kEach neighbours.  If rounding
 // leaves none, the last place that has a weight; ~0 if no place has one.
-__device__ __forceinline__ uint32_t choose(const double* w, double before, double border, double* s_sum, uint32_t* s_pick) {
+__device__ __forceinline__ uint32_t choose(const double (&w)[kEach], double before, double border, double* s_sum, uint32_t* s_pick) {
   const uint32_t t = threadIdx.x;
   if (t == 0) s_pick[0] = 0xFFFFFFFFu, s_pick[1] = 0;
   double mine = 0.0, all;
   uint32_t last = 0;  // one past the last place with a weight
+#pragma unroll
   for (uint32_t e = 0; e < kEach; ++e) {
-    const double v = w[kEach * t + e];
-    mine += v;
-    if (v > 0.0) last = kEach * t + e + 1;
+    mine += w[e];
+    if (w[e] > 0.0) last = kEach * t + e + 1;
   }
   double run = before + run_before(mine, s_sum, &all);
   if (last) atomicMax(&s_pick[1], last);
-  for (uint32_t e = 0; e < kEach && last; ++e) {
-    const double v = w[kEach * t + e];
-    run += v;
-    if (v > 0.0 && run > border) {
-      atomicMin(&s_pick[0], kEach * t + e);
-      break;
-    }
+  uint32_t pick = 0xFFFFFFFFu;
+#pragma unroll
+  for (uint32_t e = 0; e < kEach; ++e) {
+    run += w[e];
+    if (w[e] > 0.0 && run > border) pick = min(pick, kEach * t + e);
   }
+  if (pick != 0xFFFFFFFFu) atomicMin(&s_pick[0], pick);
   __syncthreads();
-  const uint32_t pick = s_pick[0], end = s_pick[1];
-  __syncthreads();
-  return pick != 0xFFFFFFFFu ? pick : end - 1;
+  return s_pick[0] != 0xFFFFFFFFu ? s_pick[0] : s_pick[1] - 1;
 }
 
-// The first segment in which the running sum passes border, by every wave for itself;
-// sum(s) is its sum.  *before: the sum of those in front.  If rounding leaves none, the
-// last segment that has a sum; ~0 if none has.
-template <class F>
-__device__ __forceinline__ uint32_t choose_segment(uint32_t segs, double border, F sum, double* before) {
+__device__ __forceinline__ double get_sum(const double* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// The sum of all segments; v: the lane's first.
+__device__ __forceinline__ double all_sums(const double* sums, uint32_t segs, double* v) {
   const uint32_t lane = threadIdx.x & 63;
-  double run = 0.0;
+  *v = lane < segs ? get_sum(sums + lane) : 0.0;
+  double total = *v;
+  for (uint32_t s = lane + 64; s < segs; s += 64) total += get_sum(sums + s);
+  return wave_sum(total);
+}
+
+// The first segment in which the running sum passes border, by every wave for itself; v: the
+// lane's first sum.  *before: the sum of those in front.  If rounding leaves none, the last
+// segment that has a sum; ~0 if none has.
+__device__ __forceinline__ uint32_t choose_segment(const double* sums, uint32_t segs, double v, double border, double* before) {
+  const uint32_t lane = threadIdx.x & 63;
+  double run = 0.0, last_before = 0.0;
   uint32_t last = 0xFFFFFFFFu;
-  double last_before = 0.0;
   for (uint32_t s0 = 0; s0 < segs; s0 += 64) {
-    const double v = s0 + lane < segs ? sum(s0 + lane) : 0.0;
+    if (s0) v = s0 + lane < segs ? get_sum(sums + s0 + lane) : 0.0;
     double scan = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -309,230 +478,164 @@ __device__ __forceinline__ uint32_t choose_segment(uint32_t segs, double border,
   return last;
 }
 
-// One workgroup a request: the way down the tree (each wave for itself, all alike: a step
-// is a few loads), and the next token where it comes from p.
-template <class L>
-__global__ __launch_bounds__(kThreads) void k_verify_walk(VerifyArgs a) {
-  extern __shared__ double s_w[];      // [kSeg] weights of a segment, then [segs] sums
-  double* s_seg = s_w + kSeg;
-  __shared__ double s_sum[4];
-  __shared__ uint32_t s_pick[2];
-  const uint32_t b = blockIdx.x, t = threadIdx.x, lane = t & 63;
-  uint32_t first, count;
-  request_rows(a.cu, b, a.tokens, &first, &count);
-  if (a.probs && t == 0) {
-    a.ends[b].row = 0xFFFFFFFFu;
-    a.ends[b].counter = 0;
+// A segment's sum for the request's last workgroup: true, for all threads, in that one.
+__device__ __forceinline__ bool put_sum(double* sums, uint32_t own, uint32_t segs, double v, uint32_t* counter, uint32_t* s_last) {
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(sums + own, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __builtin_amdgcn_s_waitcnt(0);
+    *s_last = count_in(counter) == segs - 1;
   }
-  if (count == 0) {
-    if (t == 0) {
-      a.accepted[b] = 0;
-      a.next[b] = -1;
-    }
-    return;
-  }
-  const double c = heat(a, b);
-  uint32_t end = 0, length = 1;
-  int32_t next = -1;
-  bool lost = false;  // a child of the end was refused
-  RowSum row;
-  if (t == 0) a.path[first] = 0;
-  for (;;) {
-    const uint64_t at = (uint64_t)first + end;
-    row = join_row(a.parts + at * a.segs, a.segs, c);
-    lost = false;
-    if (!row.sound) break;
-    auto logit = [&](uint32_t v) { return L::one(a.logits, at * a.logits_row + v); };
-    uint32_t go = 0;
-    double left = row.sum;  // of the row's sum, without the refused tokens
-    // children in the order of their rows, 64 candidates at a time
-    for (uint32_t j0 = end + 1; j0 < count && !go; j0 += 64) {
-      const uint32_t j = j0 + lane;
-      bool child = j < count && (a.parents ? a.parents[first + j] == (int32_t)end : j == end + 1);
-      uint64_t todo = __ballot(child);
-      if (!a.parents) j0 = count;  // a chain has one
-      if (!todo) continue;
-      // each lane prepares its own candidate
-      uint32_t x = 0xFFFFFFFFu;
-      double e = 0.0, u = 0.0;
-      if (child) {
-        x = (uint32_t)a.draft[first + j];
-        u = a.accept[first + j];
-        if (x < a.vocab) {
-          if (c > 0.0) e = exp2_64(((double)logit(x) - (double)row.top) * c);
-          if (a.probs) u *= fmax(a.probs[at * a.probs_row + x], 0.f);  // (a NaN counts as 0)
-        }
-      }
-      while (todo) {
-        const int n = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        const uint32_t token = __shfl(x, n, 64), node = (uint32_t)__shfl((int)j, n, 64);
-        const double weight = __shfl(e, n, 64), draw = __shfl(u, n, 64);
-        bool taken;
-        if (c > 0.0) {
-          // a token that an earlier sibling had is refused already
-          bool before = false;
-          if (a.parents && token < a.vocab)
-            for (uint32_t i = end + 1 + lane; i < node; i += 64)
-              before |= a.parents[first + i] == (int32_t)end && (uint32_t)a.draft[first + i] == token;
-          const bool again = __any(before);
-          taken = token < a.vocab && !again && draw * (a.probs ? row.sum : left) < weight;
-          if (!taken && token < a.vocab && !again) left -= weight;
-        } else {
-          taken = token == row.at;
-        }
-        if (taken) {
-          go = node;
-          break;
-        }
-        lost = true;
-      }
-    }
-    if (!go) break;
-    end = go;
-    if (t == 0) a.path[first + length] = (int32_t)end;
-    ++length;
-  }
-  for (uint32_t i = length + t; i < count; i += kThreads) a.path[first + i] = -1;
+  __syncthreads();
+  return *s_last != 0;
+}
 
-  const uint64_t at = (uint64_t)first + end;
-  if (row.sound && c == 0.0) {
-    next = (int32_t)row.at;
-  } else if (row.sound && a.probs && lost) {
-    if (t == 0) {
-      a.ends[b].sum = row.sum;
-      a.ends[b].top = row.top;
-      a.ends[b].row = (uint32_t)at;
-    }
-  } else if (row.sound) {
-    // p without the refused tokens: their segments are added up again without them
-    const Part* parts = a.parts + at * a.segs;
-    for (uint32_t s = t; s < a.segs; s += kThreads)
-      s_seg[s] = parts[s].sum > 0.0 ? parts[s].sum * exp2_64(((double)parts[s].top - (double)row.top) * c) : 0.0;
-    __syncthreads();
-    auto weights = [&](uint32_t seg) {  // of a segment, into s_w; returns this thread's sum
-      float x[kEach];
-      load_segment<L>(a.logits, at * a.logits_row, seg, a.vocab, a.wide, x);
-      for (uint32_t e = 0; e < kEach; ++e)
-        s_w[place<L>(e)] = x[e] > -INFINITY ? exp2_64(((double)x[e] - (double)row.top) * c) : 0.0;
-      __syncthreads();
-      if (lost)
-        for (uint32_t j = end + 1 + t; j < count; j += kThreads)
-          if (a.parents ? a.parents[first + j] == (int32_t)end : j == end + 1) {
-            const uint32_t x = (uint32_t)a.draft[first + j];
-            if (x < a.vocab && x / kSeg == seg) s_w[x % kSeg] = 0.0;
-          }
-      __syncthreads();
-    };
-    if (lost) {
-      for (uint32_t j = end + 1; j < count; ++j) {
-        if (a.parents ? a.parents[first + j] != (int32_t)end : j != end + 1) continue;
-        const uint32_t x = (uint32_t)a.draft[first + j];
-        if (x >= a.vocab) continue;
-        weights(x / kSeg);
-        double mine = 0.0, all;
-        for (uint32_t e = 0; e < kEach; ++e) mine += s_w[t + e * kThreads];
-        run_before(mine, s_sum, &all);
-        if (t == 0) s_seg[x / kSeg] = all;
-        __syncthreads();
-      }
-    }
-    double total = 0.0, before;
-    for (uint32_t s = lane; s < a.segs; s += 64) total += s_seg[s];
-    total = wave_sum(total);
-    const double border = (double)a.sample[b] * total;
-    const uint32_t seg = choose_segment(a.segs, border, [&](uint32_t s) { return s_seg[s]; }, &before);
-    next = (int32_t)row.at;  // where nothing is left
-    if (seg != 0xFFFFFFFFu) {
-      weights(seg);
-      const uint32_t pick = choose(s_w, before, border, s_sum, s_pick);
-      if (pick != 0xFFFFFFFFu) next = (int32_t)(seg * kSeg + pick);
-    }
+// The next token by the segments' sums and the weights of one of them.  Where rounding has
+// left nothing, the target's most likely token.
+template <class F>
+__device__ __forceinline__ void choose_next(const VerifyArgs& a, uint32_t b, const End& end, const double* sums, F weights,
+                                            double* s_sum, uint32_t* s_pick) {
+  double first, before;
+  const double border = all_sums(sums, a.segs, &first) * (double)a.sample[b];
+  const uint32_t seg = choose_segment(sums, a.segs, first, border, &before);
+  uint32_t next = end.at;
+  if (seg != 0xFFFFFFFFu) {
+    double w[kEach];
+    weights(seg, [](uint32_t e) { return kEach * threadIdx.x + e; }, w);
+    const uint32_t pick = choose(w, before, border, s_sum, s_pick);
+    if (pick != 0xFFFFFFFFu) next = seg * kSeg + pick;
   }
-  if (t == 0) {
-    a.accepted[b] = (int32_t)length;
-    a.next[b] = next;
+  if (threadIdx.x == 0) a.next[b] = (int32_t)next;
+}
+
+// exp((l - top) / T) at the thread's places of a segment of a path's last row.
+template <class L, class F>
+__device__ __forceinline__ void exponentials(const VerifyArgs& a, const End& end, double c, uint32_t seg, F at, double (&w)[kEach]) {
+  float x[kEach];
+  load_places<L>(a.logits, end.row * a.logits_row, seg, a.vocab, a.wide, -INFINITY, at, x);
+#pragma unroll
+  for (uint32_t e = 0; e < kEach; e += 8) {
+    double z[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) z[i] = ((double)x[e + i] - (double)end.top) * c;
+    exp2_64<8>(z);
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) w[e + i] = x[e + i] > -INFINITY ? z[i] : 0.0;
   }
 }
 
-// Where a chain was refused: sums of max(p - q, 0) by segment, and the last segment's
-// workgroup of a request chooses.
+__device__ __forceinline__ double sum_of(const double (&w)[kEach], double* s_sum) {  // to all threads
+  double mine = 0.0, all;
+#pragma unroll
+  for (uint32_t e = 0; e < kEach; ++e) mine += w[e];
+  run_before(mine, s_sum, &all);
+  return all;
+}
+
+// max(p - q, 0): a workgroup a segment, and the last chooses.  inv: 1 / the row's sum.
+template <class L>
+__device__ __forceinline__ void choose_rest(const VerifyArgs& a, uint32_t b, uint32_t own, const End& end, double c, double inv,
+                                            double* s_sum, uint32_t* s_pick, uint32_t* s_last) {
+  auto weights = [&](uint32_t seg, auto at, double (&w)[kEach]) {
+    float q[kEach];
+    exponentials<L>(a, end, c, seg, at, w);
+    load_places<Logit<F32>>(a.probs, end.row * a.probs_row, seg, a.vocab, a.probs_wide, 0.f, at, q);
+#pragma unroll
+    for (uint32_t e = 0; e < kEach; ++e) w[e] = fmax(w[e] * inv - (double)fmaxf(q[e], 0.f), 0.0);
+  };
+  double w[kEach];
+  weights(own, place<L>, w);
+  double* rest = a.rest + (uint64_t)b * a.segs;
+  if (put_sum(rest, own, a.segs, sum_of(w, s_sum), &a.ends[b].rest_counter, s_last))
+    choose_next(a, b, end, rest, weights, s_sum, s_pick);
+}
+
+// Up to this many segments every workgroup adds up a whole row itself sooner than a launch
+// more would give its sum.
+constexpr uint32_t kFew = 8;
+
+// Weights of a path's last row, a workgroup a segment; where they are p without the refused
+// tokens, the last workgroup chooses.
+template <class L>
+__global__ __launch_bounds__(kThreads) void k_verify_next(VerifyArgs a) {
+  __shared__ double s_sum[kThreads / 64];
+  __shared__ uint32_t s_gone[kSeg / 32];  // a bit for each refused token of a segment
+  __shared__ uint32_t s_pick[2], s_last;
+  const uint32_t b = blockIdx.x / a.segs, own = blockIdx.x - b * a.segs, t = threadIdx.x;
+  const End end = a.ends[b];
+  if (end.mode == kDone) return;
+  const double c = heat(a, b);
+  double w[kEach];
+  if (end.mode == kFromRest && a.segs <= kFew) {
+    double mine = 0.0, all;
+#pragma unroll 2
+    for (uint32_t seg = 0; seg < a.segs; ++seg) {
+      exponentials<L>(a, end, c, seg, place<L>, w);
+#pragma unroll
+      for (uint32_t e = 0; e < kEach; ++e) mine += w[e];
+    }
+    run_before(mine, s_sum, &all);
+    choose_rest<L>(a, b, own, end, c, 1.0 / all, s_sum, s_pick, &s_last);
+    return;
+  }
+  const bool fewer = end.mode == kFromTarget && end.lost;
+  auto weights = [&](uint32_t seg, auto at, double (&w)[kEach]) {
+    exponentials<L>(a, end, c, seg, at, w);
+    if (!fewer) return;
+    uint32_t first, count;
+    request_rows(a.cu, b, a.tokens, &first, &count);
+    __syncthreads();
+    for (uint32_t i = t; i < kSeg / 32; i += kThreads) s_gone[i] = 0;
+    __syncthreads();
+    for (uint32_t j = end.end + 1 + t; j < count; j += kThreads)
+      if (a.parents ? a.parents[first + j] == (int32_t)end.end : j == end.end + 1) {
+        const uint32_t token = (uint32_t)a.draft[first + j];
+        if (token < a.vocab && token / kSeg == seg) atomicOr(&s_gone[token % kSeg / 32], 1u << token % 32);
+      }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t e = 0; e < kEach; ++e)
+      if (s_gone[at(e) / 32] >> at(e) % 32 & 1) w[e] = 0.0;
+  };
+  weights(own, place<L>, w);
+  double* sums = a.sums + (uint64_t)b * a.segs;
+  if (put_sum(sums, own, a.segs, sum_of(w, s_sum), &a.ends[b].counter, &s_last) && end.mode == kFromTarget)
+    choose_next(a, b, end, sums, weights, s_sum, s_pick);
+}
+
 template <class L>
 __global__ __launch_bounds__(kThreads) void k_verify_rest(VerifyArgs a) {
-  __shared__ double s_w[kSeg];
-  __shared__ double s_sum[4];
+  __shared__ double s_sum[kThreads / 64];
   __shared__ uint32_t s_pick[2], s_last;
-  const uint32_t b = blockIdx.x / a.segs, own = blockIdx.x - b * a.segs, t = threadIdx.x, lane = t & 63;
+  const uint32_t b = blockIdx.x / a.segs, own = blockIdx.x - b * a.segs;
   const End end = a.ends[b];
-  if (end.row == 0xFFFFFFFFu) return;
-  const double c = heat(a, b), inv = 1.0 / end.sum;
-  auto weights = [&](uint32_t seg) {
-    float x[kEach], q[kEach];
-    load_segment<L>(a.logits, end.row * a.logits_row, seg, a.vocab, a.wide, x);
-    // (places differ with the size of the logits, so the draft's are met in the logits' order)
-    const float* p = a.probs + end.row * a.probs_row + (uint64_t)seg * kSeg;
-    const uint32_t left = a.vocab - seg * kSeg;
-    if (a.probs_wide && left >= kSeg) {
-#pragma unroll
-      for (uint32_t e = 0; e < kEach; e += 4) {
-        const floatx4 v = *reinterpret_cast<const floatx4*>(p + place<L>(e));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[e + j] = v[j];
-      }
-    } else {
-#pragma unroll
-      for (uint32_t e = 0; e < kEach; ++e) q[e] = place<L>(e) < left ? p[place<L>(e)] : 0.f;
-    }
-    double mine = 0.0;
-#pragma unroll
-    for (uint32_t e = 0; e < kEach; ++e) {
-      const double w = fmax((x[e] > -INFINITY ? exp2_64(((double)x[e] - (double)end.top) * c) * inv : 0.0) - (double)fmaxf(q[e], 0.f), 0.0);
-      s_w[place<L>(e)] = w;
-      mine += w;
-    }
-    return mine;
-  };
-  double all;
-  run_before(weights(own), s_sum, &all);
-  // Sums pass between workgroups that may sit on different dies: agent-scope accesses, and a
-  // wait for the store before the count.
-  double* rest = a.rest + (uint64_t)b * a.segs;
-  if (t == 0) {
-    __hip_atomic_store(rest + own, all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __builtin_amdgcn_s_waitcnt(0);
-    s_last = __hip_atomic_fetch_add(&a.ends[b].counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.segs - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  auto sum = [&](uint32_t s) { return __hip_atomic_load(rest + s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  double total = 0.0, before;
-  for (uint32_t s = lane; s < a.segs; s += 64) total += sum(s);
-  total = wave_sum(total);
-  const double border = (double)a.sample[b] * total;
-  const uint32_t seg = choose_segment(a.segs, border, sum, &before);
-  int32_t next;
-  if (seg == 0xFFFFFFFFu) {  // rounding has left nothing: the target's most likely token
-    next = (int32_t)join_row(a.parts + (uint64_t)end.row * a.segs, a.segs, c).at;
-  } else {
-    __syncthreads();
-    weights(seg);
-    __syncthreads();
-    next = (int32_t)(seg * kSeg + choose(s_w, before, border, s_sum, s_pick));
-  }
-  if (t == 0) a.next[b] = next;
+  if (end.mode != kFromRest) return;
+  double first;
+  const double all = all_sums(a.sums + (uint64_t)b * a.segs, a.segs, &first);
+  choose_rest<L>(a, b, own, end, heat(a, b), 1.0 / all, s_sum, s_pick, &s_last);
 }
 
 struct VerifyPlan {
   uint32_t segs;
-  size_t rest_off, ends_off, bytes;
+  size_t order_off, counters_off, states_off, sums_off, rest_off, ends_off, bytes;
 };
 
 VerifyPlan plan_verify(uint32_t tokens, uint32_t vocab, uint32_t requests) {
   VerifyPlan p;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
   p.segs = (vocab + kSeg - 1) / kSeg;
-  p.rest_off = (size_t)tokens * p.segs * sizeof(Part);
-  p.ends_off = p.rest_off + (size_t)requests * p.segs * sizeof(double);
-  p.bytes = p.ends_off + (size_t)requests * sizeof(End) + 256;
+  take((size_t)tokens * p.segs * 16);  // parts
+  p.order_off = take((size_t)tokens * 8);
+  p.counters_off = take((size_t)tokens * 4);
+  p.states_off = take((size_t)requests * sizeof(State));
+  p.sums_off = take((size_t)requests * p.segs * 8);
+  p.rest_off = take((size_t)requests * p.segs * 8);
+  p.ends_off = take((size_t)requests * sizeof(End));
+  p.bytes = std::max<size_t>(at, 256);
   return p;
 }
 
@@ -544,14 +647,15 @@ bool verify_shape_ok(uint32_t tokens, uint32_t vocab, uint32_t requests) {
 
 template <class L>
 int launch_verify(const VerifyArgs& a, hipStream_t st) {
-  const uint32_t lds = (kSeg + a.segs) * 8;  // 40 KB at most
-  if (a.tokens) {
-    hipLaunchKernelGGL(k_verify_parts<L>, dim3(a.tokens * a.segs), dim3(kThreads), 0, st, a);
-    if (int rc = launched()) return rc;
-  }
-  hipLaunchKernelGGL(k_verify_walk<L>, dim3(a.requests), dim3(kThreads), lds, st, a);
+  const uint32_t lds = (a.requests + 1) * 4;  // 32 KB at most
+  hipLaunchKernelGGL(k_verify_begin, dim3((std::max(a.tokens, a.requests) + kThreads - 1) / kThreads), dim3(kThreads), lds, st, a);
   if (int rc = launched()) return rc;
-  if (!a.probs || a.tokens == 0) return DGT_OK;
+  if (a.tokens == 0) return DGT_OK;
+  hipLaunchKernelGGL(k_verify_rows<L>, dim3(a.tokens * a.segs), dim3(kThreads), 0, st, a);
+  if (int rc = launched()) return rc;
+  hipLaunchKernelGGL(k_verify_next<L>, dim3(a.requests * a.segs), dim3(kThreads), 0, st, a);
+  if (int rc = launched()) return rc;
+  if (!a.probs || a.segs <= kFew) return DGT_OK;
   hipLaunchKernelGGL(k_verify_rest<L>, dim3(a.requests * a.segs), dim3(kThreads), 0, st, a);
   return launched();
 }
@@ -597,7 +701,11 @@ int dgt_verify(uint32_t type, const void* d_logits, uint64_t logits_row, const i
   a.path = d_path;
   a.accepted = d_accepted;
   a.next = d_next;
-  a.parts = reinterpret_cast<Part*>(ws);
+  a.parts = reinterpret_cast<uint64_t*>(ws);
+  a.order = reinterpret_cast<uint32_t*>(ws + p.order_off);
+  a.counters = reinterpret_cast<uint32_t*>(ws + p.counters_off);
+  a.states = reinterpret_cast<State*>(ws + p.states_off);
+  a.sums = reinterpret_cast<double*>(ws + p.sums_off);
   a.rest = reinterpret_cast<double*>(ws + p.rest_off);
   a.ends = reinterpret_cast<End*>(ws + p.ends_off);
   a.logits_row = logits_row;
