@@ -42,19 +42,26 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* s_sum, uint
 }
 
 // ----------------------------------------------------------------------- keep
+// One launch: a workgroup for lengths and pages, the others move rows.  A chain of
+// latencies (offsets, path, slots, rows) bounds it; a workgroup goes through it once for
+// several layers and heads, so that all of them are on the card at a time.
 struct KeepArgs {
   const int32_t *path, *kept, *ctx, *cu, *slots, *free_head;
   int32_t *free_list, *table, *lens, *counts;
-  uint32_t requests, tokens, free_len, width, units;
+  uint32_t requests, tokens, free_len, width;
+  uint32_t parts, each;  // workgroups a request, and the layers' heads that one takes
   Pool pool;
 };
 
-constexpr uint32_t kKeepRows = 16;    // tokens that a workgroup moves at a time
+constexpr uint32_t kKeepRows = 16;  // tokens that a workgroup moves at a time
 
-// The first new token of a request that the plan refused has no slot.
-__device__ __forceinline__ uint32_t kept_of(const KeepArgs& a, uint32_t b, uint32_t first, uint32_t count) {
-  if (count == 0 || !a.pool.holds((uint32_t)a.slots[first])) return 0;
-  return min((uint32_t)max(a.kept[b], 0), count);
+// How many rows a request keeps; the first new token of one that the plan refused has no
+// slot.  (The loads do not wait for each other.)
+__device__ __forceinline__ uint32_t kept_of(const KeepArgs& a, uint32_t b, uint32_t first, uint32_t count, bool* held) {
+  const int32_t kept = a.kept[b];
+  const uint32_t slot = count ? (uint32_t)a.slots[first] : ~0u;
+  *held = a.pool.holds(slot);
+  return *held ? min((uint32_t)max(kept, 0), count) : 0u;
 }
 
 // Lengths, and the pages past them, by one workgroup: the list's order is the requests'.
@@ -64,8 +71,8 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
   const uint32_t log = a.pool.log_block, round = a.pool.block() - 1;
   const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
   uint32_t total = 0;
-  // twice over the requests: how many pages, then which
-  for (int pass = 0; pass < 2; ++pass) {
+  // where 256 threads do not hold all requests, twice over them: how many pages, then which
+  for (int pass = a.requests <= 256; pass < 2; ++pass) {
     uint32_t done = 0;
     for (uint32_t b0 = 0; b0 < a.requests; b0 += 256) {
       const uint32_t b = b0 + threadIdx.x;
@@ -73,8 +80,8 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
       if (b < a.requests) {
         request_rows(a.cu, b, a.tokens, &first, &count);
         ctx = (uint32_t)max(a.ctx[b], 0);
-        const bool held = count && a.pool.holds((uint32_t)a.slots[first]);
-        const uint32_t kept = kept_of(a, b, first, count);
+        bool held;
+        const uint32_t kept = kept_of(a, b, first, count, &held);
         now = (uint32_t)min((uint64_t)ctx + kept, (uint64_t)0x7FFFFFFF);
         from = min((uint32_t)(((uint64_t)now + round) >> log), a.width);
         to = held ? min((uint32_t)(((uint64_t)ctx + count + round) >> log), a.width) : from;
@@ -90,6 +97,7 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
       uint32_t at = done + sum_before<256>(mine, s_sum, &all);
       done += all;
       if (pass == 0) continue;
+      if (a.requests <= 256) total = all;
       for (uint32_t c = from; c < to; ++c) {
         const uint32_t id = page(c);
         if (id == ~0u) continue;
@@ -108,22 +116,24 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
   }
 }
 
-// A workgroup moves the kept rows of one request, layer and head, 16 at a time: all of
-// them are read before any is written.  Index i_j >= j rises with j, so a row that a
-// later step reads lies behind every place that this one writes.  Slots are looked up
-// in the plan's list and not in the table, whose columns change at the same time.
+// A workgroup moves the kept rows of one request in some heads of the layers, 16 at a
+// time: all of them are read before any is written.  Index i_j >= j rises with j, so a
+// row that a later step reads lies behind every place that this one writes.  Slots are
+// looked up in the plan's list and not in the table, whose columns change at the same time.
 __device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint32_t* s_src, uint32_t* s_dst) {
   const uint32_t t = threadIdx.x, dim = a.pool.dim, log = a.pool.log_block, in_page = a.pool.block() - 1;
-  const uint32_t per = a.pool.layers * a.pool.heads, b = unit / per, layer = unit % per / a.pool.heads;
-  const uint32_t head = unit % a.pool.heads;
+  const uint32_t b = unit / a.parts, part = unit - b * a.parts;
+  const uint32_t lh0 = part * a.each, lh1 = min(lh0 + a.each, a.pool.layers * a.pool.heads);
   uint32_t first, count;
   request_rows(a.cu, b, a.tokens, &first, &count);
-  const uint32_t kept = kept_of(a, b, first, count);
+  int32_t ahead = t < min(count, kKeepRows) ? a.path[first + t] : 0;
+  bool held;
+  const uint32_t kept = kept_of(a, b, first, count, &held);
   for (uint32_t j0 = 0; j0 < kept; j0 += kKeepRows) {
     const uint32_t rows = min(kept - j0, kKeepRows);
     bool moves = false;
     if (t < rows) {
-      const uint32_t j = j0 + t, i = (uint32_t)a.path[first + j];
+      const uint32_t j = j0 + t, i = (uint32_t)(j0 ? a.path[first + j] : ahead);
       uint32_t src = ~0u, dst = ~0u;
       if (i > j && i < count) {
         src = (uint32_t)a.slots[first + i];
@@ -134,40 +144,34 @@ __device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint
       s_dst[t] = dst;
     }
     if (!__syncthreads_or(moves)) continue;
-    // 16-byte pieces of key rows, a row's side by side; value elements, a value row's side by side
-    const uint32_t pieces = dim / 8;
-    u32x4 k[8];
+    const uint32_t vr = t % kKeepRows, v_src = vr < rows ? s_src[vr] : ~0u, v_dst = v_src != ~0u ? s_dst[vr] : 0;
+    for (uint32_t lh = lh0; lh < lh1; ++lh) {
+      const uint32_t layer = lh / a.pool.heads, head = lh - layer * a.pool.heads;
+      // value elements, a value row's side by side; 16-byte pieces of key rows, a row's side by side
+      const uint16_t* vs = a.pool.vc + a.pool.page(layer, v_src != ~0u ? v_src >> log : 0, head) + (v_src & in_page);
+      uint16_t* vd = a.pool.vc + a.pool.page(layer, v_dst >> log, head) + (v_dst & in_page);
+      for (uint32_t d0 = 0; d0 < dim; d0 += 128) {
+        const uint32_t dims = min(dim - d0, 128u);
+        u32x4 k;
+        uint16_t v[8];
+        const uint32_t r = t / (dims / 8), d = d0 + 8 * (t % (dims / 8));
+        const bool k_on = r < rows && s_src[r] != ~0u;
+        if (k_on)
+          k = *reinterpret_cast<const u32x4*>(a.pool.kc + a.pool.page(layer, s_src[r] >> log, head) + (s_src[r] & in_page) * dim + d);
 #pragma unroll
-    for (uint32_t n = 0; n < 8; ++n) {  // kKeepRows * 1024 / 8 / 256
-      const uint32_t x = t + 256 * n, r = x / pieces;
-      if (r < rows && s_src[r] != ~0u)
-        k[n] = *reinterpret_cast<const u32x4*>(a.pool.kc + a.pool.page(layer, s_src[r] >> log, head) +
-                                               (s_src[r] & in_page) * dim + 8 * (x % pieces));
-    }
-    for (uint32_t d0 = 0; d0 < dim; d0 += 128) {
-      const uint32_t r = t % kKeepRows;
-      const bool on = r < rows && s_src[r] != ~0u;
-      const uint16_t* vs = a.pool.vc + a.pool.page(layer, on ? s_src[r] >> log : 0, head) + (on ? s_src[r] & in_page : 0);
-      uint16_t* vd = a.pool.vc + a.pool.page(layer, on ? s_dst[r] >> log : 0, head) + (on ? s_dst[r] & in_page : 0);
-      uint16_t v[8];
+        for (uint32_t n = 0; n < 8; ++n) {
+          const uint32_t e = d0 + t / kKeepRows + 16 * n;
+          if (v_src != ~0u && e < d0 + dims) v[n] = vs[(uint64_t)e << log];
+        }
+        __syncthreads();
+        if (k_on)
+          *reinterpret_cast<u32x4*>(a.pool.kc + a.pool.page(layer, s_dst[r] >> log, head) + (s_dst[r] & in_page) * dim + d) = k;
 #pragma unroll
-      for (uint32_t n = 0; n < 8; ++n) {
-        const uint32_t d = d0 + t / kKeepRows + 16 * n;
-        if (on && d < dim) v[n] = vs[(uint64_t)d << log];
+        for (uint32_t n = 0; n < 8; ++n) {
+          const uint32_t e = d0 + t / kKeepRows + 16 * n;
+          if (v_src != ~0u && e < d0 + dims) vd[(uint64_t)e << log] = v[n];
+        }
       }
-      __syncthreads();
-#pragma unroll
-      for (uint32_t n = 0; n < 8; ++n) {
-        const uint32_t d = d0 + t / kKeepRows + 16 * n;
-        if (on && d < dim) vd[(uint64_t)d << log] = v[n];
-      }
-    }
-#pragma unroll
-    for (uint32_t n = 0; n < 8; ++n) {
-      const uint32_t x = t + 256 * n, r = x / pieces;
-      if (r < rows && s_src[r] != ~0u)
-        *reinterpret_cast<u32x4*>(a.pool.kc + a.pool.page(layer, s_dst[r] >> log, head) + (s_dst[r] & in_page) * dim +
-                                  8 * (x % pieces)) = k[n];
     }
     __syncthreads();  // what was written is behind what the next step reads; s_src is reused
   }
@@ -175,11 +179,8 @@ __device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint
 
 __global__ __launch_bounds__(256) void k_page_keep(KeepArgs a) {
   __shared__ uint32_t s_sum[4], s_src[kKeepRows], s_dst[kKeepRows];
-  if (blockIdx.x == 0) {
-    keep_pages(a, s_sum);
-    return;
-  }
-  for (uint32_t unit = blockIdx.x - 1; unit < a.units; unit += gridDim.x - 1) keep_rows(a, unit, s_src, s_dst);
+  if (blockIdx.x == 0) keep_pages(a, s_sum);
+  else keep_rows(a, blockIdx.x - 1, s_src, s_dst);
 }
 
 // ----------------------------------------------------------------------- fork
@@ -253,38 +254,45 @@ __global__ __launch_bounds__(256) void k_page_fork(ForkArgs a) {
     if (!rest) continue;
     const uint32_t old = (uint32_t)from[full];
     if (old >= a.pool.blocks || fresh >= a.pool.blocks || old == fresh) continue;
-    const uint32_t k_pieces = rest * dim / 8, v_row = (rest + 7) / 8, v_pieces = v_row * dim;
-    const uint32_t in_row = a.pool.block() / 8, each = k_pieces + v_pieces;
-    const uint32_t heads = a.pool.layers * a.pool.heads;
+    const uint32_t k_pieces = rest * dim / 8, v_row = (rest + 7) / 8, each = k_pieces + v_row * dim;
+    const uint32_t in_row = a.pool.block() / 8, heads = a.pool.layers * a.pool.heads;
+    const float inv_row = 1.f / (float)v_row;
     for (uint32_t lh = part; lh < heads; lh += a.parts) {
       const uint64_t x = a.pool.page(lh / a.pool.heads, old, lh % a.pool.heads);
       const uint64_t y = a.pool.page(lh / a.pool.heads, fresh, lh % a.pool.heads);
       const u32x4 *kx = reinterpret_cast<const u32x4*>(a.pool.kc + x), *vx = reinterpret_cast<const u32x4*>(a.pool.vc + x);
       u32x4 *ky = reinterpret_cast<u32x4*>(a.pool.kc + y), *vy = reinterpret_cast<u32x4*>(a.pool.vc + y);
-      auto value_at = [&](uint32_t p) { return p / v_row * in_row + p % v_row; };
       for (uint32_t p0 = t; p0 < each; p0 += 256 * 4) {
-        u32x4 v[4];
+        u32x4 v[4], was[4];
+        uint32_t at[4], tokens[4];
 #pragma unroll
         for (uint32_t n = 0; n < 4; ++n) {
           const uint32_t p = p0 + 256 * n;
-          if (p < each) v[n] = p < k_pieces ? kx[p] : vx[value_at(p - k_pieces)];
+          at[n] = p;
+          tokens[n] = 8;
+          if (p < k_pieces) {
+            v[n] = kx[p];
+          } else if (p < each) {
+            // (exact: the quotients are below 2^17, a half off every border)
+            const uint32_t row = (uint32_t)(((float)(p - k_pieces) + 0.5f) * inv_row), in = p - k_pieces - row * v_row;
+            at[n] = row * in_row + in;
+            tokens[n] = rest - 8 * in;
+            v[n] = vx[at[n]];
+            if (tokens[n] < 8) was[n] = vy[at[n]];
+          }
         }
 #pragma unroll
         for (uint32_t n = 0; n < 4; ++n) {
           const uint32_t p = p0 + 256 * n;
-          if (p >= each) continue;
           if (p < k_pieces) {
             ky[p] = v[n];
-            continue;
-          }
-          const uint32_t at = value_at(p - k_pieces), tokens = rest - 8 * ((p - k_pieces) % v_row);
-          if (tokens >= 8) {
-            vy[at] = v[n];
-          } else {  // cells past the length stay as they are
-            uint16_t* one = reinterpret_cast<uint16_t*>(vy + at);
+          } else if (p < each) {
+            // cells past the length stay as they are
 #pragma unroll
-            for (uint32_t e = 0; e < 7; ++e)
-              if (e < tokens) one[e] = (uint16_t)(v[n][e / 2] >> 16 * (e & 1));
+            for (uint32_t w = 0; w < 4; ++w)
+              if (tokens[n] <= 2 * w) v[n][w] = was[n][w];
+              else if (tokens[n] == 2 * w + 1) v[n][w] = (v[n][w] & 0xFFFFu) | (was[n][w] & 0xFFFF0000u);
+            vy[at[n]] = v[n];
           }
         }
       }
@@ -425,12 +433,12 @@ int dgt_page_keep(const int32_t* d_path, const int32_t* d_kept, const int32_t* d
   a.free_len = free_len;
   a.width = width;
   a.pool = make_pool(d_k_cache, d_v_cache, layers, heads, dim, blocks, block);
-  // a unit is the rows of one request, layer and head
-  const uint64_t units = d_path && tokens && blocks ? (uint64_t)requests * layers * heads : 0;
-  if (units > 0xFFFFFFFFull - 64 * kCUs) return DGT_E_SHAPE;
-  a.units = (uint32_t)units;
-  hipLaunchKernelGGL(k_page_keep, dim3(1 + (uint32_t)std::min<uint64_t>(units, 16 * kCUs)), dim3(256), 0,
-                     static_cast<hipStream_t>(stream), a);
+  // as many workgroups a request as the card holds at a time, if it is not one each anyway
+  const uint32_t all = layers * heads;
+  a.parts = d_path && tokens && blocks && requests ? std::min(all, std::max(8 * kCUs / requests, 1u)) : 0;
+  a.each = a.parts ? (all + a.parts - 1) / a.parts : 0;
+  a.parts = a.parts ? (all + a.each - 1) / a.each : 0;
+  hipLaunchKernelGGL(k_page_keep, dim3(1 + requests * a.parts), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return launched();
 }
 
@@ -461,7 +469,8 @@ int dgt_page_fork(const int32_t* d_src, const int32_t* d_dst, uint32_t forks, in
   a.free_len = free_len;
   a.pool = make_pool(d_k_cache, d_v_cache, layers, heads, dim, blocks, block);
   // parts of a fork, so that a few forks fill the card; a part is at least a head of a layer
-  a.parts = std::min(layers * heads, std::max(4 * kCUs / std::max(forks, 1u), 1u));
+  // (twice what is on the card at a time: 67-70 us, once: 70-75, for 64 forks of 2.1 MB a page)
+  a.parts = std::min(layers * heads, std::max(16 * kCUs / std::max(forks, 1u), 1u));
   const uint32_t lds = 4 * (requests + forks);
   if (lds > 63 * 1024 &&  // with what the kernels have besides, more than the 64 KB of a plain launch
       (hipFuncSetAttribute(reinterpret_cast<const void*>(k_page_fork), hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -471,7 +480,7 @@ int dgt_page_fork(const int32_t* d_src, const int32_t* d_dst, uint32_t forks, in
     return DGT_E_HIP;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (forks) {
-    hipLaunchKernelGGL(k_page_fork, dim3(std::min(forks * a.parts, 8 * kCUs)), dim3(256), lds, st, a);
+    hipLaunchKernelGGL(k_page_fork, dim3(std::min(forks * a.parts, 16 * kCUs)), dim3(256), lds, st, a);
     if (int rc = launched()) return rc;
   }
   hipLaunchKernelGGL(k_fork_counts, dim3(1), dim3(256), lds, st, a);
