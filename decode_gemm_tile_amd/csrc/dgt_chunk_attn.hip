@@ -13,10 +13,10 @@ namespace {
 //
 // Rows of a request and key head are (token, query head of the group); a tile is as many
 // whole tokens as fit kRows of them.  A workgroup runs over the keys of a tile, up to the
-// last one that its last token sees, 64 at a time: tiles of keys and values are shared in
-// LDS by four waves of 32 RT rows each.  S^T = K Q^T puts keys down and rows across the lanes;
-// keys are dealt to the first operand so that a lane's scores are 8 consecutive keys of
-// one row, the second operand of O^T = V^T P^T as it stands.
+// last one that its last token sees, 64 at a time (32 where heads are longer than 128): tiles of
+// keys and values are shared in LDS by eight waves (four) of 32 rows each.  S^T = K Q^T puts
+// keys down and rows across the lanes; keys are dealt to the first operand so that a lane's
+// scores are 8 consecutive keys of one row, the second operand of O^T = V^T P^T as it stands.
 //
 // Work is dealt in items: a piece of a tile's keys.  Whole tiles where there are enough of
 // them; long tiles are cut where the card would be partly idle (k_chunk_plan weighs it),
@@ -31,12 +31,12 @@ struct ChunkArgs {
   float* parts;
   uint64_t q_row, q_head, out_row, out_head;  // element strides
   uint32_t requests, tokens, heads, group, dim, log_block, width, blocks;
-  uint32_t tile_tokens, splits;  // tokens of a tile; tiles a token's heads take (one of the two is 1)
+  uint32_t rows, tile_tokens, splits;  // rows and tokens of a tile; tiles a token's heads take (one of the two is 1)
   float scale;                   // times log2(e)
 };
 
 constexpr uint32_t kKeys = 64, kDies = 8;  // keys that pieces are counted in
-constexpr uint32_t kMostParts = 1024;  // of all tiles together
+constexpr uint32_t kPartRows = 1 << 18;  // rows of all parts together
 
 // What k_chunk_plan leaves in the workspace, in words.
 struct Plan {
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
   parts *= (float)a.heads;
   float time = items <= (float)kCUs ? (float)len : fmaxf(work / kCUs, (float)len) + 0.5f * work / items;
   if (parts > 0.f) time += kPart + parts * (kPart / kCUs);
-  if (choice && parts > (float)kMostParts) time = 3.4e38f;
+  if (choice && parts > (float)(kPartRows / a.rows)) time = 3.4e38f;
   uint32_t piece = len;
 #pragma unroll
   for (int m = 1; m < (int)kChoices; m <<= 1) {
@@ -259,8 +259,8 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, uint32_t x, uint32_t
 // A tile of keys and values in LDS, in 16-byte pieces: rows of keys, then rows of values
 // (a page holds them transposed).  Piece p of a row lies at p with some bits flipped by the
 // row's number, so that 16 neighbouring rows of an operand read lie on different banks.
-// Four tiles: one is multiplied by one half of the waves, the one before by the other,
-// and two are on their way.
+// Four tiles: of the one whose values are multiplied, the next, whose keys are, and two that
+// are on their way.
 template <int DP, int WAVES>
 struct Tile {
   static constexpr uint32_t kThreads = 64 * WAVES;
@@ -269,7 +269,10 @@ struct Tile {
   static constexpr uint32_t kPieces = kKeys * kKPieces;               // keys or values
   static constexpr uint32_t kEach = kPieces / kThreads;               // a thread
   static constexpr uint32_t kBuffers = 4;
-  static constexpr uint32_t kBytes = kBuffers * 2 * kPieces * 16;
+  static constexpr uint32_t kSpan = 64 / kGroups;                      // tiles that 64 table entries last for
+  static constexpr uint32_t kTables = kBuffers * 2 * kPieces * 16;     // bytes in front of the tables
+  static constexpr uint32_t kTable = 64 * 4 + 64 * 8;                  // a wave's: entries, addresses of values
+  static constexpr uint32_t kBytes = kTables + WAVES * kTable;
   static __device__ __forceinline__ uint32_t k_flip(uint32_t row) { return kKPieces >= 16 ? row & 15 : (row >> 1) & 7; }
   static __device__ __forceinline__ uint32_t v_flip(uint32_t row) { return kVPieces == 8 ? (row >> 1) & 7 : (row >> 2) & 3; }
   static __device__ __forceinline__ uint32_t k_at(uint32_t row, uint32_t piece) { return row * kKPieces + (piece ^ k_flip(row)); }
@@ -289,14 +292,20 @@ __device__ __forceinline__ floatx16 mfma32<F16>(u32x4 a, u32x4 b, floatx16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Maximum and sum over the two lanes that hold one row.
-__device__ __forceinline__ float half_max(float v) {
-  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+// f(FROM), ..., f(TO - 1), each with a constant.
+template <int FROM, int TO, class F>
+__device__ __forceinline__ void steps(const F& f) {
+  if constexpr (FROM < TO) {
+    f(std::integral_constant<int, FROM>{});
+    steps<FROM + 1, TO>(f);
+  }
 }
-__device__ __forceinline__ float half_sum(float v) {
+
+// Maximum and sum over the two lanes that hold one row.
+template <class F>
+__device__ __forceinline__ float over_row(float v, F f) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  return f(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 
 // Weights are 2^(score * scale - ref) against a reference that follows the row's maximum at
@@ -304,9 +313,9 @@ __device__ __forceinline__ float half_sum(float v) {
 // 16-bit weights up to 2^kSlack lose nothing by it.
 constexpr float kSlack = 8.f;
 
-template <int DP, int RT, int WAVES>
+template <int DP, int WAVES>
 struct PartOf {  // ref[rows], l[rows], then the outputs in the order of the lanes that hold them
-  static constexpr uint32_t kRows = WAVES * 32 * RT;
+  static constexpr uint32_t kRows = WAVES * 32;
   static constexpr uint32_t kFloats = kRows * (DP + 2);
 };
 
@@ -315,10 +324,15 @@ struct PartOf {  // ref[rows], l[rows], then the outputs in the order of the lan
 // more than the last n of the wave's loads are.  (The compiler's own waits for its loads count
 // these too, and so wait longer than they need.)
 __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  // (a base that a vector instruction has just written, as v_readlane does, may be read 5 steps on)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
 __device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load_word_to_lds(const void* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void loads_wait() {
@@ -333,33 +347,21 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-template <class E, int DP, int RT, int WAVES, bool PAD>
+template <class E, int DP, int WAVES, bool PAD>
 __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) {
   using T = Tile<DP, WAVES>;
-  using P = PartOf<DP, RT, WAVES>;
+  using P = PartOf<DP, WAVES>;
   constexpr int KS = DP / 16, DT = DP / 32, NH = T::kKeys / 32;
   extern __shared__ u32x4 lds[];
   u32x4* s_k = lds;                               // [kBuffers][kPieces]
   u32x4* s_v = lds + T::kBuffers * T::kPieces;    // [kBuffers][kPieces]
   __shared__ uint32_t s_item;
-  const uint32_t t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const uint32_t half = lane >> 5, l32 = lane & 31;
-  const uint32_t group = wave >> 2;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t dim = PAD ? a.dim : (uint32_t)DP, in_page = (1u << a.log_block) - 1;
   const uint64_t page_len = (uint64_t)dim << a.log_block;  // elements of a head's page
   const uint32_t page_bytes = (uint32_t)(2 * page_len) * a.heads;
   const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kItems];
 
-  // A wave's load fills 64 neighbouring pieces in LDS, so a lane asks for the piece that
-  // belongs at its place.  Of the wave's first load: the lane's row and piece of it.  (Later
-  // loads are some rows on; kinds of flips repeat with them, but for keys of 256 elements,
-  // where bit 3 changes.)
-  const uint32_t k_row = (64 * wave + lane) / T::kKPieces, k_piece = lane % T::kKPieces ^ T::k_flip(k_row);
-  const uint32_t v_row = (64 * wave + lane) / T::kVPieces, v_piece = lane % T::kVPieces ^ T::v_flip(v_row);
-  constexpr uint32_t kRowStep = T::kThreads / T::kKPieces, vRowStep = T::kThreads / T::kVPieces;
-  static_assert(T::kVPieces == 8 ? vRowStep % 16 == 0 : vRowStep % 16 == 0, "values: the same flips in all loads");
-  static_assert(T::kKPieces == 16 ? kRowStep % 16 == 0 : T::kKPieces == 8 ? kRowStep % 16 == 0 : kRowStep == 8, "keys");
-  const uint32_t k_lane = 2 * (lane / T::kKPieces) * dim;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
   const uint8_t* zeros = reinterpret_cast<const uint8_t*>(a.plan + Plan::kZeros);  // what lies past dim
 
@@ -367,6 +369,11 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
   auto draw = [&] { return __hip_atomic_fetch_add(a.plan + Plan::kQueue + 16 * queue, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
   uint32_t drawn = blockIdx.x / kDies;
   for (;;) {
+    // What follows from a thread's number is worked out anew for each item: kept over the loops
+    // below it took 32 registers, for which operands had to go to memory.
+    uint32_t t = threadIdx.x;
+    keep_here(t);
+    const uint32_t lane = t & 63, half = lane >> 5, l32 = lane & 31;
     if (t == 0) {
       uint32_t x = ~0u;
       while (tried < kDies) {
@@ -388,75 +395,106 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
     // (a piece past the tile's keys; a tile of no keys at all still has rows to write)
     if (it.k0 >= it.k1 && it.piece) continue;
 
-    const uint32_t row_w = wave * 32 * RT;  // the wave's first row
+    // A wave's load fills 64 neighbouring pieces in LDS, so a lane asks for the piece that
+    // belongs at its place.  Of the wave's first load: the lane's row and piece of it.  (Later
+    // loads are some rows on; flips repeat with them, but for keys of 256 elements, where bit 3
+    // changes.)
+    const uint32_t k_row = (64 * wave + lane) / T::kKPieces, k_piece = lane % T::kKPieces ^ T::k_flip(k_row);
+    const uint32_t v_row = (64 * wave + lane) / T::kVPieces, v_piece = lane % T::kVPieces ^ T::v_flip(v_row);
+    constexpr uint32_t kRowStep = T::kThreads / T::kKPieces, vRowStep = T::kThreads / T::kVPieces;
+    static_assert(vRowStep % 16 == 0, "values: the same flips in all loads");
+    static_assert(T::kKPieces == 32 ? kRowStep == 8 : kRowStep % 16 == 0, "keys");
+    const uint32_t k_lane = 2 * (lane / T::kKPieces + 64 * wave / T::kKPieces % 8) * dim;
+
+    const uint32_t row_w = wave * 32;  // the wave's first row
     const uint32_t live = it.rows();
-    const bool works = row_w < live;
-    u32x4 q[RT][KS];
-    uint32_t sees[RT];  // keys that a row sees
+    u32x4 q[KS];
+    const uint32_t row = min(row_w + l32, live - 1), token = it.token + row / it.members;
+    const uint32_t sees = min(it.c.ctx + token + 1, it.c.keys);  // keys that the row sees
+    const uint16_t* from_q = a.q + (uint64_t)(it.c.first + token) * a.q_row +
+                             (uint64_t)(it.head * a.group + it.member + row % it.members) * a.q_head;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const uint32_t r = min(row_w + 32 * i + l32, live - 1), tok = it.token + r / it.members;
-      sees[i] = min(it.c.ctx + tok + 1, it.c.keys);
-      const uint16_t* p = a.q + (uint64_t)(it.c.first + tok) * a.q_row +
-                          (uint64_t)(it.head * a.group + it.member + r % it.members) * a.q_head;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint32_t d = 16 * s + 8 * half;
-        q[i][s] = (!PAD || d < dim) ? *reinterpret_cast<const u32x4*>(p + d) : u32x4{};
-      }
+    for (int s = 0; s < KS; ++s) {
+      const uint32_t d = 16 * s + 8 * half;
+      q[s] = (!PAD || d < dim) ? *reinterpret_cast<const u32x4*>(from_q + d) : u32x4{};
     }
     const uint32_t all_see = min(it.c.ctx + it.token + 1, it.c.keys);  // keys that every row sees
-    floatx16 o[RT][DT];
-    float ref[RT], l[RT];
+    floatx16 o[DT];
+    float ref = -INFINITY, base = 0.f, l = 0.f;  // base: the reference, or 0 where there is none yet
 
     const int32_t* pages = a.table + (uint64_t)it.b * a.width;
     const uint8_t* keys = reinterpret_cast<const uint8_t*>(a.kc + it.head * page_len);
     const uint8_t* values = reinterpret_cast<const uint8_t*>(a.vc + it.head * page_len);
-    // Pages of the groups of 8 keys of kSpan tiles, one a lane.  A table entry is looked at
-    // kSpan tiles after it was asked for: waiting for it in each tile was a third of the
-    // kernel's time.
-    constexpr uint32_t kSpan = 64 / T::kGroups;
-    auto key_of = [&](uint32_t n) { return it.k0 + n * T::kKeys + 8 * lane; };
-    auto ask = [&](uint32_t n) { return (uint32_t)pages[min(key_of(n), it.k1 - 1) >> a.log_block]; };
-    uint32_t coming = 0, have = 0;  // entries asked for, and pages in hand
-    uint64_t gone = 0;              // a bit for each group in hand that does not exist
-    // Sets tile n on its way into its buffer; where a group does not exist, page 0 is read
-    // instead.  A wave's keys of one load lie in one group, so their page is a scalar.
-    auto load = [&](uint32_t n) {
+    // Table entries of the groups of 8 keys of kSpan tiles come into LDS, a copy a wave, kSpan
+    // tiles ahead.  As the first of these tiles is loaded each lane turns an entry into addresses:
+    // of the group's keys, which it keeps, and of its values, which go back into LDS.  What is
+    // left to do in each tile is a few instructions: a wave gets one in about 5 cycles, and
+    // addresses worked out in each tile (100 instructions) took as long as its weights.
+    constexpr uint32_t kSpan = T::kSpan, kLoads = 2 * T::kEach;  // loads of a wave and tile
+    uint32_t* entries = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(lds) + T::kTables + wave * T::kTable);
+    uint64_t* places = reinterpret_cast<uint64_t*>(entries + 64);
+    auto ask = [&](uint32_t n) {
+      const uint32_t at = min(it.k0 + n * T::kKeys + 8 * lane, it.k1 - 1) >> a.log_block;
+      load_word_to_lds(pages, 4 * at, lds0 + T::kTables + wave * T::kTable);
+    };
+    uint32_t keys_lo = 0, keys_hi = 0;  // where the keys of this lane's group are
+    uint64_t gone = 0;                  // a bit for each group that does not exist; page 0 is read instead
+    auto locate = [&](uint32_t n) {
+      const uint32_t key = it.k0 + n * T::kKeys + 8 * lane, id = entries[lane];
+      const bool off = id >= a.blocks || key >= it.k1;
+      gone = __ballot(off);
+      const uint64_t page = (uint64_t)(off ? 0u : id) * page_bytes;
+      const uint64_t k = (uint64_t)(uintptr_t)keys + page + (key & in_page) * (2 * dim);
+      keys_lo = (uint32_t)k;
+      keys_hi = (uint32_t)(k >> 32);
+      places[lane] = (uint64_t)(uintptr_t)values + page + 2 * (key & in_page);
+    };
+    const uint32_t v_lane = (2 * v_row) << a.log_block, v_step = (2 * vRowStep) << a.log_block;
+    // Before tile n's loads: bits of its groups that do not exist; `from`: of the lane's values.
+    auto begin = [&](uint32_t n, uint64_t& from) {
+      if (n % kSpan == 0) {
+        locate(n);
+        ask(n + kSpan);
+      }
       const uint32_t in = n % kSpan * T::kGroups;
-      if (in == 0) {
-        const bool off = coming >= a.blocks || key_of(n) >= it.k1;
-        gone = __ballot(off);
-        have = off ? 0u : coming;
-        coming = ask(n + kSpan);
-      }
-      const uint32_t inside = (it.k0 + n * T::kKeys) & in_page;  // where the tile begins in a page longer than it
-      const uint32_t to = lds0 + (n % T::kBuffers) * T::kPieces * 16 + wave * 1024;
-#pragma unroll
-      for (uint32_t j = 0; j < T::kEach; ++j) {
-        const uint32_t row = 64 * wave / T::kKPieces + kRowStep * j, p = k_piece ^ (T::kKPieces == 32 ? 8 * (j & 1) : 0);
-        const uint8_t* from = keys + (uint64_t)__builtin_amdgcn_readlane(have, in + row / 8) * page_bytes +
-                              (inside + (row & in_page)) * (2 * dim);
-        // (every wave makes the same number of loads: waits count them)
-        if constexpr (PAD) load_to_lds(8 * p < dim ? from + k_lane + 16 * p : zeros, to + T::kThreads * 16 * j);
-        else load_to_lds(from, k_lane + 16 * p, to + T::kThreads * 16 * j);
-      }
-      const uint64_t page = (uint32_t)__shfl((int)have, in + v_piece, 64);
-      const uint8_t* from = values + page * page_bytes + 2 * ((v_row << a.log_block) + inside + (8 * v_piece & in_page));
-#pragma unroll
-      for (uint32_t j = 0; j < T::kEach; ++j) {
-        const uint8_t* row = from + j * ((uint64_t)(2 * vRowStep) << a.log_block);
-        load_to_lds(!PAD || v_row + vRowStep * j < dim ? row : zeros, to + (T::kBuffers * T::kPieces + T::kThreads * j) * 16);
-      }
+      from = places[in + v_piece];
       return (uint32_t)(gone >> in) & ((1u << T::kGroups) - 1);
     };
-    constexpr int kLoads = 2 * T::kEach;  // of a wave and tile
+    // Sets a part of tile n on its way into its buffer: kEach parts of keys, kEach of values.  A
+    // wave's keys of one part lie in one group.  (Every wave makes the same number of loads: waits
+    // count them.)
+    auto load_part = [&](uint32_t n, uint64_t from, uint32_t part) {
+      const uint32_t j = part % T::kEach;
+      const uint32_t to = lds0 + (n % T::kBuffers) * T::kPieces * 16 + wave * 1024 + T::kThreads * 16 * j;
+      if (part < T::kEach) {
+        const uint32_t at = n % kSpan * T::kGroups + (64 * wave / T::kKPieces + kRowStep * j) / 8;
+        const uint8_t* k = reinterpret_cast<const uint8_t*>((uint64_t)__builtin_amdgcn_readlane(keys_hi, at) << 32 |
+                                                            (uint32_t)__builtin_amdgcn_readlane(keys_lo, at));
+        const uint32_t p = k_piece ^ (T::kKPieces == 32 ? 8 * (j & 1) : 0);
+        if constexpr (PAD) load_to_lds(8 * p < dim ? k + k_lane + 16 * p : zeros, to);
+        else load_to_lds(k, k_lane + 16 * p, to);
+      } else {
+        const uint8_t* v = reinterpret_cast<const uint8_t*>(from + v_lane + (uint64_t)v_step * j);
+        load_to_lds(!PAD || v_row + vRowStep * j < dim ? v : zeros, to + T::kBuffers * T::kPieces * 16);
+      }
+    };
+    auto load_keys = [&](uint32_t n) {
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) load_part(n, 0, j);
+    };
+    auto load_values = [&](uint32_t n, uint64_t from) {
+#pragma unroll
+      for (uint32_t j = 0; j < T::kEach; ++j) load_part(n, from, T::kEach + j);
+    };
     // Some row does not see all of tile n, or a page is missing.
     auto edge = [&](uint32_t n, uint32_t absent) { return it.k0 + (n + 1) * T::kKeys > all_see || absent; };
-    // Such a tile, once it is there: values of keys that do not exist become zero, and one
-    // that is not finite is noted, for a weight of zero times it is not zero.
+    // Such a tile, once it is there: values of keys that do not exist become zero, and so do those
+    // that are not finite, for a weight of zero times them is not zero; they are added at the end.
+    bool odd = false;
+    uint32_t mended = ~0u;
     auto mend = [&](uint32_t n, uint32_t absent) {
-      bool odd = false;
+      mended = min(mended, n);
+#pragma unroll 1
       for (uint32_t j = 0; j < T::kEach; ++j) {
         if (PAD && v_row + vRowStep * j >= dim) continue;
         u32x4* at = s_v + (n % T::kBuffers) * T::kPieces + t + T::kThreads * j;
@@ -466,259 +504,268 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           v[w] = real <= 2u * w ? 0u : real == 2u * w + 1 ? v[w] & 0xFFFFu : v[w];
-          odd |= !E::finite2(v[w]);
+          const uint32_t kept = (E::finite2(v[w] & 0xFFFFu) ? v[w] & 0xFFFFu : 0u) |
+                                (E::finite2(v[w] & 0xFFFF0000u) ? v[w] & 0xFFFF0000u : 0u);
+          odd |= kept != v[w];
+          v[w] = kept;
         }
         *at = v;
       }
-      return __syncthreads_or(odd);
+      lds_barrier();
     };
 
-    // The plain loop gives up at the first such value, and the slow one begins again.
-    //
-    // Waves w and w + 4 share a SIMD: while one is at its products, the other is at its
-    // weights, and a barrier after each keeps it so.  (Left to themselves both did the same
-    // at a time.)  In step 2 n the first half of the waves add the values of tile n - 1 and
-    // multiply the keys of tile n, in step 2 n + 1 they turn scores into weights and set a
-    // tile on its way; the second half is a step behind, and a tile ahead with its loads.
-    // Tile n + 1 is there for all after step 2 n + 1.
-    auto run = [&](auto slow) {
-      constexpr bool kSlow = decltype(slow)::value;
+    // Two waves share a SIMD, whose matrix unit takes a product of 32 cycles while it issues four or
+    // so other instructions, as long as they come from the same wave: products of the next tile's
+    // keys and of this one's values alternate with this one's weights, a few instructions after
+    // each product.  (Waves that took turns, one at its products and the other at its weights,
+    // needed the sum of both: a product that waits for the unit keeps the other wave's
+    // instructions back.)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        ref[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[i][d] = floatx16{};
+    for (int d = 0; d < DT; ++d) o[d] = floatx16{};
+    const uint32_t tiles = it.k0 < it.k1 ? (it.k1 - it.k0 + T::kKeys - 1) / T::kKeys : 0;
+    if (tiles) {
+      ask(0);
+      loads_wait<0>();
+      // Bits of the missing groups of a tile and of the next ones; where the next values are.  Keys
+      // are a tile ahead of values with their loads as they are with their products.
+      uint64_t from, from1 = 0, from2 = 0, from3 = 0;
+      uint32_t absent = begin(0, from), absent1 = 0, absent2 = 0, absent3 = 0;
+      load_keys(0);
+      load_values(0, from);
+      if (tiles > 1) {
+        absent1 = begin(1, from1);
+        load_keys(1);
       }
-      const uint32_t tiles = it.k0 < it.k1 ? (it.k1 - it.k0 + T::kKeys - 1) / T::kKeys : 0;
-      if (tiles == 0) return true;
-      coming = ask(0);
-      // bits of the missing groups of the tile at the products, and of those after it
-      uint32_t absent = load(0), absent1 = 0, absent2 = 0, ahead = 1;
-      if (ahead < tiles) absent1 = load(ahead++);
-      if (group && ahead < tiles) absent2 = load(ahead++);
-      if (ahead == 3) loads_wait<2 * kLoads>();
-      else if (ahead == 2) loads_wait<kLoads>();
+      if (tiles > 2) {
+        absent2 = begin(2, from2);
+        load_keys(2);
+      }
+      if (tiles > 1) load_values(1, from1);
+      if (tiles > 3) {
+        absent3 = begin(3, from3);
+        load_keys(3);
+      }
+      if (tiles > 2) load_values(2, from2);
+      // the first tile's and the second one's keys
+      if (tiles > 3) loads_wait<4 * T::kEach>();
+      else if (tiles > 2) loads_wait<3 * T::kEach>();
+      else if (tiles > 1) loads_wait<T::kEach>();
       else loads_wait<0>();
       lds_barrier();
-      if (edge(0, absent) && mend(0, absent) && !kSlow) return false;
+      if (edge(0, absent)) mend(0, absent);
 
-      floatx16 s[RT][NH];
-      u32x4 p[RT][2 * NH];
-      // Operands are read a step of four ahead of the products that take them.  Pieces 2 x on
-      // from the first lie at its place with 2 x flipped, whatever the row: one register
-      // addresses them all (with one each, some were kept in memory, and fetching those
-      // waited for all loads of the next tile).  Row of the operand to key: bits 2 and 3
-      // change places.
+      using Scores = floatx16[NH];
+      u32x4 p[2 * NH];
+      float top;
+      // Steps of a tile: NA operands of keys, NB of values, read kAhead steps before the products
+      // that take them, the next tile's first ones at the end of this one.  Pieces 2 x on from the
+      // first lie at its place with 2 x flipped, whatever the row: one register addresses them all.
+      // Row of the operand to key: bits 2 and 3 change places.
+      constexpr int NA = NH * KS, NB = 2 * NH * DT, kAhead = 7;
+      static_assert((NA + NB) % (kAhead + 1) == 0 && NB > kAhead, "the next tile's operands follow this one's");
       const uint32_t k_first = T::k_at((l32 & 19) | ((l32 & 4) << 1) | ((l32 & 8) >> 1), half);
       const uint32_t v_first = T::v_at(l32, half);
-      constexpr int kStep = 4, NK = NH * KS / kStep, NV = 2 * NH * DT / kStep;
-      u32x4 kf[2][kStep], vf[2][kStep];
-      auto read_keys = [&](uint32_t buf, int i) {
-#pragma unroll
-        for (int e = 0; e < kStep; ++e) {
-          const int h = (kStep * i + e) / KS, x = (kStep * i + e) % KS;
-          kf[i & 1][e] = s_k[((buf * T::kPieces + k_first) ^ 2 * x) + 32 * h * T::kKPieces];
+      u32x4 f[kAhead + 1];
+      auto read = [&](uint32_t n, int step) {  // of the round of tile n: keys of the next, its own values
+        if (step >= NA + NB) {
+          step -= NA + NB;
+          ++n;
         }
-      };
-      auto read_values = [&](uint32_t buf, int i) {
-#pragma unroll
-        for (int e = 0; e < kStep; ++e) {
-          const int g = (kStep * i + e) / DT, d = (kStep * i + e) % DT;
-          vf[i & 1][e] = s_v[((buf * T::kPieces + v_first) ^ 2 * g) + 32 * d * T::kVPieces];
-        }
-      };
-      // o += the weighted values of the tile in buffer `buf`, whose first operands are in hand;
-      // `then`: the buffer whose keys come next
-      auto add_values = [&](uint32_t buf, uint32_t then) {
-        if constexpr (!kSlow) {
-#pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            if (n + 1 < NV) read_values(buf, n + 1);
-            else read_keys(then, 0);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int e = 0; e < kStep; ++e) {
-              const int g = (kStep * n + e) / DT, d = (kStep * n + e) % DT;
-#pragma unroll
-              for (int i = 0; i < RT; ++i) o[i][d] = mfma32<E>(vf[n & 1][e], p[i][g], o[i][d]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }
+        if (step < NA) {
+          const int h = step / KS, x = step % KS;
+          f[step % (kAhead + 1)] = s_k[(((n + 1) % T::kBuffers * T::kPieces + k_first) ^ 2 * x) + 32 * h * T::kKPieces];
         } else {
-          // key by key, leaving out those of weight zero
-          const uint16_t* value = reinterpret_cast<const uint16_t*>(s_v + buf * T::kPieces);
+          const int g = (step - NA) / DT, d = (step - NA) % DT;
+          f[step % (kAhead + 1)] = s_v[((n % T::kBuffers * T::kPieces + v_first) ^ 2 * g) + 32 * d * T::kVPieces];
+        }
+      };
+      // Weights of a tile come in pairs, in the order of the keys; those of 8 keys a lane have to be
+      // there before their values' products.  kPairsA of them go beside the keys' products, the
+      // rest beside the first kBy of the values', and the next tile's maximum beside the others.
+      constexpr int kPairs = 8 * NH, kPairsA = (5 * kPairs + 4) / 8, kBy = (2 * NH - 1) * DT, kRefer = 2;
+      constexpr auto pairs_after = [](int step) {
+        return step < kRefer       ? 0
+               : step < NA         ? (step - kRefer + 1) * kPairsA / (NA - kRefer)
+               : step < NA + kBy   ? kPairsA + (step - NA + 1) * (kPairs - kPairsA) / kBy
+                                   : kPairs;
+      };
+      auto weigh = [&](Scores& s, int pair) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i)
+        for (int e = 2 * pair; e < 2 * pair + 2; ++e)
+          s[e >> 4][e & 15] = __builtin_amdgcn_exp2f(fmaf(s[e >> 4][e & 15], a.scale, -base));
+      };
+      auto pack = [&](Scores& s, int pair) {
+        const int e = 2 * pair;
+        p[pair / 4][pair % 4] = E::pack2(s[e >> 4][e & 15], s[e >> 4][(e & 15) + 1]);
+        l = E::add2(p[pair / 4][pair % 4], l);
+      };
+      auto mask = [&](Scores& s, uint32_t n, uint32_t absent) {
+        // a lane's scores: keys kb + 16 g + 8 half + e are element 8 (g & 1) + e of s[g / 2]
+        const uint32_t kb = it.k0 + n * T::kKeys;
+        if (kb + T::kKeys <= all_see && !absent) return;
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
+        for (int g = 0; g < 2 * NH; ++g) {
+          const uint32_t key = kb + 16 * g + 8 * half;
+          const uint32_t seen = (absent >> (2 * g + half)) & 1 || key >= sees ? 0u : min(sees - key, 8u);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) l[i] += s[i][h][e];
-#pragma unroll 1
-          for (uint32_t x = 0; x < T::kKeys; ++x) {
-            uint32_t h_now = half;
-            keep_here(h_now);
-            float w[RT];
+          for (uint32_t e = 0; e < 8; ++e)
+            if (e >= seen) s[g >> 1][8 * (g & 1) + e] = -INFINITY;
+        }
+      };
+      auto maximum = [&](Scores& s, int from, int to) {
+        if (from == 0) top = s[0][0];
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              w[i] = 0.f;
+        for (int e = from; e < to; e += 2)
+          top = fmaxf(fmaxf(top, s[e >> 4][e & 15]), s[e >> 4][(e & 15) + 1]);
+      };
+      // (whether some score is far above its row's reference needs no maximum over the row's lanes)
+      auto refer = [&] {
+        top *= a.scale;
+        if (!__any(top > ref + kSlack)) return;
+        const float now = fmaxf(ref, over_row(top, [](float x, float y) { return fmaxf(x, y); }));
+        const float keep = ref == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref - now);
+        ref = now;
+        base = now == -INFINITY ? 0.f : now;  // nothing seen: the weights are 2^-inf = 0
+        l *= keep;
 #pragma unroll
-              for (uint32_t e = 0; e < 16 * NH; ++e) w[i] = (x >> 4) * 8 + (x & 7) == e ? s[i][e >> 4][e & 15] : w[i];
-              w[i] = __shfl(w[i], ((x >> 3) & 1) * 32 + l32, 64);
-            }
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float v = E::up(value[T::v_at(32 * d + (e & 3) + 4 * h_now + 8 * (e >> 2), x >> 3) * 8 + (x & 7)]);
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-                  if (w[i] != 0.f) o[i][d][e] = fmaf(w[i], v, o[i][d][e]);
+        for (int d = 0; d < DT; ++d) o[d] *= keep;
+      };
+      // Tile n: its scores are in `s`, and their maximum is known.  kNext: there is a next one, whose
+      // scores go to `t`; kFull: there are at least four.  In the midst of the values' products
+      // all waves are through with the keys of tile n + 1 and with tile n - 1, and the keys of tile
+      // n + 2 and the values of tile n + 1 have arrived; the keys of tile n + 4 and the values of
+      // tile n + 3 set out.
+      constexpr int kMid = NA + NB - kAhead - 1, kEvery = (NA + NB - kMid) / kLoads;
+      static_assert(kEvery >= 1, "a load in a step");
+      auto round = [&](uint32_t n, Scores& s, Scores& t, auto next, auto full) {
+        constexpr bool kNext = decltype(next)::value, kFull = decltype(full)::value;
+        if constexpr (!kNext) {
+          refer();
+          steps<NA, NA + kAhead>([&](auto step) { read(n, step); });
+          steps<0, kPairs>([&](auto pair) { weigh(s, pair); });
+          steps<0, kPairs>([&](auto pair) { pack(s, pair); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        steps<kNext ? 0 : NA, NA + NB>([&](auto at) {
+          constexpr int step = decltype(at)::value;
+          if constexpr (kNext && step == kMid) {
+            if (kFull || n + 3 < tiles) loads_wait<2 * T::kEach>();
+            else if (n + 2 < tiles) loads_wait<T::kEach>();
+            else loads_wait<0>();
+            lds_barrier();
+            if (edge(n + 1, absent1)) mend(n + 1, absent1);
+            from = from3;
+            if (kFull || n + 4 < tiles) absent = begin(n + 4, from3);
+          }
+          if constexpr (kNext || step + kAhead < NA + NB) read(n, step + kAhead);
+          if constexpr (kNext) {
+            if constexpr (step == kRefer) refer();
+            steps<pairs_after(step - 2), pairs_after(step - 1)>([&](auto pair) { pack(s, pair); });
+            if constexpr (step == NA + kBy) mask(t, n + 1, absent1);
+          }
+          if constexpr (step < NA) {
+            constexpr int h = step / KS, x = step % KS;
+            t[h] = mfma32<E>(f[step % (kAhead + 1)], q[x], x ? t[h] : floatx16{});
+          } else {
+            constexpr int g = (step - NA) / DT, d = (step - NA) % DT;
+            static_assert(!kNext || pairs_after(step - 1) >= 4 * (g + 1), "weights before their products");
+            o[d] = mfma32<E>(f[step % (kAhead + 1)], p[g], o[d]);
+          }
+          if constexpr (kNext) {
+            steps<pairs_after(step - 1), pairs_after(step)>([&](auto pair) { weigh(s, pair); });
+            constexpr int in = step - NA - kBy, kEach = 16 * NH / (NB - kBy);
+            if constexpr (in >= 0) maximum(t, in * kEach, (in + 1) * kEach);
+            constexpr int part = (step - kMid) / kEvery;
+            if constexpr (step >= kMid && (step - kMid) % kEvery == 0 && part < (int)kLoads) {
+              if constexpr (part < (int)T::kEach) {
+                if (kFull || n + 4 < tiles) load_part(n + 4, 0, part);
+              } else {
+                if (kFull || n + 3 < tiles) load_part(n + 3, from, part);
               }
-          }
-        }
-      };
-
-      if (group) lds_barrier();
-      // after step 2 n + 1: waits for tile n + 1, all but the loads of the tile after it
-      auto arrive = [&](uint32_t n, uint32_t absent) {
-        if (ahead > n + 2) loads_wait<kLoads>();
-        else loads_wait<0>();
-        lds_barrier();
-        return n + 1 < tiles && edge(n + 1, absent) && mend(n + 1, absent) && !kSlow;
-      };
-      // scores of the tile in buffer `buf`, whose first operands are in hand
-      auto multiply = [&](uint32_t buf) {
-#pragma unroll
-        for (int m = 0; m < NK; ++m) {
-          if (m + 1 < NK) read_keys(buf, m + 1);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int e = 0; e < kStep; ++e) {
-            const int h = (kStep * m + e) / KS, x = (kStep * m + e) % KS;
-#pragma unroll
-            for (int i = 0; i < RT; ++i) s[i][h] = mfma32<E>(kf[m & 1][e], q[i][x], x ? s[i][h] : floatx16{});
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
-        }
-      };
-      if (works) {
-        read_keys(0, 0);
-        multiply(0);
-      }
-      for (uint32_t n = 0;; ++n) {
-        if (!group) lds_barrier();
-        else if (arrive(n, absent1)) return false;
-
-        const uint32_t kb = it.k0 + n * T::kKeys, buf = n % T::kBuffers, then = (n + 1) % T::kBuffers;
-        const uint32_t absent_now = absent;
+        });
+        const uint32_t last = absent;  // of tile n + 4
         absent = absent1;
         absent1 = absent2;
-        if (ahead < tiles) {
-          const uint32_t x = load(ahead++);
-          (group ? absent2 : absent1) = x;
-        }
-        if (works) {
-          // a lane's scores: keys kb + 16 g + 8 half + e are element 8 (g & 1) + e of s[g / 2]
-          if (kb + T::kKeys > all_see || absent_now) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-              for (int g = 0; g < 2 * NH; ++g) {
-                const uint32_t key = kb + 16 * g + 8 * half;
-                const uint32_t seen = (absent_now >> (2 * g + half)) & 1 || key >= sees[i] ? 0u : min(sees[i] - key, 8u);
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e)
-                  if (e >= seen) s[i][g >> 1][8 * (g & 1) + e] = -INFINITY;
-              }
-          }
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            float top = s[i][0][0];
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(top, s[i][h][e]), s[i][h][e + 1]);
-            top = half_max(top) * a.scale;
-            if (__any(top > ref[i] + kSlack)) {
-              const float now = fmaxf(ref[i], top);
-              const float keep = ref[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ref[i] - now);
-              ref[i] = now;
-              l[i] *= keep;
-#pragma unroll
-              for (int d = 0; d < DT; ++d) o[i][d] *= keep;
-            }
-            const float base = ref[i] == -INFINITY ? 0.f : ref[i];  // nothing seen: the weights are 2^-inf = 0
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) s[i][h][e] = __builtin_amdgcn_exp2f(fmaf(s[i][h][e], a.scale, -base));
-            if constexpr (!kSlow) {
-#pragma unroll
-              for (int g = 0; g < 2 * NH; ++g)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  p[i][g][w] = E::pack2(s[i][g >> 1][8 * (g & 1) + 2 * w], s[i][g >> 1][8 * (g & 1) + 2 * w + 1]);
-                  l[i] = E::add2(p[i][g][w], l[i]);
-                }
-            }
-          }
-          if (!kSlow) read_values(buf, 0);
-        }
-        if (group) lds_barrier();
-        else if (arrive(n, absent)) return false;
-
-        if (works) add_values(buf, then);
-        if (n + 1 == tiles) break;
-        if (works) {
-          if (kSlow) read_keys(then, 0);
-          multiply(then);
-        }
+        absent2 = absent3;
+        absent3 = last;
+      };
+      Scores s, t;
+      steps<0, NA>([&](auto step) {
+        constexpr int h = step / KS, x = step % KS;
+        read(~0u, step);
+        s[h] = mfma32<E>(f[step % (kAhead + 1)], q[x], x ? s[h] : floatx16{});
+      });
+      mask(s, 0, absent);
+      maximum(s, 0, 16 * NH);
+      if (tiles > 1) steps<0, kAhead>([&](auto step) { read(0, step); });
+      uint32_t n = 0;
+      for (; n + 5 < tiles; n += 2) {
+        round(n, s, t, std::true_type{}, std::true_type{});
+        round(n + 1, t, s, std::true_type{}, std::true_type{});
       }
-      if (!group) lds_barrier();
-      return true;
-    };
-    if (!run(std::false_type{})) {
-      loads_wait<0>();
-      __syncthreads();  // the buffers are refilled
-      run(std::true_type{});
+      for (; n + 1 < tiles; ++n) {
+        round(n, s, t, std::true_type{}, std::false_type{});
+#pragma unroll
+        for (int h = 0; h < NH; ++h) s[h] = t[h];
+      }
+      round(n, s, t, std::false_type{}, std::false_type{});
     }
 
     const bool whole = it.keys <= piece;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      l[i] = half_sum(l[i]);
-      const uint32_t r = row_w + 32 * i + l32;
-      if (r >= live) continue;
-      if (whole) {
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-        const uint32_t tok = it.token + r / it.members;
-        uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
-                      (uint64_t)(it.head * a.group + it.member + r % it.members) * a.out_head;
+    uint32_t t_end = threadIdx.x;
+    keep_here(t_end);
+    const uint32_t row32 = t_end & 31, dim4 = 4 * (t_end >> 5 & 1);
+    if (__syncthreads_or(odd)) {
+      // values that are not finite and were left out: whatever the weight of a key that a row sees
+      for (uint32_t key = it.k0 + mended * T::kKeys; key < it.k1; ++key) {
+        const uint32_t page = pages[key >> a.log_block];
+        if (page >= a.blocks) continue;
+        const uint8_t* from = values + (uint64_t)page * page_bytes + 2 * (key & in_page);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t at = 32 * d + 8 * g + 4 * half;
-            if (!PAD || at < dim) {
-              *reinterpret_cast<uint32_t*>(p + at) = E::pack2(o[i][d][4 * g] * inv, o[i][d][4 * g + 1] * inv);
-              *reinterpret_cast<uint32_t*>(p + at + 2) = E::pack2(o[i][d][4 * g + 2] * inv, o[i][d][4 * g + 3] * inv);
-            }
+          for (uint32_t e = 0; e < 16; ++e) {
+            const uint32_t at = 32 * d + 8 * (e >> 2) + dim4 + (e & 3);
+            if (PAD && at >= dim) continue;
+            const uint32_t v = *reinterpret_cast<const uint16_t*>(from + ((uint64_t)(2 * at) << a.log_block));
+            if (E::finite2(v)) continue;
+            if (key < sees) o[d][e] += E::up((uint16_t)v);
           }
-      } else {
-        float* part = a.parts + (uint64_t)it.part * P::kFloats;
-        if (half == 0) {
-          part[r] = ref[i];
-          part[P::kRows + r] = l[i];
-        }
-        float* to = part + 2 * P::kRows + r * DP;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<floatx4*>(to + 32 * d + 8 * g + 4 * half) =
-                floatx4{o[i][d][4 * g], o[i][d][4 * g + 1], o[i][d][4 * g + 2], o[i][d][4 * g + 3]};
       }
+    }
+    l = over_row(l, [](float x, float y) { return x + y; });
+    const uint32_t r = row_w + row32;
+    if (r < live && whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const uint32_t tok = it.token + r / it.members;
+      uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
+                    (uint64_t)(it.head * a.group + it.member + r % it.members) * a.out_head;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t at = 32 * d + 8 * g + dim4;
+          if (!PAD || at < dim) {
+            *reinterpret_cast<uint32_t*>(p + at) = E::pack2(o[d][4 * g] * inv, o[d][4 * g + 1] * inv);
+            *reinterpret_cast<uint32_t*>(p + at + 2) = E::pack2(o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv);
+          }
+        }
+    } else if (r < live) {
+      float* part = a.parts + (uint64_t)it.part * P::kFloats;
+      if (dim4 == 0) {
+        part[r] = ref;
+        part[P::kRows + r] = l;
+      }
+      float* to = part + 2 * P::kRows + r * DP;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<floatx4*>(to + 32 * d + 8 * g + dim4) =
+              floatx4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
     }
     __syncthreads();  // the buffers are refilled
   }
@@ -726,9 +773,9 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
 
 // Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes
 // some rows of a tile, a thread four outputs of a row.
-template <class E, int DP, int RT, int WAVES>
+template <class E, int DP, int WAVES>
 __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
-  using P = PartOf<DP, RT, WAVES>;
+  using P = PartOf<DP, WAVES>;
   constexpr uint32_t kFours = DP / 4, kRowsEach = 256 / kFours, kSteps = P::kRows / kRowsEach;
   const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kCut], t = threadIdx.x;
   for (uint64_t unit = blockIdx.x; unit < (uint64_t)items * kSteps; unit += gridDim.x) {
@@ -785,7 +832,7 @@ ChunkPlan plan_chunk(uint32_t heads, uint32_t kv_heads, uint32_t dim, uint32_t r
   p.tile_tokens = std::max(p.rows / group, 1u);
   p.splits = (group + p.rows - 1) / p.rows;
   p.part_off = ((size_t)Plan::words(requests) * 4 + 255) / 256 * 256;
-  p.ws_bytes = p.part_off + (size_t)kMostParts * p.rows * (p.dp + 2) * 4;
+  p.ws_bytes = p.part_off + (size_t)kPartRows * (p.dp + 2) * 4;
   return p;
 }
 
@@ -795,17 +842,17 @@ bool chunk_shape_ok(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t
          (uint64_t)tokens * heads <= (1u << 30);
 }
 
-template <class E, int DP, int RT, int WAVES, bool PAD>
+template <class E, int DP, int WAVES, bool PAD>
 int launch_chunk(const ChunkArgs& a, hipStream_t st) {
   using T = Tile<DP, WAVES>;
-  const auto kernel = k_chunk_attention<E, DP, RT, WAVES, PAD>;
+  const auto kernel = k_chunk_attention<E, DP, WAVES, PAD>;
   if (T::kBytes > 64 * 1024 &&
       hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                           (int)T::kBytes) != hipSuccess)
     return DGT_E_HIP;
   hipLaunchKernelGGL(kernel, dim3(kCUs), dim3(64 * WAVES), T::kBytes, st, a);
   if (int rc = launched()) return rc;
-  hipLaunchKernelGGL((k_chunk_join<E, DP, RT, WAVES>), dim3(4 * kCUs), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_chunk_join<E, DP, WAVES>), dim3(4 * kCUs), dim3(256), 0, st, a);
   return launched();
 }
 
@@ -819,10 +866,10 @@ int launch_chunk(const ChunkArgs& a, uint32_t dp, hipStream_t st) {
   if (int rc = launched()) return rc;
   const bool pad = a.dim != dp;
   switch (dp) {
-    case 64: return pad ? launch_chunk<E, 64, 1, 8, true>(a, st) : launch_chunk<E, 64, 1, 8, false>(a, st);
-    case 128: return pad ? launch_chunk<E, 128, 1, 8, true>(a, st) : launch_chunk<E, 128, 1, 8, false>(a, st);
+    case 64: return pad ? launch_chunk<E, 64, 8, true>(a, st) : launch_chunk<E, 64, 8, false>(a, st);
+    case 128: return pad ? launch_chunk<E, 128, 8, true>(a, st) : launch_chunk<E, 128, 8, false>(a, st);
   }
-  return pad ? launch_chunk<E, 256, 1, 4, true>(a, st) : launch_chunk<E, 256, 1, 4, false>(a, st);
+  return pad ? launch_chunk<E, 256, 4, true>(a, st) : launch_chunk<E, 256, 4, false>(a, st);
 }
 
 }  // namespace
@@ -884,6 +931,7 @@ int dgt_chunk_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t
   a.log_block = (uint32_t)__builtin_ctz(block);
   a.width = width;
   a.blocks = blocks;
+  a.rows = p.rows;
   a.tile_tokens = p.tile_tokens;
   a.splits = p.splits;
   a.scale = scale * 1.4426950408889634f;

@@ -227,3 +227,37 @@ def test_empty_calls():
     args = d["kc"].cuda(), d["vc"].cuda()
     none = torch.empty((0, 2, 64), dtype=d["q"].dtype, device="cuda")
     assert dgt.dgt_chunk_attention(none, *args, _i32(d["table"]), _i32([3]), _i32([0, 0])).numel() == 0
+
+
+@pytest.mark.parametrize("dim,ctx,dtype", [(64, 0, "float16"), (80, 300, "bfloat16"), (128, 20000, "bfloat16"),
+                                           (256, 500, "float16")])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(dim, ctx, dtype):
+    """Single elements of new tokens' values, in some tiles of the keys: their dimension becomes
+    infinite or NaN in the rows from theirs on, all else is as with zeros in their places."""
+    import torch
+    d = _long([ctx], [200], 4, 2, dim, 16, dtype, seed=3)
+    d["table"] = d["table"].cpu().numpy()
+    bad = [(3, 0, 1, float("inf")), (90, 0, dim - 1, -float("inf")), (90, 1, 7, float("nan")), (199, 1, 7, 1.0),
+           (150, 0, 1, float("inf")), (170, 0, 1, -float("inf"))]
+    odd, zero = d["vc"].clone(), d["vc"].clone()
+    want = torch.zeros((200, 4, dim), device="cuda")
+    for at, head, e, value in bad:
+        pos = ctx + at
+        page, cell = int(d["table"][0, pos // 16]), pos % 16
+        odd[page, head, e, cell] = value
+        zero[page, head, e, cell] = value if value == 1.0 else 0.0
+        if value != 1.0:
+            want[at:, 2 * head:2 * head + 2, e] += value
+    got, clean = _run(dict(d, vc=odd)), _run(dict(d, vc=zero))
+    finite = want == 0
+    assert torch.equal(got[finite], clean[finite])
+    assert torch.equal(torch.nan_to_num(got[~finite].float(), 12345.0), torch.nan_to_num(want[~finite], 12345.0))
+
+
+@pytest.mark.parametrize("dim", [64, 72, 128, 192, 256])
+def test_every_number_of_tiles(dim):
+    """Lengths around each multiple of the keys that are multiplied at a time, up to where the loop's
+    first, middle and last rounds have all run."""
+    lens = [1, 31, 32, 33, 63, 64, 65, 96, 97, 127, 129, 191, 193, 255, 257, 321, 384, 449, 513, 577]
+    d = _long([n - 1 for n in lens], [1] * len(lens), 4, 2, dim, 8, "bfloat16", seed=dim)
+    _check_long(d, _run(dict(d, table=d["table"].cpu().numpy())))
