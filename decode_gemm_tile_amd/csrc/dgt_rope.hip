@@ -352,7 +352,7 @@ extern "C" int dgt_rope_store(const void* d_q, const void* d_k, const void* d_v,
   const uint64_t values = blocks == 0 ? 0 : (uint64_t)((tokens + kStoreRows - 1) / kStoreRows) * kv_heads *
                                                 ((dim + kStoreDims - 1) / kStoreDims);
   const uint64_t grid = (uint64_t)tiles * a.runs + values;
-  if (grid > 0x7FFFFFFFull) return DGT_E_SHAPE;
+  if (grid > kMaxGroups) return DGT_E_SHAPE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (type == DGT_ELT_BF16)
     return source == DGT_ELT_F32 ? launch_rope<Bf16, float>(a, (uint32_t)grid, st)

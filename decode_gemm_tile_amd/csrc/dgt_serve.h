@@ -174,6 +174,7 @@ __device__ __forceinline__ void keep_here(uint32_t& v) { asm volatile("" : "+v"(
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool power_of_two(uint32_t v) { return v && !(v & (v - 1)); }
+constexpr uint32_t kMaxGroups = 0xFFFFFF;  // workgroups of 256 threads: a launch counts threads in 32 bits
 inline int launched() { return hipGetLastError() == hipSuccess ? DGT_OK : DGT_E_HIP; }
 
 // Page sizes that the operators take, and their bound on requests per call.

@@ -648,7 +648,7 @@ VerifyPlan plan_verify(uint32_t tokens, uint32_t vocab, uint32_t requests) {
 constexpr uint32_t kMaxVocab = 1u << 22;
 bool verify_shape_ok(uint32_t tokens, uint32_t vocab, uint32_t requests) {
   return vocab >= 1 && vocab <= kMaxVocab && requests <= kMaxRequests && tokens <= (1u << 20) &&
-         (uint64_t)tokens * ((vocab + kSeg - 1) / kSeg) <= 0x7FFFFFFFull;
+         (uint64_t)tokens * ((vocab + kSeg - 1) / kSeg) <= kMaxGroups;
 }
 
 template <class L>

@@ -379,7 +379,8 @@ int dgt_lora_add(const float* d_y, uint64_t y_row, const uint16_t* d_x, uint64_t
  *   d_q_weight, d_k_weight: float[dim] or NULL.  eps >= 0.
  *   type: BF16 or F16, of d_q_out and the pages.  d_q_out [tokens, heads, dim], strides
  *          multiples of 8; it does not overlap an input.
- * dim: a multiple of 8 up to 256.  d_q_out and the pages are 16-byte aligned.
+ * dim: a multiple of 8 up to 256.  d_q_out and the pages are 16-byte aligned.  tokens <= 2^20,
+ * and what the launch can count: about 2^29 token heads.
  * Errors: E_ARG, E_SHAPE, E_UNSUPPORTED, E_HIP. */
 int dgt_rope_store(const void* d_q, const void* d_k, const void* d_v, uint32_t source, int64_t q_row,
                    int64_t q_head, int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
@@ -434,7 +435,7 @@ int dgt_chunk_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t
  *   d_accepted: int32[requests], how many (0 for a request of no rows).
  *   d_next: int32[requests] (-1 for a request of no rows).
  *   d_ws: dgt_verify_workspace(...) bytes, any contents.
- * vocab <= 2^22; tokens * vocab may pass 2^32.
+ * vocab <= 2^22; tokens * ceil(vocab / 4096) < 2^24 (tokens * vocab may pass 2^32).
  * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED (draft probabilities of a tree), E_HIP. */
 size_t dgt_verify_workspace(uint32_t tokens, uint32_t vocab, uint32_t requests);
 int dgt_verify(uint32_t type, const void* d_logits, uint64_t logits_row, const int32_t* d_draft,

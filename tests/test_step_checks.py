@@ -183,3 +183,12 @@ def test_empty_calls_do_nothing():
                                  None, 0, None) == 0
     assert L.dgt_verify(3, None, 50, None, None, 0, None, None, None, None, None, 0, 0, 50, None, None, None, None, 0,
                         None) == 0
+
+
+def test_more_work_than_a_launch_counts():
+    """Workgroups past 2^24 of 256 threads are refused before anything is launched."""
+    L, p = dgt.lib(), 256
+    assert L.dgt_rope_store(p, p, p, 3, 65536, 8, 65536, 8, 65536, 8, p, p, 1 << 17, 8192, 8192, 8, None, 0, 0, None, None,
+                            1e-6, 1, p, 65536, 8, p, p, 8, 16, None) == -2
+    assert L.dgt_verify_workspace(1 << 15, 1 << 21, 4) == 0 and L.dgt_verify_workspace((1 << 15) - 1, 1 << 21, 4) > 0
+    assert L.dgt_verify(3, p, 1 << 21, p, None, 0, None, p, None, p, p, 4, 1 << 15, 1 << 21, p, p, p, p, 1 << 40, None) == -2
