@@ -108,10 +108,11 @@ __device__ __forceinline__ double exp2_64(double z) {
 }
 
 constexpr double kLog2e = 1.44269504088896340736;
-// What logits are multiplied by: 1 / T in powers of two, or 0 for the largest logit's token.
+// What logits are multiplied by: 1 / T in powers of two, or 0 for the largest logit's token.  (Of an
+// infinite T a little is left, less than of any finite one: all tokens weigh the same.)
 __device__ __forceinline__ double heat(const VerifyArgs& a, uint32_t b) {
   const float t = a.temperature ? a.temperature[b] : 1.f;
-  return t > 0.f ? kLog2e / (double)t : 0.0;
+  return t > 0.f ? fmax(kLog2e / (double)t, 4e-39) : 0.0;
 }
 __device__ __forceinline__ float heat32(double c) { return (float)fmin(c, 3e38); }
 

@@ -420,7 +420,8 @@ int dgt_chunk_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t
  *   With no child left the next token is the first v whose running sum of r passes
  *   s * sum(r): r = p without the refused tokens, or max(p - q, 0) after a refusal.
  * T = d_temperature[b] (NULL: 1); T <= 0 (or not a number): a child is accepted if its
- * token is the row's largest logit's (the first of equals), and so is the next token.
+ * token is the row's largest logit's (the first of equals), and so is the next token.  With
+ * T = +inf all tokens that are not excluded weigh the same.
  * Sums over a vocabulary are fp64, and so are the exponentials in them.
  *   d_logits: [tokens, vocab] of type `type` (F32, BF16, F16), row stride in elements;
  *          -inf excludes a token.  A row with a NaN or +inf, or of -inf alone, ends the

@@ -284,3 +284,12 @@ def test_no_rows():
     d = _make(19, [0, 0], 50, tree=True)
     v = _run(d)
     assert v.accepted.tolist() == [0, 0] and v.next.tolist() == [-1, -1]
+
+
+@pytest.mark.parametrize("kind", ["chain", "probs", "tree"])
+def test_an_infinite_temperature(kind):
+    """All tokens weigh the same; the largest finite temperature comes close to it."""
+    d = _make(8, [6] * 12, 900, tree=int(kind == "tree"), probs=kind == "probs",
+              temperature=[float("inf"), 3.4e38] * 6)
+    _check(d, _run(d))
+    assert len(set(_run(d).next.tolist())) > 6  # not one most likely token after the other
