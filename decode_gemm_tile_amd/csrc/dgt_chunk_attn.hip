@@ -43,10 +43,11 @@ struct Plan {
   static constexpr uint32_t kQueue = 0;        // a counter a die, 64 bytes apart
   static constexpr uint32_t kPiece = 128;      // keys of a piece, a multiple of kKeys
   static constexpr uint32_t kItems = 129;      // in all
-  static constexpr uint32_t kCut = 130;        // items among which those of cut tiles are
+  static constexpr uint32_t kCut = 130;        // cut tiles
   static constexpr uint32_t kZeros = 144;      // 16 bytes
   static constexpr uint32_t kRecord = 160;     // [requests][kWords], the longest request first
-  static constexpr uint32_t kWords = 8;        // item, part: the first ones; request, first row, rows, cached keys
+  // item, part: the first ones; request, first row, rows, cached keys, first cut tile
+  static constexpr uint32_t kItem = 0, kTile = 6, kWords = 8;
   static __host__ __device__ constexpr uint32_t words(uint32_t requests) { return kRecord + kWords * requests; }
 };
 
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
   extern __shared__ uint32_t s_keys[];  // [requests] keys, [requests] tiles, [requests] the order
   uint32_t *s_tiles = s_keys + a.requests, *s_order = s_tiles + a.requests;
   __shared__ float s_f[kPlanThreads / 64], s_items[kPlanThreads], s_parts[kPlanThreads];
-  __shared__ uint32_t s_u[kPlanThreads / 64], s_v[kPlanThreads / 64];
+  __shared__ uint32_t s_u[kPlanThreads / 64], s_v[kPlanThreads / 64], s_w[kPlanThreads / 64];
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
   float work = 0.f, rows = 0.f;
   uint32_t most = 0;
@@ -157,48 +158,54 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
     s_order[rank] = b;
   }
   __syncthreads();
-  uint32_t item = 0, part = 0;
+  uint32_t item = 0, part = 0, cut = 0;
   for (uint32_t i0 = 0; i0 < a.requests; i0 += kPlanThreads) {
     const uint32_t i = i0 + t;
     Chunk c = {};
-    uint32_t n = 0, p = 0;
+    uint32_t n = 0, p = 0, c1 = 0;
     if (i < a.requests) {
       c = chunk_of(a, s_order[i]);
       const uint32_t pieces = max((uint32_t)(((uint64_t)c.keys + piece - 1) / piece), 1u);
       n = c.tiles * pieces * a.heads;
       p = pieces > 1 ? n : 0;
+      c1 = pieces > 1 ? c.tiles * a.heads : 0;
     }
-    uint32_t sn = n, sp = p;  // running sums of both
+    uint32_t sn = n, sp = p, sc = c1;  // running sums of them
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t on = __shfl_up(sn, d, 64), op = __shfl_up(sp, d, 64);
+      const uint32_t on = __shfl_up(sn, d, 64), op = __shfl_up(sp, d, 64), oc = __shfl_up(sc, d, 64);
       if (lane >= (uint32_t)d) {
         sn += on;
         sp += op;
+        sc += oc;
       }
     }
     if (lane == 63) {
       s_u[wave] = sn;
       s_v[wave] = sp;
+      s_w[wave] = sc;
     }
     __syncthreads();
-    uint32_t bn = item, bp = part;
+    uint32_t bn = item, bp = part, bc = cut;
     for (uint32_t w = 0; w < kPlanThreads / 64; ++w) {
       if (w == wave) {
         sn += bn;
         sp += bp;
+        sc += bc;
       }
       bn += s_u[w];
       bp += s_v[w];
+      bc += s_w[w];
     }
     __syncthreads();
     if (i < a.requests) {
       u32x4* r = reinterpret_cast<u32x4*>(a.plan + Plan::kRecord + Plan::kWords * i);
       r[0] = u32x4{sn - n, sp - p, s_order[i], c.first};
-      r[1] = u32x4{c.count, c.ctx, 0u, 0u};
+      r[1] = u32x4{c.count, c.ctx, sc - c1, 0u};
     }
     item = bn;
     part = bp;
+    cut = bc;
   }
   // every workgroup begins with the item of its own number
   if (t < kDies) a.plan[Plan::kQueue + 16 * t] = kCUs / kDies;
@@ -206,8 +213,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
   if (t == 0) {
     a.plan[Plan::kPiece] = piece;
     a.plan[Plan::kItems] = sound ? item : 0;
-    // cut tiles come first where requests are sorted
-    a.plan[Plan::kCut] = !sound || part == 0 ? 0 : a.requests <= kMaxSorted ? part : item;
+    a.plan[Plan::kCut] = sound ? cut : 0;
   }
 }
 
@@ -220,14 +226,16 @@ struct Item {
   __device__ __forceinline__ uint32_t rows() const { return tokens * members; }
 };
 
-// Item x of the call.  Of a request: tiles from the last, which sees most, pieces, heads.
+// Item x of the call, or (BY = Plan::kTile) the first item of cut tile x.  Of a request: tiles
+// from the last, which sees most, pieces, heads.
+template <uint32_t BY>
 __device__ __forceinline__ Item item_of(const ChunkArgs& a, uint32_t x, uint32_t piece, uint32_t rows) {
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t* records = a.plan + Plan::kRecord;
   uint32_t lo = 0, len = a.requests;
   while (len > 1) {
     const uint32_t step = (len + 63) / 64, at = lane * step;
-    const bool before = lane == 0 || (at < len && records[Plan::kWords * (lo + at)] <= x);
+    const bool before = lane == 0 || (at < len && records[Plan::kWords * (lo + at) + BY] <= x);
     const uint32_t hits = (uint32_t)__popcll(__ballot(before));
     const uint32_t skip = (hits - 1) * step;
     lo += skip;
@@ -240,8 +248,12 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, uint32_t x, uint32_t
   it.c = Chunk{r0[3], r1[0], r1[1], 0, 0};
   size_chunk(a, it.c);
   it.pieces = max((uint32_t)(((uint64_t)it.c.keys + piece - 1) / piece), 1u);
-  const uint32_t in = x - r0[0], rest = in / a.heads;
+  uint32_t in = x - (BY == Plan::kItem ? r0[0] : r1[2]), rest = in / a.heads;
   it.head = in - rest * a.heads;
+  if (BY == Plan::kTile) {
+    rest *= it.pieces;
+    in = rest * a.heads + it.head;
+  }
   it.piece = rest % it.pieces;
   it.tile = it.c.tiles - 1 - rest / it.pieces;
   it.part = r0[1] + in;
@@ -391,7 +403,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
     __syncthreads();
     if (x == ~0u) break;
     if (t == 0) drawn = draw();  // the next item's number is on its way while this one is worked on
-    const Item it = item_of(a, x, piece, P::kRows);
+    const Item it = item_of<Plan::kItem>(a, x, piece, P::kRows);
     // (a piece past the tile's keys; a tile of no keys at all still has rows to write)
     if (it.k0 >= it.k1 && it.piece) continue;
 
@@ -788,30 +800,31 @@ template <class E, int DP, int WAVES>
 __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
   using P = PartOf<DP, WAVES>;
   constexpr uint32_t kFours = DP / 4, kRowsEach = 256 / kFours, kSteps = P::kRows / kRowsEach;
-  const uint32_t piece = a.plan[Plan::kPiece], items = a.plan[Plan::kCut], t = threadIdx.x;
-  for (uint64_t unit = blockIdx.x; unit < (uint64_t)items * kSteps; unit += gridDim.x) {
-    const Item it = item_of(a, (uint32_t)(unit / kSteps), piece, P::kRows);
-    if (it.piece || it.keys <= piece) continue;
+  const uint32_t piece = a.plan[Plan::kPiece], cut = a.plan[Plan::kCut], t = threadIdx.x;
+  for (uint64_t unit = blockIdx.x; unit < (uint64_t)cut * kSteps; unit += gridDim.x) {
+    const Item it = item_of<Plan::kTile>(a, (uint32_t)(unit / kSteps), piece, P::kRows);
+    if (it.keys <= piece) continue;  // a tile that sees fewer keys is one piece
     const uint32_t r = (uint32_t)(unit % kSteps) * kRowsEach + t / kFours, d = 4 * (t % kFours);
     if (r >= it.rows()) continue;
-    // item numbers of a tile's pieces lie `heads` apart; four are asked for at a time
+    // item numbers of a tile's pieces lie `heads` apart; eight are asked for at a time
+    constexpr uint32_t kAtOnce = 8;
     float m = -INFINITY, l = 0.f;
     floatx4 o = {};
     const uint32_t count = (it.keys + piece - 1) / piece;
     const float* part = a.parts + (uint64_t)it.part * P::kFloats;
     const uint64_t step = (uint64_t)a.heads * P::kFloats;
-    for (uint32_t k0 = 0; k0 < count; k0 += 4) {
-      float mw[4], lw[4];
-      floatx4 ow[4];
+    for (uint32_t k0 = 0; k0 < count; k0 += kAtOnce) {
+      float mw[kAtOnce], lw[kAtOnce];
+      floatx4 ow[kAtOnce];
 #pragma unroll
-      for (uint32_t k = 0; k < 4; ++k) {
+      for (uint32_t k = 0; k < kAtOnce; ++k) {
         const float* from = part + min(k0 + k, count - 1) * step;
         mw[k] = from[r];
         lw[k] = from[P::kRows + r];
         ow[k] = *reinterpret_cast<const floatx4*>(from + 2 * P::kRows + r * DP + d);
       }
 #pragma unroll
-      for (uint32_t k = 0; k < 4; ++k) {
+      for (uint32_t k = 0; k < kAtOnce; ++k) {
         if (k0 + k >= count) break;
         const float now = fmaxf(m, mw[k]), base = now == -INFINITY ? 0.f : now;
         const float f = __builtin_amdgcn_exp2f(m - base), fw = __builtin_amdgcn_exp2f(mw[k] - base);
