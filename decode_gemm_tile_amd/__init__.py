@@ -1022,20 +1022,20 @@ def _layers(k_cache, v_cache):
 def _fast_layers(k_cache, v_cache):
     """The same without the words: the five numbers, or None where something is wrong."""
     import torch
-    front = k_cache.shape[:-4]
-    blocks, heads, block, dim = k_cache.shape[-4:]
+    *front, blocks, heads, block, dim = k_cache.shape
     dtype = k_cache.dtype
-    good = (len(front) < 2 and k_cache.device.type == "cuda" and (dtype is torch.bfloat16 or dtype is torch.float16)
-            and k_cache.is_contiguous() and v_cache.dtype is dtype and v_cache.shape == front + (blocks, heads, dim, block)
-            and v_cache.is_contiguous() and v_cache.device == k_cache.device)
+    good = (len(front) < 2 and k_cache.is_cuda and (dtype is torch.bfloat16 or dtype is torch.float16)
+            and k_cache.is_contiguous() and v_cache.dtype is dtype and v_cache.shape == (*front, blocks, heads, dim, block)
+            and v_cache.is_contiguous() and v_cache.get_device() == k_cache.get_device())
     return (front[0] if front else 1, blocks, heads, block, dim) if good else None
 
 
 def _i32(dev, *arrays):
     """True if all (tensor, shape) are contiguous int32 tensors on `dev`."""
     import torch
+    i32, index = torch.int32, dev.index
     for t, shape in arrays:
-        if not (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and t.device == dev):
+        if not (t.dtype is i32 and t.get_device() == index and t.shape == shape and t.is_contiguous()):
             return False
     return True
 
