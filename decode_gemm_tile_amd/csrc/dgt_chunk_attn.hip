@@ -533,7 +533,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
     // needed the sum of both: a product that waits for the unit keeps the other wave's
     // instructions back.)
     //
-    // 3 prompts of 8190 tokens, 32 heads over 8 of 128, bf16: 824 us, 988 TFLOP/s (in turns 861; the
+    // 3 prompts of 8190 tokens, 32 heads over 8 of 128, bf16: 800 us, 1017 TFLOP/s (in turns 861; the
     // products alone 467).  The matrix units are busy for 46% of the cycles, at 1.8 to 2 GHz of 2.4:
     // the clock gives way to power (3 x 4096 tokens: 950 TFLOP/s, with zeros for keys and values 1125).
 #pragma unroll
@@ -794,52 +794,71 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
   }
 }
 
-// Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes
-// some rows of a tile, a thread four outputs of a row.
+// Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes some
+// rows of a tile, a thread four outputs of a row in a quarter of the parts, eight of which are
+// asked for at a time; the quarters meet in LDS.  (One thread for all parts of a row took 44 us
+// of 64 where one tile had 125.)
+struct Joined {
+  float m = -INFINITY, l = 0.f;
+  floatx4 o = {};
+  __device__ __forceinline__ void add(float om, float ol, floatx4 oo) {
+    const float now = fmaxf(m, om), base = now == -INFINITY ? 0.f : now;
+    const float f = __builtin_amdgcn_exp2f(m - base), g = __builtin_amdgcn_exp2f(om - base);
+    m = now;
+    l = fmaf(ol, g, l * f);
+    o = o * f + oo * g;
+  }
+};
+
 template <class E, int DP, int WAVES>
 __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
   using P = PartOf<DP, WAVES>;
-  constexpr uint32_t kFours = DP / 4, kRowsEach = 256 / kFours, kSteps = P::kRows / kRowsEach;
+  constexpr uint32_t kFours = DP / 4, kQuarters = 4, kRowsEach = 256 / kFours / kQuarters, kSteps = P::kRows / kRowsEach;
+  constexpr uint32_t kAtOnce = 8;
+  __shared__ floatx4 s_o[256];
+  __shared__ float s_m[256], s_l[256];
   const uint32_t piece = a.plan[Plan::kPiece], cut = a.plan[Plan::kCut], t = threadIdx.x;
+  const uint32_t d = 4 * (t % kFours), row = t / kFours % kRowsEach, quarter = t / (kFours * kRowsEach);
   for (uint64_t unit = blockIdx.x; unit < (uint64_t)cut * kSteps; unit += gridDim.x) {
     const Item it = item_of<Plan::kTile>(a, (uint32_t)(unit / kSteps), piece, P::kRows);
-    if (it.keys <= piece) continue;  // a tile that sees fewer keys is one piece
-    const uint32_t r = (uint32_t)(unit % kSteps) * kRowsEach + t / kFours, d = 4 * (t % kFours);
-    if (r >= it.rows()) continue;
-    // item numbers of a tile's pieces lie `heads` apart; eight are asked for at a time
-    constexpr uint32_t kAtOnce = 8;
-    float m = -INFINITY, l = 0.f;
-    floatx4 o = {};
-    const uint32_t count = (it.keys + piece - 1) / piece;
+    const uint32_t r = (uint32_t)(unit % kSteps) * kRowsEach + row;
+    // (a tile that sees fewer keys is one piece)
+    if (it.keys <= piece || r - row >= it.rows()) continue;
+    // item numbers of a tile's pieces lie `heads` apart
+    const uint32_t count = (it.keys + piece - 1) / piece, each = (count + kQuarters - 1) / kQuarters;
+    const uint32_t first = min(quarter * each, count), last = min(first + each, count);
     const float* part = a.parts + (uint64_t)it.part * P::kFloats;
     const uint64_t step = (uint64_t)a.heads * P::kFloats;
-    for (uint32_t k0 = 0; k0 < count; k0 += kAtOnce) {
-      float mw[kAtOnce], lw[kAtOnce];
-      floatx4 ow[kAtOnce];
+    Joined sum;
+    for (uint32_t k0 = first; k0 < last; k0 += kAtOnce) {
+      float m[kAtOnce], l[kAtOnce];
+      floatx4 o[kAtOnce];
 #pragma unroll
       for (uint32_t k = 0; k < kAtOnce; ++k) {
-        const float* from = part + min(k0 + k, count - 1) * step;
-        mw[k] = from[r];
-        lw[k] = from[P::kRows + r];
-        ow[k] = *reinterpret_cast<const floatx4*>(from + 2 * P::kRows + r * DP + d);
+        const float* from = part + min(k0 + k, last - 1) * step;
+        m[k] = from[r];
+        l[k] = from[P::kRows + r];
+        o[k] = *reinterpret_cast<const floatx4*>(from + 2 * P::kRows + r * DP + d);
       }
 #pragma unroll
-      for (uint32_t k = 0; k < kAtOnce; ++k) {
-        if (k0 + k >= count) break;
-        const float now = fmaxf(m, mw[k]), base = now == -INFINITY ? 0.f : now;
-        const float f = __builtin_amdgcn_exp2f(m - base), fw = __builtin_amdgcn_exp2f(mw[k] - base);
-        m = now;
-        l = fmaf(lw[k], fw, l * f);
-        o = o * f + ow[k] * fw;
-      }
+      for (uint32_t k = 0; k < kAtOnce; ++k)
+        if (k0 + k < last) sum.add(m[k], l[k], o[k]);
     }
-    if (d >= a.dim) continue;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const uint32_t tok = it.token + r / it.members;
-    uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
-                  (uint64_t)(it.head * a.group + it.member + r % it.members) * a.out_head + d;
-    *reinterpret_cast<uint32_t*>(p) = E::pack2(o[0] * inv, o[1] * inv);
-    *reinterpret_cast<uint32_t*>(p + 2) = E::pack2(o[2] * inv, o[3] * inv);
+    s_m[t] = sum.m;
+    s_l[t] = sum.l;
+    s_o[t] = sum.o;
+    __syncthreads();
+    if (quarter == 0 && r < it.rows() && d < a.dim) {
+#pragma unroll
+      for (uint32_t x = t + 256 / kQuarters; x < 256; x += 256 / kQuarters) sum.add(s_m[x], s_l[x], s_o[x]);
+      const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+      const uint32_t tok = it.token + r / it.members;
+      uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
+                    (uint64_t)(it.head * a.group + it.member + r % it.members) * a.out_head + d;
+      *reinterpret_cast<uint32_t*>(p) = E::pack2(sum.o[0] * inv, sum.o[1] * inv);
+      *reinterpret_cast<uint32_t*>(p + 2) = E::pack2(sum.o[2] * inv, sum.o[3] * inv);
+    }
+    __syncthreads();  // the LDS is free again
   }
 }
 
@@ -876,7 +895,7 @@ int launch_chunk(const ChunkArgs& a, hipStream_t st) {
     return DGT_E_HIP;
   hipLaunchKernelGGL(kernel, dim3(kCUs), dim3(64 * WAVES), T::kBytes, st, a);
   if (int rc = launched()) return rc;
-  hipLaunchKernelGGL((k_chunk_join<E, DP, WAVES>), dim3(4 * kCUs), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_chunk_join<E, DP, WAVES>), dim3(8 * kCUs), dim3(256), 0, st, a);
   return launched();
 }
 
