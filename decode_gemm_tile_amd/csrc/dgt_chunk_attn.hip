@@ -44,6 +44,7 @@ struct Plan {
   static constexpr uint32_t kPiece = 128;      // keys of a piece, a multiple of kKeys
   static constexpr uint32_t kItems = 129;      // in all
   static constexpr uint32_t kCut = 130;        // cut tiles
+  static constexpr uint32_t kMost = 131;       // pieces of the longest
   static constexpr uint32_t kZeros = 144;      // 16 bytes
   static constexpr uint32_t kRecord = 160;     // [requests][kWords], the longest request first
   // item, part: the first ones; request, first row, rows, cached keys, first cut tile
@@ -214,6 +215,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
     a.plan[Plan::kPiece] = piece;
     a.plan[Plan::kItems] = sound ? item : 0;
     a.plan[Plan::kCut] = sound ? cut : 0;
+    a.plan[Plan::kMost] = (uint32_t)(((uint64_t)most + piece - 1) / piece);
   }
 }
 
@@ -533,8 +535,8 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
     // needed the sum of both: a product that waits for the unit keeps the other wave's
     // instructions back.)
     //
-    // 3 prompts of 8190 tokens, 32 heads over 8 of 128, bf16: 800 us, 1017 TFLOP/s (in turns 861; the
-    // products alone 467).  The matrix units are busy for 46% of the cycles, at 1.8 to 2 GHz of 2.4:
+    // 3 prompts of 8190 tokens, 32 heads over 8 of 128, bf16: 797-837 us on several cards, 973-1021
+    // TFLOP/s (in turns 861 where it is 820; the products alone 467).  The matrix units are busy for 46% of the cycles, at 1.8 to 2 GHz of 2.4:
     // the clock gives way to power (3 x 4096 tokens: 950 TFLOP/s, with zeros for keys and values 1125).
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = floatx16{};
@@ -795,9 +797,11 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
 }
 
 // Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes some
-// rows of a tile, a thread four outputs of a row in a quarter of the parts, eight of which are
-// asked for at a time; the quarters meet in LDS.  (One thread for all parts of a row took 44 us
-// of 64 where one tile had 125.)
+// rows of a tile, a thread four outputs of a row in all parts, eight of which are asked for at a
+// time.  Where a tile has more, a workgroup takes a quarter as many rows, a thread a quarter of the
+// parts, and the quarters meet in LDS.  (26 tokens behind 16000 keys of one head, 125 parts: 7 us in
+// quarters, 44 without; 128 tokens behind 4000 of 8 requests, 4 parts: the call 106 us without, 124
+// in quarters.)
 struct Joined {
   float m = -INFINITY, l = 0.f;
   floatx4 o = {};
@@ -813,19 +817,20 @@ struct Joined {
 template <class E, int DP, int WAVES>
 __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
   using P = PartOf<DP, WAVES>;
-  constexpr uint32_t kFours = DP / 4, kQuarters = 4, kRowsEach = 256 / kFours / kQuarters, kSteps = P::kRows / kRowsEach;
-  constexpr uint32_t kAtOnce = 8;
+  constexpr uint32_t kFours = DP / 4, kQuarters = 4, kAtOnce = 8;
   __shared__ floatx4 s_o[256];
   __shared__ float s_m[256], s_l[256];
   const uint32_t piece = a.plan[Plan::kPiece], cut = a.plan[Plan::kCut], t = threadIdx.x;
-  const uint32_t d = 4 * (t % kFours), row = t / kFours % kRowsEach, quarter = t / (kFours * kRowsEach);
-  for (uint64_t unit = blockIdx.x; unit < (uint64_t)cut * kSteps; unit += gridDim.x) {
-    const Item it = item_of<Plan::kTile>(a, (uint32_t)(unit / kSteps), piece, P::kRows);
-    const uint32_t r = (uint32_t)(unit % kSteps) * kRowsEach + row;
+  const uint32_t quarters = a.plan[Plan::kMost] > kAtOnce ? kQuarters : 1;
+  const uint32_t rows = 256 / kFours / quarters, steps = P::kRows / rows;  // of a workgroup, of a tile
+  const uint32_t d = 4 * (t % kFours), row = t / kFours % rows, quarter = t / kFours / rows;
+  for (uint64_t unit = blockIdx.x; unit < (uint64_t)cut * steps; unit += gridDim.x) {
+    const Item it = item_of<Plan::kTile>(a, (uint32_t)(unit / steps), piece, P::kRows);
+    const uint32_t r = (uint32_t)(unit % steps) * rows + row;
     // (a tile that sees fewer keys is one piece)
     if (it.keys <= piece || r - row >= it.rows()) continue;
     // item numbers of a tile's pieces lie `heads` apart
-    const uint32_t count = (it.keys + piece - 1) / piece, each = (count + kQuarters - 1) / kQuarters;
+    const uint32_t count = (it.keys + piece - 1) / piece, each = (count + quarters - 1) / quarters;
     const uint32_t first = min(quarter * each, count), last = min(first + each, count);
     const float* part = a.parts + (uint64_t)it.part * P::kFloats;
     const uint64_t step = (uint64_t)a.heads * P::kFloats;
@@ -844,13 +849,15 @@ __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
       for (uint32_t k = 0; k < kAtOnce; ++k)
         if (k0 + k < last) sum.add(m[k], l[k], o[k]);
     }
-    s_m[t] = sum.m;
-    s_l[t] = sum.l;
-    s_o[t] = sum.o;
-    __syncthreads();
+    if (quarters > 1) {
+      s_m[t] = sum.m;
+      s_l[t] = sum.l;
+      s_o[t] = sum.o;
+      __syncthreads();
+    }
     if (quarter == 0 && r < it.rows() && d < a.dim) {
-#pragma unroll
-      for (uint32_t x = t + 256 / kQuarters; x < 256; x += 256 / kQuarters) sum.add(s_m[x], s_l[x], s_o[x]);
+      if (quarters > 1)
+        for (uint32_t x = t + 256 / kQuarters; x < 256; x += 256 / kQuarters) sum.add(s_m[x], s_l[x], s_o[x]);
       const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
       const uint32_t tok = it.token + r / it.members;
       uint16_t* p = a.out + (uint64_t)(it.c.first + tok) * a.out_row +
@@ -858,7 +865,7 @@ __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
       *reinterpret_cast<uint32_t*>(p) = E::pack2(sum.o[0] * inv, sum.o[1] * inv);
       *reinterpret_cast<uint32_t*>(p + 2) = E::pack2(sum.o[2] * inv, sum.o[3] * inv);
     }
-    __syncthreads();  // the LDS is free again
+    if (quarters > 1) __syncthreads();  // the LDS is free again
   }
 }
 
