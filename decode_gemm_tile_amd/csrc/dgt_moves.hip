@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t kept_of(const KeepArgs& a, uint32_t b, uint3
 
 // Lengths, and the pages past them, by one workgroup: the list's order is the requests'.
 // A column past the kept tokens begins at or behind the cached ones' end, so a new token
-// lies first in it and its slot names the page.
+// lies first in it and its slot names the page.  One that the plan gave no slot (a bad link,
+// an index past the mask) has taken its page all the same: then the table names it.
 __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
   const uint32_t log = a.pool.log_block, round = a.pool.block() - 1;
   const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
@@ -90,8 +91,10 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
       }
       auto page = [&](uint32_t c) {  // of column c
         const uint32_t at = max(c << log, ctx) - ctx;
-        const uint32_t slot = at < count ? (uint32_t)a.slots[first + at] : ~0u;
-        return a.pool.holds(slot) ? slot >> log : ~0u;
+        if (at >= count) return ~0u;
+        const uint32_t slot = (uint32_t)a.slots[first + at];
+        const uint32_t id = a.pool.holds(slot) ? slot >> log : (uint32_t)a.table[(uint64_t)b * a.width + c];
+        return id < a.pool.blocks ? id : ~0u;
       };
       uint32_t mine = 0;
       for (uint32_t c = from; c < to; ++c) mine += page(c) != ~0u;

@@ -455,7 +455,8 @@ int dgt_verify(uint32_t type, const void* d_logits, uint64_t logits_row, const i
 /* After a step: of request b the first d_kept[b] rows of its path are kept (cut to its new
  * tokens).  Their keys and values move to the places of its first new tokens, in all
  * layers; its length becomes ctx[b] + kept; pages past that length go back to the list,
- * request by request, and their columns of the table become -1.
+ * request by request, and their columns of the table become -1 (those too whose tokens the
+ * plan gave no slot: they are looked up in the table, as the plan left it).
  *   d_path: int32[tokens] as dgt_verify writes it: row cu[b] + j holds the index, within
  *          the request, of the j-th kept row; or NULL: the first rows are kept.  The
  *          indexes rise; where one is out of range, or below j, the j-th place is left as it is.

@@ -210,8 +210,9 @@ def page_keep(path, kept, ctx, cu, slots, free, head, table, block, blocks):
             continue
         for col in range(-(-(c + k) // block), min(-(-(c + n) // block), table.shape[1])):
             slot = int(slots[start + max(col * block, c) - c])
-            if valid(slot):
-                gone.append(slot // block)
+            page = slot // block if valid(slot) else int(table[b, col])  # (the plan wrote it there)
+            if 0 <= page < blocks:
+                gone.append(page)
                 table[b, col] = -1
     free[head - len(gone):head] = gone
     return moves, np.array(lens), free, table, np.array([head - len(gone), len(gone)])

@@ -294,3 +294,32 @@ def test_empty_calls():
     assert dgt.dgt_page_keep(none, none, _i32([0]), none, free, head, table, k, v).tolist() == [1, 0]
     assert dgt.dgt_page_fork(none, none, none, free, head, table, shares, k, v).tolist() == [1, 0]
     assert dgt.dgt_page_free(none, none, free, head, table, shares, 8).tolist() == [1, 0]
+
+
+@pytest.mark.parametrize("many", [1, 70])
+@pytest.mark.parametrize("kept", [[1, 1, 1, 1], [40, 11, 1, 20], [64, 1, 0, 0]])
+def test_keep_returns_pages_of_tokens_without_a_slot(kept, many):
+    """The plan takes pages for every node, also for one past the mask or behind a bad link, which gets no
+    slot: after the keep each page is held or free.  (70 steps' requests in one: more than one round.)"""
+    import torch
+    from tests.test_oracle_step import held_or_free, odd_step
+    d = odd_step()
+    shift = lambda x: np.concatenate([np.where(np.asarray(x) >= 0, np.asarray(x) + i * d["blocks"], -1)
+                                      for i in range(many)])
+    ctx, new, parents = np.tile(d["ctx"], many), np.tile(d["new"], many), np.tile(d["parents"], many)
+    table = shift(np.where(np.arange(9) < -(-d["ctx"][:, None] // 16), d["table"], -1))
+    # pages of the list in the order in which the requests take them
+    first = np.concatenate([d["free"][:d["first"]] + i * d["blocks"] for i in range(many)])
+    free = np.concatenate([first] + [d["free"][d["first"]:d["head"]] + i * d["blocks"] for i in range(many)]
+                          + [d["free"][d["head"]:] + i * d["blocks"] for i in range(many)])
+    k, v = _caches(5, None, many * d["blocks"], 1, 16, 8)
+    lens, ids, t = _i32(ctx), _i32(free), _i32(table)
+    plan = dgt.dgt_page_plan(lens, _i32(new), ids, _i32([len(first)]), t, 16, many * d["blocks"], int(new.sum()),
+                             parents=_i32(parents))
+    assert plan.counts.tolist() == [int(new.sum()), many * d["head"], 0]
+    assert np.array_equal(t.cpu().numpy(), shift(d["table"]))
+    kd, vd = k.cuda(), v.cuda()
+    counts = dgt.dgt_page_keep(_i32(kept * many), lens, plan.cu, plan.slots, ids, plan.counts[1:2], t, kd, vd)
+    assert lens.tolist() == (ctx + np.array(kept * many)).tolist()
+    held_or_free(dict(d, blocks=many * d["blocks"]), t.tolist(), lens.tolist(), ids.tolist(), int(counts[0]))
+    assert torch.equal(_bits(kd), _bits(k)) and torch.equal(_bits(vd), _bits(v))

@@ -97,3 +97,49 @@ def test_fork_and_free_by_hand():
     assert shares.sum() == 0 and t.tolist() == [[-1] * 3, [4, 2, -1], [-1] * 3]
     _, free, t, _, counts = serving.page_free([1], lens, free, 3, t, shares, 8, 10)
     assert counts.tolist() == [1, 2] and free.tolist() == [9, 2, 4, 3, 7]
+
+
+def _odd_trees():
+    """Trees of the page plan whose nodes do not all get a slot: 100 nodes in one mask word, a bad link at a
+    page's start and inside one, one whose nodes past the first all hang off a bad link; and a plain one."""
+    chain = [-1] + list(range(99))
+    bent = [-1] + list(range(39))
+    bent[11], bent[27] = 11, -7  # node 11 lies first in a page of 16 behind 5 cached tokens
+    cut = [-1, 1] + list(range(1, 29))
+    new, ctx = [100, 40, 30, 20], [0, 5, 16, 9]
+    return ctx, new, np.array(chain + bent + cut + [-1] + list(range(19)))
+
+
+def odd_step(block=16, spare=3):
+    """A step of such trees, planned by the oracle: what the plan left, and each request's tokens with a slot."""
+    ctx, new, parents = _odd_trees()
+    have = [-(-c // block) for c in ctx]
+    pages = sum(-(-(c + n) // block) for c, n in zip(ctx, new))
+    blocks = pages + spare
+    ids = np.random.default_rng(3).permutation(blocks)
+    table, at = np.full((4, 9), -1), 0
+    for b, h in enumerate(have):
+        table[b, :h] = ids[at:at + h]
+        at += h
+    table, cu, slots, _, _, counts = serving.page_plan(ctx, new, ids, at, table, block, blocks, sum(new), parents, 1)
+    assert counts.tolist() == [sum(new), pages, 0]
+    return dict(ctx=np.array(ctx), new=np.array(new), parents=parents, cu=cu, table=table, slots=slots, free=ids,
+                first=at, head=int(counts[1]), blocks=blocks, block=block)
+
+
+def held_or_free(d, table, lens, free, head):
+    """Every page is in one request's columns up to its length, or in the list; no column past a length is set."""
+    held = [int(p) for row, n in zip(table, lens) for p in row[:-(-int(n) // d["block"])]]
+    past = [int(p) for row, n in zip(table, lens) for p in row[-(-int(n) // d["block"]):]]
+    assert set(past) <= {-1}
+    assert sorted(held + [int(p) for p in free[head:]]) == list(range(d["blocks"]))
+
+
+def test_keep_returns_pages_of_tokens_without_a_slot():
+    d = odd_step()
+    assert (d["slots"][64:100] == -1).all() and d["slots"][111] == -1
+    for kept in ([1, 1, 1, 1], [40, 11, 1, 20], [64, 1, 0, 0]):
+        moves, lens, free, table, counts = serving.page_keep(
+            None, kept, d["ctx"], d["cu"], d["slots"], d["free"], d["head"], d["table"], d["block"], d["blocks"])
+        assert lens.tolist() == (d["ctx"] + kept).tolist() and moves == []
+        held_or_free(d, table, lens, free, int(counts[0]))
