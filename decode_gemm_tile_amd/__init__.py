@@ -1057,7 +1057,7 @@ def dgt_page_keep(kept, ctx_lens, cu, slots, free_blocks, free_head, block_table
     (dgt_verify; None: of its new rows) stay.  Their keys and values move behind the cached tokens, in
     all layers of k_cache and v_cache ([layers, blocks, ...], or one layer's [blocks, ...]); `lens`
     (default: ctx_lens, in place) gets the new lengths; pages past them go back into free_blocks, in
-    front of its head.  Returns counts int32[2]: the list's new head, the pages that went back."""
+    front of its head.  A path is cut at its first row without a slot, which was never stored.  Returns counts int32[2]: the list's new head, the pages that went back."""
     out = ctx_lens if lens is None else lens
     try:
         dev = k_cache.device

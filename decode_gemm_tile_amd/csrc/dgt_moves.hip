@@ -66,11 +66,89 @@ __device__ __forceinline__ uint32_t kept_of(const KeepArgs& a, uint32_t b, uint3
   return *held ? min((uint32_t)max(kept, 0), count) : 0u;
 }
 
+// The kept rows that stay, of a request a thread (kept: how many at most, its rows are `count`
+// from `first` on).  Row j of a path stays if its own place has a slot, and so has the row that
+// moves there: a token that the plan gave no slot was never stored.  Of the first it and all
+// behind it go.  16 lanes look at the first 16 rows of a request side by side; what longer ones
+// have besides goes round the waves.
+struct Kept {
+  uint32_t first, count, rows;
+};
+__device__ __forceinline__ uint32_t rows_that_stay(const KeepArgs& a, uint32_t first, uint32_t count, uint32_t kept,
+                                                   uint32_t left, Kept* s_kept) {
+  const uint32_t t = threadIdx.x, lane = t & 63, n = t % 16;
+  if (a.tokens == 0) return 0;
+  // Four rows a thread at a time, their loads beside one another (row 0's where there is none).
+  auto look = [&](const Kept (&it)[4], const uint32_t (&j)[4], bool (&gone)[4]) {
+    uint32_t place[4], from[4], slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = j[i] < it[i].rows ? it[i].first + j[i] : 0;
+      place[i] = (uint32_t)a.slots[at];
+      from[i] = a.path ? (uint32_t)a.path[at] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool moves = j[i] < it[i].rows && from[i] > j[i] && from[i] < it[i].count;
+      slot[i] = (uint32_t)a.slots[moves ? it[i].first + from[i] : 0];
+      if (!moves) slot[i] = place[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gone[i] = j[i] < it[i].rows && !(a.pool.holds(place[i]) && a.pool.holds(slot[i]));
+  };
+  s_kept[t] = Kept{first, count, kept};
+  __syncthreads();
+  for (uint32_t x0 = t / 16; x0 - t / 16 < min(left, 256u); x0 += 64) {
+    Kept it[4];
+    uint32_t j[4];
+    bool gone[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      it[i] = s_kept[x0 + 16 * i];
+      j[i] = n;
+    }
+    look(it, j, gone);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t all = __ballot(gone[i]) >> (lane & 48) & 0xFFFFu;
+      if (n == 0 && all) s_kept[x0 + 16 * i].rows = (uint32_t)__builtin_ctzll(all);
+    }
+  }
+  __syncthreads();
+  if (__syncthreads_or(s_kept[t].rows > 16)) {
+    const uint32_t wave = t >> 6;
+    for (uint64_t todo = __ballot(s_kept[4 * lane + wave].rows > 16); todo; todo &= todo - 1) {
+      const uint32_t x = 4 * (uint32_t)__builtin_ctzll(todo) + wave;
+      const Kept one = s_kept[x];
+      uint32_t least = one.rows;
+      for (uint32_t j0 = 16; j0 < least; j0 += 256) {
+        Kept it[4];
+        uint32_t j[4];
+        bool gone[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          it[i] = one;
+          j[i] = j0 + 64 * i + lane;
+        }
+        look(it, j, gone);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (gone[i]) least = min(least, j[i]);
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) least = min(least, (uint32_t)__shfl_xor((int)least, m, 64));
+      }
+      if (lane == 0) s_kept[x].rows = least;
+    }
+    __syncthreads();
+  }
+  return s_kept[t].rows;  // (the next round's write is of the same thread)
+}
+
 // Lengths, and the pages past them, by one workgroup: the list's order is the requests'.
 // A column past the kept tokens begins at or behind the cached ones' end, so a new token
 // lies first in it and its slot names the page.  One that the plan gave no slot (a bad link,
 // an index past the mask) has taken its page all the same: then the table names it.
-__device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
+__device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum, Kept* s_kept) {
   const uint32_t log = a.pool.log_block, round = a.pool.block() - 1;
   const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
   uint32_t total = 0;
@@ -79,12 +157,15 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
     uint32_t done = 0;
     for (uint32_t b0 = 0; b0 < a.requests; b0 += 256) {
       const uint32_t b = b0 + threadIdx.x;
-      uint32_t first = 0, count = 0, ctx = 0, now = 0, from = 0, to = 0;
+      uint32_t first = 0, count = 0, ctx = 0, kept = 0, now = 0, from = 0, to = 0;
+      bool held = false;
       if (b < a.requests) {
         request_rows(a.cu, b, a.tokens, &first, &count);
         ctx = (uint32_t)max(a.ctx[b], 0);
-        bool held;
-        const uint32_t kept = kept_of(a, b, first, count, &held);
+        kept = kept_of(a, b, first, count, &held);
+      }
+      kept = rows_that_stay(a, first, count, kept, a.requests - b0, s_kept);
+      if (b < a.requests) {
         now = (uint32_t)min((uint64_t)ctx + kept, (uint64_t)0x7FFFFFFF);
         from = min((uint32_t)(((uint64_t)now + round) >> log), a.width);
         to = held ? min((uint32_t)(((uint64_t)ctx + count + round) >> log), a.width) : from;
@@ -125,7 +206,8 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum) {
 // time: all of them are read before any is written.  Index i_j >= j rises with j, so a
 // row that a later step reads lies behind every place that this one writes.  Slots are
 // looked up in the plan's list and not in the table, whose columns change at the same time.
-__device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint32_t* s_src, uint32_t* s_dst) {
+// s_end: of two steps in turn, the first row that does not stay.
+__device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint32_t* s_src, uint32_t* s_dst, uint32_t* s_end) {
   const uint32_t t = threadIdx.x, dim = a.pool.dim, log = a.pool.log_block, in_page = a.pool.block() - 1;
   const uint32_t b = unit / a.parts, part = unit - b * a.parts;
   const uint32_t lh0 = part * a.each, lh1 = min(lh0 + a.each, a.pool.layers * a.pool.heads);
@@ -134,21 +216,33 @@ __device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint
   int32_t ahead = t < min(count, kKeepRows) ? a.path[first + t] : 0;
   bool held;
   const uint32_t kept = kept_of(a, b, first, count, &held);
-  for (uint32_t j0 = 0; j0 < kept; j0 += kKeepRows) {
+  bool ends = false;
+  for (uint32_t j0 = 0; j0 < kept && !ends; j0 += kKeepRows) {
     const uint32_t rows = min(kept - j0, kKeepRows);
+    uint32_t* end = s_end + j0 / kKeepRows % 2;
     bool moves = false;
-    if (t < rows) {
-      const uint32_t j = j0 + t, i = (uint32_t)(j0 ? a.path[first + j] : ahead);
+    if (t < 64) {
       uint32_t src = ~0u, dst = ~0u;
-      if (i > j && i < count) {
-        src = (uint32_t)a.slots[first + i];
+      bool stay = true;
+      if (t < rows) {
+        const uint32_t j = j0 + t, i = (uint32_t)(j0 ? a.path[first + j] : ahead);
+        moves = i > j && i < count;
         dst = (uint32_t)a.slots[first + j];
+        if (moves) src = (uint32_t)a.slots[first + i];
+        stay = a.pool.holds(dst) && (!moves || a.pool.holds(src));
       }
-      moves = a.pool.holds(src) && a.pool.holds(dst);
-      s_src[t] = moves ? src : ~0u;
-      s_dst[t] = dst;
+      const uint64_t gone = __ballot(!stay);
+      const uint32_t least = gone ? (uint32_t)__builtin_ctzll(gone) : rows;
+      moves = moves && t < least;
+      if (t < rows) {
+        s_src[t] = moves ? src : ~0u;
+        s_dst[t] = dst;
+      }
+      if (t == 0) *end = least;
     }
-    if (!__syncthreads_or(moves)) continue;
+    const bool any = __syncthreads_or(moves);
+    ends = *end < rows;
+    if (!any) continue;
     const uint32_t vr = t % kKeepRows, v_src = vr < rows ? s_src[vr] : ~0u, v_dst = v_src != ~0u ? s_dst[vr] : 0;
     for (uint32_t lh = lh0; lh < lh1; ++lh) {
       const uint32_t layer = lh / a.pool.heads, head = lh - layer * a.pool.heads;
@@ -182,10 +276,12 @@ __device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint
   }
 }
 
-__global__ __launch_bounds__(256) void k_page_keep(KeepArgs a) {
-  __shared__ uint32_t s_sum[4], s_src[kKeepRows], s_dst[kKeepRows];
-  if (blockIdx.x == 0) keep_pages(a, s_sum);
-  else keep_rows(a, blockIdx.x - 1, s_src, s_dst);
+// (eight workgroups a CU, 64 registers: with 123 registers and four of them the trees take 20.6 us)
+__global__ __launch_bounds__(256, 8) void k_page_keep(KeepArgs a) {
+  __shared__ uint32_t s_sum[4], s_src[kKeepRows], s_dst[kKeepRows], s_end[2];
+  __shared__ Kept s_kept[256];
+  if (blockIdx.x == 0) keep_pages(a, s_sum, s_kept);
+  else keep_rows(a, blockIdx.x - 1, s_src, s_dst, s_end);
 }
 
 // ----------------------------------------------------------------------- fork

@@ -460,6 +460,9 @@ int dgt_verify(uint32_t type, const void* d_logits, uint64_t logits_row, const i
  *   d_path: int32[tokens] as dgt_verify writes it: row cu[b] + j holds the index, within
  *          the request, of the j-th kept row; or NULL: the first rows are kept.  The
  *          indexes rise; where one is out of range, or below j, the j-th place is left as it is.
+ *          A row without a slot (dgt_page_plan gives none to a node past the mask or behind a
+ *          bad link) was never stored: it is not kept, nor is what follows it or a place
+ *          without a slot on the path, and the length does not count them.
  *   d_slots: int32[tokens], the step's slots (dgt_page_plan).  A request whose first new
  *          token has no slot (the plan refused it) keeps nothing and returns nothing.
  *   d_lens: int32[requests], the new lengths; may be d_ctx.

@@ -200,11 +200,15 @@ def page_keep(path, kept, ctx, cu, slots, free, head, table, block, blocks):
     for b in range(len(kept)):
         start, n, c = int(cu[b]), int(cu[b + 1] - cu[b]), max(int(ctx[b]), 0)
         refused = n == 0 or not valid(slots[start])
-        k = 0 if refused else min(max(int(kept[b]), 0), n)
-        for j in range(k if path is not None else 0):
-            i = int(path[start + j])
-            if j < i < n and valid(slots[start + i]) and valid(slots[start + j]):
-                moves.append((int(slots[start + i]), int(slots[start + j])))
+        k = 0
+        while not refused and k < min(int(kept[b]), n):
+            i = int(path[start + k]) if path is not None else k
+            i = i if k < i < n else k  # (any other index leaves the place as it is)
+            if not (valid(slots[start + i]) and valid(slots[start + k])):
+                break  # never stored
+            if i > k:
+                moves.append((int(slots[start + i]), int(slots[start + k])))
+            k += 1
         lens.append(c + k)
         if refused:
             continue

@@ -323,3 +323,32 @@ def test_keep_returns_pages_of_tokens_without_a_slot(kept, many):
     assert lens.tolist() == (ctx + np.array(kept * many)).tolist()
     held_or_free(dict(d, blocks=many * d["blocks"]), t.tolist(), lens.tolist(), ids.tolist(), int(counts[0]))
     assert torch.equal(_bits(kd), _bits(k)) and torch.equal(_bits(vd), _bits(v))
+
+
+def test_keep_ends_a_path_at_a_row_without_a_slot():
+    """Rows past the mask, behind a bad link, and places without a slot; in the first 16 rows of a path, behind
+    them, and far behind, with requests before and after that keep all."""
+    from tests.test_oracle_step import odd_step
+    d = odd_step()
+    path = np.full(190, -1)
+    path[:4], path[100:104], path[140:142], path[170:173] = [0, 60, 63, 64], [0, 5, 11, 12], [0, 1], [0, 3, 4]
+    for in_place in (True, False):
+        _keep(d, path, [4, 4, 2, 3], 2, 2, 40, in_place=in_place)
+        _keep(d, None, [100, 40, 30, 20], 2, 2, 40, in_place=in_place)
+        _keep(d, np.concatenate([np.arange(n) for n in d["new"]]), [100, 40, 30, 20], 1, 1, 8, in_place=in_place)
+    rng = np.random.default_rng(8)
+    new = [3000, 20, 0, 700, 40, 1, 2000] + [12] * 300
+    d = _step(23, rng.integers(0, 50, len(new)), new, 16)
+    start = np.concatenate([[0], np.cumsum(new)])
+    for b, row in ((0, 2900), (1, 17), (3, 15), (4, 16), (6, 1999), (8, 3), (200, 11)):
+        d["slots"][start[b] + row] = -1
+    kept = np.array(new) - rng.integers(0, 2, len(new))
+    _keep(d, None, kept, None, 1, 8)
+    # upward paths that leave out a row in three
+    path = np.full(sum(new), -1)
+    for b, n in enumerate(new):
+        way = np.array([i for i in range(n) if i % 3 != 1])
+        path[start[b]:start[b] + len(way)] = way
+        kept[b] = len(way)
+    _keep(d, path, kept, 2, 1, 8)
+    _keep(d, path, kept, None, 1, 24, "float16", in_place=False)

@@ -143,3 +143,22 @@ def test_keep_returns_pages_of_tokens_without_a_slot():
             None, kept, d["ctx"], d["cu"], d["slots"], d["free"], d["head"], d["table"], d["block"], d["blocks"])
         assert lens.tolist() == (d["ctx"] + kept).tolist() and moves == []
         held_or_free(d, table, lens, free, int(counts[0]))
+
+
+def test_keep_ends_a_path_at_a_row_without_a_slot():
+    """What was never stored is not counted: a node past the mask, one behind a bad link, a place on the path
+    that has no slot."""
+    d = odd_step()
+    keep = lambda path, kept: serving.page_keep(path, kept, d["ctx"], d["cu"], d["slots"], d["free"], d["head"],
+                                                d["table"], d["block"], d["blocks"])
+    _, lens, free, table, counts = keep(None, [100, 40, 30, 20])
+    assert lens.tolist() == [64, 5 + 11, 16 + 1, 9 + 20]
+    held_or_free(d, table, lens, free, int(counts[0]))
+    # request 0: rows 0, 60, 63, 64; request 1: rows 0, 5, 11 (no slot); request 3: rows 0, 3, 4
+    path = np.full(190, -1)
+    path[:4], path[100:104], path[140:142], path[170:173] = [0, 60, 63, 64], [0, 5, 11, 12], [0, 1], [0, 3, 4]
+    moves, lens, free, table, counts = keep(path, [4, 4, 2, 3])
+    s = d["slots"]
+    assert lens.tolist() == [3, 5 + 2, 16 + 1, 9 + 3]
+    assert moves == [(s[60], s[1]), (s[63], s[2]), (s[105], s[101]), (s[173], s[171]), (s[174], s[172])]
+    held_or_free(d, table, lens, free, int(counts[0]))
