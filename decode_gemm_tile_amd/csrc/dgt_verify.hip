@@ -8,8 +8,9 @@ namespace serve {
 namespace {
 
 // A request's path starts at row 0 and goes down its tree or chain; an end's largest logit
-// and sum of exponentials decide about the drafted tokens that follow it (the sum is fp32:
-// a draft whose number lies within 2^-20 or so of the border may fall either way).  A
+// and sum of exponentials decide about the drafted tokens that follow it.  The sum is formed
+// in fp32; where a draft's number lies nearer to its border than that can tell, about once in
+// 50000 drafts, the wave that decides forms it again in fp64 (see kNear).  A
 // workgroup looks at one segment of one row.  The last to come for a row that is the path's
 // end decides, and goes on if the row after it is complete too; else whoever completes
 // that one does.  Nobody waits.  Rows come in the order of their index within the request,
@@ -220,6 +221,32 @@ __device__ __forceinline__ void add_elements(RowSum& r, const float (&x)[N], F p
   r.join(sum, top, at, odd, c);
 }
 
+// How far the fp32 sum may be off, relative to it.  A weight is e^-y, y >= 0.  On its way into the
+// sum it is multiplied by powers whose arguments add up to -y, each off by 3 * 2^-24 of itself (the
+// difference, 1 / T, their product), at most 33 of them, each off by 2^-23; and 48 additions, 2^-24
+// each, follow.  The weighted mean of y is at most ln(vocabulary) < 15.3 (the weights sum to at least
+// 1).  Together less than (46 + 66 + 48) * 2^-24 < 2^-16.
+constexpr double kNear = 1.0 / 65536;
+
+// A row's sum in fp64, by the wave.
+template <class L>
+__device__ __forceinline__ double whole_sum(const VerifyArgs& a, uint64_t row, float top, double c) {
+  double sum = 0.0;
+  for (uint32_t v0 = threadIdx.x & 63; v0 < a.vocab; v0 += 256) {
+    float x[4];
+    double z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = v0 + 64 * i < a.vocab ? L::one(a.logits, row * a.logits_row + v0 + 64 * i) : -INFINITY;
+      z[i] = ((double)x[i] - (double)top) * c;
+    }
+    exp2_64<4>(z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += x[i] > -INFINITY ? z[i] : 0.0;
+  }
+  return wave_sum(sum);
+}
+
 // Before all: rows in the order of their index within the request, no counts, paths of row
 // 0 alone.  Offsets that fall have no such order; their rows come as they are.
 __global__ __launch_bounds__(kThreads) void k_verify_begin(VerifyArgs a) {
@@ -297,7 +324,9 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, uint32_t b, uint32_t
     row.across_wave(c);
     uint32_t go = 0;
     bool lost = false;  // a child of the end was refused
-    double left = row.sum;  // of the row's sum, without the refused tokens
+    // (the lanes' own fp32 sums differ in their last bits, as the terms come in another order)
+    double total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(row.sum))), left = total;
+    double near = c64 < 3e38 ? total * kNear : INFINITY;  // left: without the refused tokens
     // children in the order of their rows, 64 candidates at a time
     for (uint32_t j0 = end + 1; j0 < last && !go && row.sound(); j0 += 64) {
       if (j0 != end + 1) todo = candidate(j0 + lane);
@@ -314,7 +343,13 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, uint32_t b, uint32_t
           if (a.parents && lost && token < a.vocab)
             for (uint32_t i = end + 1 + lane; i < node; i += 64) before |= is_child(i) && (uint32_t)a.draft[first + i] == token;
           if (token < a.vocab && !__any(before)) {
-            taken = draw * (a.probs ? (double)row.sum : left) < weight;
+            if (fabs(draw * (a.probs ? total : left) - weight) < draw * near) {
+              const double sum = whole_sum<L>(a, at, row.top, c64);
+              left += sum - total;
+              total = sum;
+              near = -1.0;
+            }
+            taken = draw * (a.probs ? total : left) < weight;
             if (!taken) left -= weight;
           }
         } else {

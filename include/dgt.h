@@ -422,7 +422,8 @@ int dgt_chunk_attention(uint32_t type, const void* d_q, uint64_t q_row, uint64_t
  * T = d_temperature[b] (NULL: 1); T <= 0 (or not a number): a child is accepted if its
  * token is the row's largest logit's (the first of equals), and so is the next token.  With
  * T = +inf all tokens that are not excluded weigh the same.
- * Sums over a vocabulary are fp64, and so are the exponentials in them.
+ * Decisions are those of fp64 sums over the vocabulary (of exponentials off by 2^-39): fp32
+ * sums are only trusted where a draft's number lies further from its border than they can be off.
  *   d_logits: [tokens, vocab] of type `type` (F32, BF16, F16), row stride in elements;
  *          -inf excludes a token.  A row with a NaN or +inf, or of -inf alone, ends the
  *          path, and the next token is -1.

@@ -293,3 +293,73 @@ def test_an_infinite_temperature(kind):
               temperature=[float("inf"), 3.4e38] * 6)
     _check(d, _run(d))
     assert len(set(_run(d).next.tolist())) > 6  # not one most likely token after the other
+
+
+def _beside(border, above):
+    """float32 numbers next to their borders (in 64 bits), above or below, at least 2^-26 of the border and at
+    most three of its last places away."""
+    u = np.float32(border)
+    for i, (b, up) in enumerate(zip(border, above)):
+        while (float(u[i]) - b) * (1 if up else -1) < b * 2.0 ** -26:
+            u[i] = np.nextafter(u[i], np.float32(2 if up else -1))
+    far = np.abs(u.astype(float) - border) / border
+    assert far.min() >= 2.0 ** -26 and far.max() <= 3 * 2.0 ** -23 and u.max() < 1
+    return u
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("kind", ["chain", "probs", "tree"])
+@pytest.mark.parametrize("vocab", [300, 5000, 50001, 130000])
+def test_numbers_next_to_their_borders(vocab, kind, dtype):
+    """A draft's number one last place from the border falls on the border's right side: sums over a vocabulary
+    are 64-bit.  (Their weights are off by 2^-39, the numbers by 2^-26 at least.)"""
+    n = 40 if vocab < 100000 else 16
+    d = _make(30, [2] * n, vocab, probs=kind == "probs", dtype=dtype, temperature=np.linspace(0.5, 1.5, n))
+    rng = np.random.default_rng(31)
+    above = rng.random(n) < 0.5
+    z = d["logits"].double().numpy()[::2] / d["heat"].astype(float)[:, None]
+    p = np.exp(z - z.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    best = np.argsort(p, 1)[np.arange(n), -1 - rng.integers(1, 5, n)]
+    d["draft"][1::2] = best
+    border = p[np.arange(n), best]
+    if kind == "probs":
+        d["probs"][::2][np.arange(n), best] = q = np.float32(border * (1.1 + rng.random(n)))
+        border = border / q.astype(float)
+    if kind == "tree":
+        d["parents"] = np.tile([-1, 0], n)
+    d["accept"][1::2] = _beside(border, above)
+    lengths = _check(d, _run(d))
+    assert lengths == (2 - above).tolist()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("levels", [1, 2, 4, 6])
+def test_numbers_next_to_their_borders_behind_refused_siblings(levels, dtype):
+    """What siblings leave of the mass, down to a millionth of it, keeps its bits: each takes about nine tenths of
+    what is left, and the last one's number lies next to the border."""
+    n, vocab = 30, 20000
+    import torch
+    rng = np.random.default_rng(33)
+    new = levels + 2
+    logits = rng.normal(size=(n * new, vocab)) * 2
+    ids = np.stack([rng.permutation(vocab)[:levels + 1] for _ in range(n)])
+    total = np.log(np.exp(logits[::new]).sum(1))
+    for i in range(levels + 1):
+        logits[np.arange(n) * new, ids[:, i]] = total + (levels - i) * np.log(10) + np.log(9)
+    logits = torch.from_numpy(logits).to(getattr(torch, dtype))
+    z = logits.double().numpy()[::new]
+    p = np.exp(z - z.max(1, keepdims=True))
+    border = np.zeros((n, levels + 1))
+    for i in range(levels + 1):
+        border[:, i] = p[np.arange(n), ids[:, i]] / p.sum(1)
+        p[np.arange(n), ids[:, i]] = 0
+    above = rng.random(n) < 0.5
+    accept = np.full((n, new), 0.99, np.float32)
+    assert border.max() < 0.98
+    accept[:, -1] = _beside(border[:, -1], above)
+    d = dict(logits=logits, draft=np.concatenate([np.zeros((n, 1), int), ids], 1).reshape(-1), new=[new] * n,
+             cu=np.arange(n + 1) * new, parents=np.tile([-1] + [0] * (levels + 1), n), probs=None, heat=None,
+             accept=accept.reshape(-1), sample=rng.random(n).astype(np.float32))
+    lengths = _check(d, _run(d))
+    assert lengths == (2 - above).tolist()
