@@ -110,12 +110,17 @@ __device__ __forceinline__ double exp2_64(double z) {
 
 constexpr double kLog2e = 1.44269504088896340736;
 // What logits are multiplied by: 1 / T in powers of two, or 0 for the largest logit's token.  (Of an
-// infinite T a little is left, less than of any finite one: all tokens weigh the same.)
+// infinite T so little is left that all tokens weigh the same, whatever their logits.)
 __device__ __forceinline__ double heat(const VerifyArgs& a, uint32_t b) {
   const float t = a.temperature ? a.temperature[b] : 1.f;
-  return t > 0.f ? fmax(kLog2e / (double)t, 4e-39) : 0.0;
+  return !(t > 0.f) ? 0.0 : t < INFINITY ? kLog2e / (double)t : 1e-60;
 }
-__device__ __forceinline__ float heat32(double c) { return (float)fmin(c, 3e38); }
+// Twice that in fp32, where halves of logits are taken from each other: a mask of the type's lowest
+// value and a large logit lie further apart than fp32 reaches.
+__device__ __forceinline__ float heat32(double c) { return c > 0.0 ? fmaxf((float)fmin(2.0 * c, 3e38), 1.4e-45f) : 0.f; }
+__device__ __forceinline__ float weight32(float x, float top, float c) {
+  return __builtin_amdgcn_exp2f(fmaf(x, 0.5f, -0.5f * top) * c);
+}
 
 template <class E>
 struct Logit {
@@ -187,7 +192,7 @@ struct RowSum {
   __device__ __forceinline__ void join(float osum, float otop, uint32_t oat, bool oodd, float c) {
     const float now = fmaxf(top, otop);
     if (now > -INFINITY)
-      sum = sum * __builtin_amdgcn_exp2f((top - now) * c) + osum * __builtin_amdgcn_exp2f((otop - now) * c);
+      sum = sum * weight32(top, now, c) + osum * weight32(otop, now, c);
     better(top, at, otop, oat);
     odd |= oodd;
   }
@@ -217,7 +222,7 @@ __device__ __forceinline__ void add_elements(RowSum& r, const float (&x)[N], F p
   float sum = 0.f;
   if (c > 0.f && top > -INFINITY)
 #pragma unroll
-    for (int e = 0; e < N; ++e) sum += __builtin_amdgcn_exp2f((x[e] - top) * c);
+    for (int e = 0; e < N; ++e) sum += weight32(x[e], top, c);
   r.join(sum, top, at, odd, c);
 }
 
@@ -326,7 +331,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, uint32_t b, uint32_t
     bool lost = false;  // a child of the end was refused
     // (the lanes' own fp32 sums differ in their last bits, as the terms come in another order)
     double total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(row.sum))), left = total;
-    double near = c64 < 3e38 ? total * kNear : INFINITY;  // left: without the refused tokens
+    double near = c64 < 1.5e38 ? total * kNear : INFINITY;  // left: without the refused tokens
     // children in the order of their rows, 64 candidates at a time
     for (uint32_t j0 = end + 1; j0 < last && !go && row.sound(); j0 += 64) {
       if (j0 != end + 1) todo = candidate(j0 + lane);

@@ -167,7 +167,9 @@ def verify(logits, draft, accept, sample, parents=None, probs=None, temperature=
                 return path, token
             path.append(go)
             continue
-        p = softmax(row / np.float64(temperature))
+        z = np.full(len(row), -np.inf)  # (-inf excludes a token at an infinite temperature too)
+        z[row > -np.inf] = row[row > -np.inf] / np.float64(temperature)
+        p = softmax(z)
         q = None
         if probs is not None:
             q = np.where(probs[end] > 0, probs[end].astype(np.float64), 0.0)

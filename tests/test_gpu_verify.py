@@ -363,3 +363,27 @@ def test_numbers_next_to_their_borders_behind_refused_siblings(levels, dtype):
              accept=accept.reshape(-1), sample=rng.random(n).astype(np.float32))
     lengths = _check(d, _run(d))
     assert lengths == (2 - above).tolist()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("kind", ["chain", "tree", "probs"])
+def test_masks_of_the_lowest_value(kind, dtype):
+    """A mask of the type's lowest value excludes a token at an ordinary temperature; at an infinite one, which
+    makes all tokens but those of -inf weigh the same, it does not; at a very large one it weighs what the
+    formula says, also beside a logit as large, whose distance fp32 does not hold."""
+    import torch
+    low = float(torch.finfo(getattr(torch, dtype)).min)
+    n, vocab = 24, 900
+    for large, heats in ((False, [1.0, 1e-3]), (False, [float("inf")]), (False, [3.4e38, 1e38]),
+                         (True, [float("inf"), 3.4e38, 1e38, 3e37])):
+        d = _make(40, [3] * n, vocab, tree=int(kind == "tree"), probs=kind == "probs", dtype=dtype,
+                  temperature=np.resize(heats, n))
+        d["logits"][:, 5:600] = low
+        d["logits"][:, 600:640] = float("-inf")
+        if large:
+            d["logits"][:, 640:700] = -low
+        drafted = np.random.default_rng(41).integers(0, 700, 3 * n)
+        d["draft"] = drafted
+        if kind == "probs":
+            d["probs"][:] = 1.0 / vocab
+        _check(d, _run(d))

@@ -162,3 +162,10 @@ def test_keep_ends_a_path_at_a_row_without_a_slot():
     assert lens.tolist() == [3, 5 + 2, 16 + 1, 9 + 3]
     assert moves == [(s[60], s[1]), (s[63], s[2]), (s[105], s[101]), (s[173], s[171]), (s[174], s[172])]
     held_or_free(d, table, lens, free, int(counts[0]))
+
+
+def test_verify_at_an_infinite_temperature():
+    """All tokens weigh the same but those of -inf."""
+    row = np.array([[-np.inf, 3.0, -3.4e38, 7.0, -np.inf]])
+    got = [serving.verify(row, [0], [0.0], s, temperature=np.inf) for s in (0.0, 0.33, 0.34, 0.66, 0.67)]
+    assert got == [([0], 1), ([0], 1), ([0], 2), ([0], 2), ([0], 3)]
