@@ -9,9 +9,9 @@ namespace {
 
 // A request's path starts at row 0 and goes down its tree or chain; an end's largest logit
 // and sum of exponentials decide about the drafted tokens that follow it.  The sum is formed
-// in fp32; where a draft's number lies nearer to its border than that can tell, about once in
-// 50000 drafts, the wave that decides forms it again in fp64 (see kNear).  A
-// workgroup looks at one segment of one row.  The last to come for a row that is the path's
+// in fp32; where a draft's number lies nearer to its border than that can tell (kNear), about once
+// in 50000 drafts, the path waits there for the launch of the last rows, which goes on with fp64
+// sums.  A workgroup looks at one segment of one row.  The last to come for a row that is the path's
 // end decides, and goes on if the row after it is complete too; else whoever completes
 // that one does.  Nobody waits.  Rows come in the order of their index within the request,
 // so a row's turn is mostly after the decisions above it, and one that the path has
@@ -40,7 +40,7 @@ struct VerifyArgs {
   struct State* states;     // [requests]
   double* sums;             // [requests][segs]: of a last row's weights, then of max(p - q, 0)
   double* rest;
-  struct End* ends;         // [requests]
+  struct End* ends;         // [2][requests]: of the paths; of those that were left open, once they are not
   uint64_t logits_row, probs_row;
   uint32_t requests, tokens, vocab, segs;
   bool wide, probs_wide;    // rows are 16-byte aligned
@@ -67,25 +67,25 @@ struct State {
 };
 constexpr uint32_t kOver = 0x7FFFFFFF;
 
-enum Mode : uint32_t { kDone, kFromTarget, kFromRest };
+enum Mode : uint32_t { kDone, kFromTarget, kFromRest, kOpen };
 struct End {  // of a path
   uint32_t mode, row, counter, rest_counter;
   float top;     // of the row
   uint32_t at;   // the largest logit's place
   uint32_t end;  // the row within its request
-  uint32_t lost; // children of it were refused
+  uint32_t lost; // children of it were refused; of an open one: the path's length
 };
 
 // 2^z for z <= 0 in fp64, off by 2^-39: the polynomial of degree 8 that meets 2^f in the nine
 // Chebyshev points of |f| <= 1/2.  z is cut at -1000, whose power is as good as zero; the
 // whole number is read out of the low bits of z + 1.5 * 2^52.
 // (Eight side by side: one after another, each step waits for the one before.)
+__device__ constexpr double kPowers[9] = {1.3255224878668817e-06, 1.5310079402249296e-05, 0.00015403455852453838,
+                                          0.0013333450568000645,  0.009618129159402558,   0.05550410941205933,
+                                          0.2402265069581299,     0.6931471805459335,     1.0};
 template <int N>
-__device__ __forceinline__ void exp2_64(double (&z)[N]) {
+__device__ __forceinline__ void exp2_64(double (&z)[N], const double* kC = kPowers) {
   constexpr double kRound = 6755399441055744.0;
-  constexpr double kC[9] = {1.3255224878668817e-06, 1.5310079402249296e-05, 0.00015403455852453838,
-                            0.0013333450568000645,  0.009618129159402558,   0.05550410941205933,
-                            0.2402265069581299,     0.6931471805459335,     1.0};
   double f[N], p[N];
   uint32_t n[N];
 #pragma unroll
@@ -102,9 +102,9 @@ __device__ __forceinline__ void exp2_64(double (&z)[N]) {
 #pragma unroll
   for (int e = 0; e < N; ++e) z[e] = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, p[e]) + ((uint64_t)n[e] << 52));
 }
-__device__ __forceinline__ double exp2_64(double z) {
+__device__ __forceinline__ double exp2_64(double z, const double* powers = kPowers) {
   double one[1] = {z};
-  exp2_64<1>(one);
+  exp2_64<1>(one, powers);
   return one[0];
 }
 
@@ -230,27 +230,9 @@ __device__ __forceinline__ void add_elements(RowSum& r, const float (&x)[N], F p
 // sum it is multiplied by powers whose arguments add up to -y, each off by 3 * 2^-24 of itself (the
 // difference, 1 / T, their product), at most 33 of them, each off by 2^-23; and 48 additions, 2^-24
 // each, follow.  The weighted mean of y is at most ln(vocabulary) < 15.3 (the weights sum to at least
-// 1).  Together less than (46 + 66 + 48) * 2^-24 < 2^-16.
-constexpr double kNear = 1.0 / 65536;
-
-// A row's sum in fp64, by the wave.
-template <class L>
-__device__ __forceinline__ double whole_sum(const VerifyArgs& a, uint64_t row, float top, double c) {
-  double sum = 0.0;
-  for (uint32_t v0 = threadIdx.x & 63; v0 < a.vocab; v0 += 256) {
-    float x[4];
-    double z[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = v0 + 64 * i < a.vocab ? L::one(a.logits, row * a.logits_row + v0 + 64 * i) : -INFINITY;
-      z[i] = ((double)x[i] - (double)top) * c;
-    }
-    exp2_64<4>(z);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum += x[i] > -INFINITY ? z[i] : 0.0;
-  }
-  return wave_sum(sum);
-}
+// 1).  Together less than (46 + 66 + 48) * 2^-24 < 2^-16.  (1 / T has fewer bits above T = 2^126, but
+// y is less than 8 there.)
+constexpr float kNear = 1.f / 65536;
 
 // Before all: rows in the order of their index within the request, no counts, paths of row
 // 0 alone.  Offsets that fall have no such order; their rows come as they are.
@@ -294,6 +276,97 @@ __global__ __launch_bounds__(kThreads) void k_verify_begin(VerifyArgs a) {
   if (live) a.path[row] = j ? -1 : 0;
 }
 
+// Up to 64 candidates for children of a path's end, a lane each: their tokens, and what is asked
+// about them.
+template <class L>
+struct Children {
+  float l = 0.f, u = 0.f, q = 1.f;
+  uint32_t x = 0xFFFFFFFFu;
+  static __device__ __forceinline__ uint32_t last(const VerifyArgs& a, uint32_t count, uint32_t end) {
+    return a.parents ? count : min(count, end + 2);  // a chain has one child
+  }
+  static __device__ __forceinline__ bool is_child(const VerifyArgs& a, uint32_t first, uint32_t end, uint32_t j) {
+    return a.parents ? a.parents[first + j] == (int32_t)end : j == end + 1;
+  }
+  // those from row j0 on; returns the lanes that are children
+  __device__ __forceinline__ uint64_t load(const VerifyArgs& a, uint32_t first, uint32_t count, uint32_t end, uint32_t j0) {
+    const uint64_t at = (uint64_t)first + end;
+    const uint32_t j = j0 + (threadIdx.x & 63);
+    const bool child = j < last(a, count, end) && is_child(a, first, end, j);
+    x = child ? (uint32_t)a.draft[first + j] : 0xFFFFFFFFu;
+    if (child) u = a.accept[first + j];
+    if (x < a.vocab) {
+      l = L::one(a.logits, at * a.logits_row + x);
+      if (a.probs) q = fmaxf(a.probs[at * a.probs_row + x], 0.f);  // (a NaN counts as 0)
+    }
+    return __ballot(child);
+  }
+};
+
+// The row's parts joined, by a wave; top, place and NaN are the same in all lanes.
+__device__ __forceinline__ RowSum join_parts(const VerifyArgs& a, uint64_t at, float c) {
+  RowSum row = RowSum::none();
+  for (uint32_t s = threadIdx.x & 63; s < a.segs; s += 64) {
+    const uint64_t* p = a.parts + 2 * (at * a.segs + s);
+    const uint64_t v = get(p), w = get(p + 1);
+    const float top = __uint_as_float((uint32_t)(v >> 32));
+    row.join(__uint_as_float((uint32_t)v), top, (uint32_t)w, top != top, c);
+  }
+  row.across_wave(c);
+  return row;
+}
+
+// Which child of `end` the wave's request goes to (0: none), against `left`, the row's sum, or none
+// while a number lies within `near` of it (*open).  *lost: a child was refused.
+template <class L>
+__device__ __forceinline__ uint32_t choose_child(const VerifyArgs& a, uint32_t first, uint32_t count, uint32_t end, double c64,
+                                                 const RowSum& row, Children<L>& child, uint64_t todo, double left, float near,
+                                                 bool* open, bool* lost, const double* powers = kPowers) {
+  const uint32_t lane = threadIdx.x & 63, last = Children<L>::last(a, count, end);
+  // children in the order of their rows, 64 candidates at a time
+  for (uint32_t j0 = end + 1; j0 < last && row.sound(); j0 += 64) {
+    if (j0 != end + 1) todo = child.load(a, first, count, end, j0);
+    const double e = child.x < a.vocab && child.l > -INFINITY ? exp2_64(((double)child.l - (double)row.top) * c64, powers) : 0.0;
+    while (todo) {
+      const int n = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      const uint32_t token = __shfl(child.x, n, 64), node = j0 + (uint32_t)n;
+      const double weight = __shfl(e, n, 64), draw = (double)__shfl(child.u, n, 64) * (double)__shfl(child.q, n, 64);
+      if (c64 > 0.0) {
+        // a token that an earlier sibling had is refused already
+        bool before = false;
+        if (a.parents && *lost && token < a.vocab)
+          for (uint32_t i = end + 1 + lane; i < node; i += 64)
+            before |= Children<L>::is_child(a, first, end, i) && (uint32_t)a.draft[first + i] == token;
+        if (token < a.vocab && !__any(before)) {
+          // (left is without the refused tokens; with draft probabilities there is one child)
+          if (fabs(draw * left - weight) < draw * near) {
+            *open = true;
+            return 0;
+          }
+          if (draw * left < weight) return node;
+          left -= weight;
+        }
+      } else if (token == row.at) {
+        return node;
+      }
+      *lost = true;
+    }
+  }
+  return 0;
+}
+
+// A path's end; its next token if no more than the largest logit is asked for, or -1 if there is none.
+__device__ __forceinline__ End end_path(const VerifyArgs& a, uint32_t b, uint32_t first, uint32_t end, uint32_t length, double c64,
+                                        const RowSum& row, bool lost, bool writes) {
+  const bool more = row.sound() && c64 > 0.0;  // the next token is still to be chosen
+  if (writes) {
+    a.accepted[b] = (int32_t)length;
+    if (!more) a.next[b] = row.sound() ? (int32_t)row.at : -1;
+  }
+  return End{!more ? kDone : a.probs && lost ? kFromRest : kFromTarget, first + end, 0, 0, row.top, row.at, end, lost};
+}
+
 // The wave decides about row `end` of request b, all parts of which are there, and about
 // those after it as far as theirs are.
 template <class L>
@@ -302,78 +375,22 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, uint32_t b, uint32_t
   const float c = heat32(c64);
   uint32_t length = (uint32_t)(get(&a.states[b].path) >> 32);
   for (;;) {
-    const uint64_t at = (uint64_t)first + end;
-    // the first 64 candidates for children, and what is asked about them ahead of the sum
-    const uint32_t last = a.parents ? count : min(count, end + 2);  // a chain has one child
-    float l = 0.f, u = 0.f, q = 1.f;
-    uint32_t x = 0xFFFFFFFFu;
-    auto is_child = [&](uint32_t j) { return a.parents ? a.parents[first + j] == (int32_t)end : j == end + 1; };
-    auto candidate = [&](uint32_t j) {
-      const bool child = j < last && is_child(j);
-      x = child ? (uint32_t)a.draft[first + j] : 0xFFFFFFFFu;
-      if (child) u = a.accept[first + j];
-      if (x < a.vocab) {
-        l = L::one(a.logits, at * a.logits_row + x);
-        if (a.probs) q = fmaxf(a.probs[at * a.probs_row + x], 0.f);  // (a NaN counts as 0)
-      }
-      return __ballot(child);
-    };
-    uint64_t todo = candidate(end + 1 + lane);
-    RowSum row = RowSum::none();
-    for (uint32_t s = lane; s < a.segs; s += 64) {
-      const uint64_t* p = a.parts + 2 * (at * a.segs + s);
-      const uint64_t v = get(p), w = get(p + 1);
-      const float top = __uint_as_float((uint32_t)(v >> 32));
-      row.join(__uint_as_float((uint32_t)v), top, (uint32_t)w, top != top, c);
-    }
-    row.across_wave(c);
-    uint32_t go = 0;
-    bool lost = false;  // a child of the end was refused
+    Children<L> child;
+    const uint64_t todo = child.load(a, first, count, end, end + 1);  // (ahead of the sum)
+    const RowSum row = join_parts(a, (uint64_t)first + end, c);
     // (the lanes' own fp32 sums differ in their last bits, as the terms come in another order)
-    double total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(row.sum))), left = total;
-    double near = c64 < 1.5e38 ? total * kNear : INFINITY;  // left: without the refused tokens
-    // children in the order of their rows, 64 candidates at a time
-    for (uint32_t j0 = end + 1; j0 < last && !go && row.sound(); j0 += 64) {
-      if (j0 != end + 1) todo = candidate(j0 + lane);
-      const double e = x < a.vocab && l > -INFINITY ? exp2_64(((double)l - (double)row.top) * c64) : 0.0;
-      while (todo) {
-        const int n = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        const uint32_t token = __shfl(x, n, 64), node = j0 + (uint32_t)n;
-        const double weight = __shfl(e, n, 64), draw = (double)__shfl(u, n, 64) * (double)__shfl(q, n, 64);
-        bool taken = false;
-        if (c > 0.f) {
-          // a token that an earlier sibling had is refused already
-          bool before = false;
-          if (a.parents && lost && token < a.vocab)
-            for (uint32_t i = end + 1 + lane; i < node; i += 64) before |= is_child(i) && (uint32_t)a.draft[first + i] == token;
-          if (token < a.vocab && !__any(before)) {
-            if (fabs(draw * (a.probs ? total : left) - weight) < draw * near) {
-              const double sum = whole_sum<L>(a, at, row.top, c64);
-              left += sum - total;
-              total = sum;
-              near = -1.0;
-            }
-            taken = draw * (a.probs ? total : left) < weight;
-            if (!taken) left -= weight;
-          }
-        } else {
-          taken = token == row.at;
-        }
-        if (taken) {
-          go = node;
-          break;
-        }
-        lost = true;
-      }
-    }
+    const float total = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(row.sum)));
+    bool open = false, lost = false;
+    const uint32_t go = choose_child<L>(a, first, count, end, c64, row, child, todo, total,
+                                        c < 3e38f ? total * kNear : INFINITY, &open, &lost);
     if (!go) {
       if (lane == 0) {
-        put(&a.states[b].path, kOver);
-        a.accepted[b] = (int32_t)length;
-        const bool more = row.sound() && c > 0.f;  // the next token is still to be chosen
-        a.ends[b] = End{!more ? kDone : a.probs && lost ? kFromRest : kFromTarget, first + end, 0, 0, row.top, row.at, end, lost};
-        if (!more) a.next[b] = row.sound() ? (int32_t)row.at : -1;
+        if (!open) {
+          put(&a.states[b].path, kOver);
+          a.ends[b] = end_path(a, b, first, end, length, c64, row, lost, true);
+        } else {  // the state stays, so the rows below are all looked at
+          a.ends[b] = End{kOpen, first + end, 0, 0, row.top, row.at, end, length};
+        }
       }
       return;
     }
@@ -596,6 +613,52 @@ __device__ __forceinline__ void choose_rest(const VerifyArgs& a, uint32_t b, uin
     choose_next(a, b, end, rest, weights, s_sum, s_pick);
 }
 
+// A path that was left open, to its end, by every workgroup of its request for itself (one writes):
+// all rows that it may come to have their parts by now.  (Here and not on the spot: the fp64 sum
+// in k_verify_rows takes 101 registers where 71 do, and of 96 chains 114.8 us for 109.6, of 64 trees
+// 102.5 for 97.)
+template <class L>
+__device__ __forceinline__ End finish_path(const VerifyArgs& a, uint32_t b, const End& open, double c64, bool writes, double* s_sum) {
+  uint32_t first, count, end = open.end, length = open.lost;
+  request_rows(a.cu, b, a.tokens, &first, &count);
+  for (;;) {
+    const RowSum row = join_parts(a, (uint64_t)first + end, heat32(c64));
+    const double* powers = kPowers;  // (read here: constants that stand ready for all loops hold 18 registers)
+    asm volatile("" : "+s"(powers));
+    double mine = 0.0, all = 0.0;
+    if (row.sound()) {
+#pragma unroll 1
+      for (uint32_t v0 = threadIdx.x; v0 < a.vocab; v0 += 4 * kThreads) {
+        double z[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t v = v0 + i * kThreads;
+          const float x = v < a.vocab ? L::one(a.logits, (first + end) * a.logits_row + v) : -INFINITY;
+          z[i] = x > -INFINITY ? ((double)x - (double)row.top) * c64 : -INFINITY;  // (2^-1000 is nothing beside 1)
+        }
+        exp2_64<4>(z, powers);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) mine += z[i];
+      }
+      run_before(mine, s_sum, &all);
+    }
+    Children<L> child;
+    bool never = false, lost = false;
+    const uint64_t todo = child.load(a, first, count, end, end + 1);
+    const uint32_t go = choose_child<L>(a, first, count, end, c64, row, child, todo, all, 0.f, &never, &lost, powers);
+    if (!go) {
+      End done = end_path(a, b, first, end, length, c64, row, lost, writes);
+      uint32_t* words = reinterpret_cast<uint32_t*>(&done);  // (the same in all lanes: no vector registers for them)
+#pragma unroll
+      for (uint32_t i = 0; i < sizeof(End) / 4; ++i) words[i] = __builtin_amdgcn_readfirstlane(words[i]);
+      return done;
+    }
+    end = __builtin_amdgcn_readfirstlane(go);
+    if (writes) a.path[first + length] = (int32_t)end;
+    ++length;
+  }
+}
+
 // Up to this many segments every workgroup adds up a whole row itself sooner than a launch
 // more would give its sum.
 constexpr uint32_t kFew = 8;
@@ -603,14 +666,19 @@ constexpr uint32_t kFew = 8;
 // Weights of a path's last row, a workgroup a segment; where they are p without the refused
 // tokens, the last workgroup chooses.
 template <class L>
-__global__ __launch_bounds__(kThreads) void k_verify_next(VerifyArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void k_verify_next(VerifyArgs a) {
   __shared__ double s_sum[kThreads / 64];
   __shared__ uint32_t s_gone[kSeg / 32];  // a bit for each refused token of a segment
   __shared__ uint32_t s_pick[2], s_last;
   const uint32_t b = blockIdx.x / a.segs, own = blockIdx.x - b * a.segs, t = threadIdx.x;
-  const End end = a.ends[b];
+  End end = a.ends[b];
   if (end.mode == kDone) return;
   const double c = heat(a, b);
+  if (end.mode == kOpen) {
+    end = finish_path<L>(a, b, end, c, own == 0 && t == 0, s_sum);
+    if (own == 0 && t == 0) a.ends[a.requests + b] = end;
+    if (end.mode == kDone) return;
+  }
   double w[kEach];
   if (end.mode == kFromRest && a.segs <= kFew) {
     double mine = 0.0, all;
@@ -654,7 +722,8 @@ __global__ __launch_bounds__(kThreads) void k_verify_rest(VerifyArgs a) {
   __shared__ double s_sum[kThreads / 64];
   __shared__ uint32_t s_pick[2], s_last;
   const uint32_t b = blockIdx.x / a.segs, own = blockIdx.x - b * a.segs;
-  const End end = a.ends[b];
+  End end = a.ends[b];
+  if (end.mode == kOpen) end = a.ends[a.requests + b];
   if (end.mode != kFromRest) return;
   double first;
   const double all = all_sums(a.sums + (uint64_t)b * a.segs, a.segs, &first);
@@ -681,7 +750,7 @@ VerifyPlan plan_verify(uint32_t tokens, uint32_t vocab, uint32_t requests) {
   p.states_off = take((size_t)requests * sizeof(State));
   p.sums_off = take((size_t)requests * p.segs * 8);
   p.rest_off = take((size_t)requests * p.segs * 8);
-  p.ends_off = take((size_t)requests * sizeof(End));
+  p.ends_off = take((size_t)requests * 2 * sizeof(End));
   p.bytes = std::max<size_t>(at, 256);
   return p;
 }

@@ -387,3 +387,47 @@ def test_masks_of_the_lowest_value(kind, dtype):
         if kind == "probs":
             d["probs"][:] = 1.0 / vocab
         _check(d, _run(d))
+
+
+@pytest.mark.parametrize("kind", ["chain", "probs", "tree"])
+@pytest.mark.parametrize("vocab", [700, 30000, 60000])
+def test_paths_of_numbers_next_to_their_borders(vocab, kind):
+    """Number after number next to its border, some requests greedy or with rows that end a path: paths go on
+    behind a close one."""
+    n, new = 24, 7
+    heat = np.where(np.arange(n) % 8 == 7, 0.0, np.linspace(0.6, 1.4, n)).astype(np.float32)
+    d = _make(50, [new] * n, vocab, probs=kind == "probs", temperature=heat)
+    rng = np.random.default_rng(51)
+    d["parents"] = np.tile([-1, 0, 0, 2, 2, 2, 5], n) if kind == "tree" else None
+    up = np.tile([-1, 0, 0, 2, 2, 2, 5] if kind == "tree" else np.arange(-1, new - 1), (n, 1))
+    # where the path is to go: of a tree to 2 (past 1), 5 (past 3 and 4), 6; of a chain down to a row of its own
+    stop = rng.integers(1, new + 1, n)
+    refused = np.tile([False, True, False, True, True, False, False], (n, 1)) if kind == "tree" else (
+        np.arange(new) >= stop[:, None])
+    refused[::5, -1] = True
+    logits = d["logits"].numpy().reshape(n, new, vocab)
+    logits[3, 2, 17] = np.nan
+    draft, accept = d["draft"].reshape(n, new), d["accept"].reshape(n, new)
+    for b in range(n):
+        left = {}
+        for i in range(1, new):
+            row = logits[b, up[b, i]].astype(float)
+            if not np.isfinite(row).all() or heat[b] <= 0:
+                draft[b, i] = np.nanargmax(row) if not refused[b, i] else np.nanargmin(row)
+                continue
+            p = np.exp((row - row.max()) / float(heat[b]))
+            p /= p.sum()
+            gone = left.setdefault(up[b, i], [])
+            draft[b, i] = x = np.argsort(p)[-1 - len(gone) - int(rng.integers(0, 2)) * 3]
+            border = p[x] / np.delete(p, gone).sum()
+            if kind == "probs":
+                d["probs"][b * new + up[b, i], x] = q = np.float32(p[x] * 1.3)
+                border = p[x] / float(q)
+            accept[b, i] = _beside(np.array([border]), [refused[b, i]])[0]
+            gone.append(x)
+    lengths = _check(d, _run(d))
+    live = [b for b in range(n) if b != 3]
+    if kind == "tree":
+        assert [lengths[b] for b in live] == [3 if refused[b, -1] else 4 for b in live]
+    else:
+        assert [lengths[b] for b in live] == [int(np.argmax(np.append(refused[b], True))) for b in live]
