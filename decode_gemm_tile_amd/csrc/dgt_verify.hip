@@ -411,6 +411,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, uint32_t b, uint32_t
 template <class L>
 __global__ __launch_bounds__(kThreads) void k_verify_rows(VerifyArgs a) {
   __shared__ RowSum s_part[kThreads / 64];
+  __shared__ uint32_t s_passed[kThreads / 64];
   const uint32_t turn = blockIdx.x / a.segs, seg = blockIdx.x - turn * a.segs, t = threadIdx.x;
   const uint32_t row = a.order[2 * turn], b = a.order[2 * turn + 1];
   if (b >= a.requests) return;
@@ -419,30 +420,35 @@ __global__ __launch_bounds__(kThreads) void k_verify_rows(VerifyArgs a) {
   const uint32_t j = row - first;
   if (j >= count) return;
   // On the way down from the path's end?  (An end that is not the latest only means that
-  // less is passed by.)
-  const uint32_t end = (uint32_t)get(&a.states[b].path);
-  if (j < end) return;
-  if (end && a.parents) {
+  // less is passed by.  Each wave asks for itself while the path goes on, so some may find the
+  // row passed by and others not: what one has found holds for good, and no part is left then.)
+  const uint32_t end = __builtin_amdgcn_readfirstlane((uint32_t)get(&a.states[b].path));
+  bool passed = j < end;
+  if (end && a.parents && !passed) {
     uint32_t x = j;
     while (x > end) {
       const uint32_t up = (uint32_t)a.parents[first + x];
-      if (up >= x) return;
-      x = up;
+      x = up < x ? up : 0;  // (a link that is no tree's leads nowhere, and 0 is above the end)
     }
-    if (x < end) return;
+    passed = x < end;
   }
   const double c64 = heat(a, b);
   const float c = heat32(c64);
-  float x[kEach];
-  load_places<L>(a.logits, row * a.logits_row, seg, a.vocab, a.wide, -INFINITY, place<L>, x);
   RowSum r = RowSum::none();
-  add_elements(r, x, [&](uint32_t e) { return seg * kSeg + place<L>(e); }, c);
-  r.across_wave(c);
-  if ((t & 63) == 0) s_part[t >> 6] = r;
+  if (!passed) {
+    float x[kEach];
+    load_places<L>(a.logits, row * a.logits_row, seg, a.vocab, a.wide, -INFINITY, place<L>, x);
+    add_elements(r, x, [&](uint32_t e) { return seg * kSeg + place<L>(e); }, c);
+    r.across_wave(c);
+  }
+  if ((t & 63) == 0) {
+    s_part[t >> 6] = r;
+    s_passed[t >> 6] = passed;
+  }
   __syncthreads();
   if (t >= 64) return;
   uint32_t old = 0;
-  if (t == 0) {
+  if (t == 0 && !(s_passed[0] | s_passed[1] | s_passed[2] | s_passed[3])) {
     for (uint32_t w = 1; w < kThreads / 64; ++w) r.join(s_part[w].sum, s_part[w].top, s_part[w].at, s_part[w].odd, c);
     uint64_t* p = a.parts + 2 * ((uint64_t)row * a.segs + seg);
     put(p, __float_as_uint(r.sum) | (uint64_t)__float_as_uint(r.odd ? NAN : r.top) << 32);

@@ -431,3 +431,16 @@ def test_paths_of_numbers_next_to_their_borders(vocab, kind):
         assert [lengths[b] for b in live] == [3 if refused[b, -1] else 4 for b in live]
     else:
         assert [lengths[b] for b in live] == [int(np.argmax(np.append(refused[b], True))) for b in live]
+
+
+def test_rows_that_the_path_passes_by():
+    """Many trees whose rows are read and passed by while the paths go on: every run gives the same, and what the
+    definition says."""
+    d = _make(60, [27] * 60 + [70] * 4, 12300, tree=True)
+    args, named = _args(d)
+    ws = dgt.alloc_workspace(dgt.dgt_verify_workspace(1900, 12300, 64))
+    _check(d, _run(d, ws=ws))
+    first = _run(d, ws=ws)
+    for _ in range(20):
+        v = dgt.dgt_verify(*args, **named, ws=ws)
+        assert v.path.equal(first.path) and v.accepted.equal(first.accepted) and v.next.equal(first.next)
