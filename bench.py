@@ -64,7 +64,7 @@ def source_hash() -> str:
     d = os.path.join(ROOT, "decode_gemm_tile_amd", "csrc")
     for name in sorted(os.listdir(d)):
         if name in ("dgt_host.cpp", "dgt_serve.h", "dgt_pages.hip", "dgt_tree_attn.hip", "dgt_lora.hip",
-                    "dgt_rope.hip", "dgt_verify.hip", "dgt_moves.hip", "dgt_chunk_attn.hip"):
+                    "dgt_rope.hip", "dgt_verify.hip", "dgt_moves.hip", "dgt_chunk_attn.hip", "dgt_chunk_plan.h"):
             continue
         with open(os.path.join(d, name), "rb") as fh:
             h.update(name.encode() + fh.read())

@@ -1,4 +1,5 @@
 // Attention of a chunk of new tokens over a paged cache.
+#include "dgt_chunk_plan.h"
 #include "dgt_serve.h"
 
 #include <algorithm>
@@ -73,7 +74,7 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, uint32_t b) {
 // keys, a call takes one piece where no CU gets two; else its work over the CUs, or a
 // piece if that is more, and half an item, as the longest go first.  A part written and
 // read again costs as much as kPart of them.
-constexpr uint32_t kPlanThreads = 256, kMaxSorted = 1024, kChoices = 32;
+constexpr uint32_t kPlanThreads = 256, kMaxSorted = 1024;
 constexpr float kPart = 6.f;
 
 template <class T, class F>
@@ -113,10 +114,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_chunk_plan(ChunkArgs a) {
   const bool sound = reduce_all(rows, s_f, add) <= (float)a.tokens;
   most = reduce_all(most, s_u, [](uint32_t x, uint32_t y) { return max(x, y); });
 
-  // Choice i cuts the longest tile into about 1.25^i pieces; 32 choices side by side, each
-  // over the requests in eight strides.
+  // 32 choices of lengths side by side, each over the requests in eight strides.
   const uint32_t units = max((most + kKeys - 1) / kKeys, 1u), choice = t % kChoices;
-  const uint32_t len = max((uint32_t)ceilf((float)units * exp2f(-0.32192809f * (float)choice)), min(units, 2u));
+  const uint32_t len = piece_units(units, choice);
   float items = 0.f, parts = 0.f;
   for (uint32_t b = t / kChoices; b < a.requests; b += kPlanThreads / kChoices) {
     const uint32_t n = (uint32_t)(((uint64_t)s_keys[b] + len * kKeys - 1) / (len * kKeys));
