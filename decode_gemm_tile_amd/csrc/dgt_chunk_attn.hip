@@ -333,21 +333,24 @@ struct PartOf {  // ref[rows], l[rows], then the outputs in the order of the lan
   static constexpr uint32_t kFloats = kRows * (DP + 2);
 };
 
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is reserved, and named so that nothing of the compiler's is kept in it
 // 16 bytes a lane from memory into LDS, lane after lane from `to` (the same for all lanes of
 // the wave) on.  The compiler does not know that it is under way: loads_wait<n> waits until no
 // more than the last n of the wave's loads are.  (The compiler's own waits for its loads count
 // these too, and so wait longer than they need.)
 __device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, uint32_t to) {
   // (a base that a vector instruction has just written, as v_readlane does, may be read 5 steps on)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory", "m0");
 }
 // The same with 4 bytes a lane.
 __device__ __forceinline__ void load_word_to_lds(const void* base, uint32_t offset, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 template <int N>
 __device__ __forceinline__ void loads_wait() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
