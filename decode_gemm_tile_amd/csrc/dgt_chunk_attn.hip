@@ -457,7 +457,9 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
     uint32_t keys_lo = 0, keys_hi = 0;  // where the keys of this lane's group are
     uint64_t gone = 0;                  // a bit for each group that does not exist; page 0 is read instead
     auto locate = [&](uint32_t n) {
-      const uint32_t key = it.k0 + n * T::kKeys + 8 * lane, id = entries[lane];
+      const uint32_t key = it.k0 + n * T::kKeys + 8 * lane;
+      uint32_t id = entries[lane];
+      keep_here(id);  // it is there before the next entries set out for its place
       const bool off = id >= a.blocks || key >= it.k1;
       gone = __ballot(off);
       const uint64_t page = (uint64_t)(off ? 0u : id) * page_bytes;
