@@ -803,10 +803,10 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
 
 // Adds up the parts of tiles that were cut, in the order of the keys: a workgroup takes some
 // rows of a tile, a thread four outputs of a row in all parts, eight of which are asked for at a
-// time.  Where a tile has more, a workgroup takes a quarter as many rows, a thread a quarter of the
-// parts, and the quarters meet in LDS.  (26 tokens behind 16000 keys of one head, 125 parts: 7 us in
-// quarters, 44 without; 128 tokens behind 4000 of 8 requests, 4 parts: the call 106 us without, 124
-// in quarters.)
+// time.  Where the call's longest tile has more than kWhole, a workgroup takes a quarter as many rows,
+// a thread a quarter of the parts, and the quarters meet in LDS.  (In quarters and without, by the
+// longest tile's parts: 2 parts 46 and 16 us, 10 8.5 and 6.2, 14 to 16 9.2 and 7.6, 18 9.4 and 8.9, 21
+// 5.9 and 6.8, 23 9.0 and 9.1, 28 8.4 and 9.9, 126 7.4 and 22.)
 struct Joined {
   float m = -INFINITY, l = 0.f;
   floatx4 o = {};
@@ -822,11 +822,11 @@ struct Joined {
 template <class E, int DP, int WAVES>
 __global__ __launch_bounds__(256) void k_chunk_join(ChunkArgs a) {
   using P = PartOf<DP, WAVES>;
-  constexpr uint32_t kFours = DP / 4, kQuarters = 4, kAtOnce = 8;
+  constexpr uint32_t kFours = DP / 4, kQuarters = 4, kAtOnce = 8, kWhole = 20;
   __shared__ floatx4 s_o[256];
   __shared__ float s_m[256], s_l[256];
   const uint32_t piece = a.plan[Plan::kPiece], cut = a.plan[Plan::kCut], t = threadIdx.x;
-  const uint32_t quarters = a.plan[Plan::kMost] > kAtOnce ? kQuarters : 1;
+  const uint32_t quarters = a.plan[Plan::kMost] > kWhole ? kQuarters : 1;
   const uint32_t rows = 256 / kFours / quarters, steps = P::kRows / rows;  // of a workgroup, of a tile
   const uint32_t d = 4 * (t % kFours), row = t / kFours % rows, quarter = t / kFours / rows;
   for (uint64_t unit = blockIdx.x; unit < (uint64_t)cut * steps; unit += gridDim.x) {

@@ -261,3 +261,24 @@ def test_every_number_of_tiles(dim):
     lens = [1, 31, 32, 33, 63, 64, 65, 96, 97, 127, 129, 191, 193, 255, 257, 321, 384, 449, 513, 577]
     d = _long([n - 1 for n in lens], [1] * len(lens), 4, 2, dim, 8, "bfloat16", seed=dim)
     _check_long(d, _run(dict(d, table=d["table"].cpu().numpy())))
+
+
+@pytest.mark.parametrize("shape", [
+    # tiles of about 10, 16, 18, 21, 27 and 126 parts, and a long request beside short ones
+    ([3000], [100], 32, 8, 128, 16, "bfloat16"),
+    ([4000], [64], 32, 8, 128, 16, "float16"),
+    ([20000], [64], 48, 12, 128, 16, "bfloat16"),
+    ([9000], [30], 12, 12, 128, 32, "bfloat16"),
+    ([20000], [64], 36, 9, 64, 16, "float16"),
+    ([16000], [26], 3, 1, 128, 64, "bfloat16"),
+    ([16000, 900, 40], [26, 30, 3], 3, 1, 80, 16, "bfloat16"),
+    ([16000], [20], 8, 2, 256, 16, "bfloat16"),
+])
+def test_joins_of_few_and_many_parts(shape):
+    """One thread for all parts of a row, or a quarter each; the same on every run."""
+    import torch
+    d = _long(*shape, seed=70)
+    run = lambda: dgt.dgt_chunk_attention(d["q"], d["kc"], d["vc"], d["table"], _i32(d["ctx"]), _i32(d["cu"]))
+    out = run()
+    _check_long(d, out)
+    assert torch.equal(run().view(torch.int16), out.view(torch.int16))
