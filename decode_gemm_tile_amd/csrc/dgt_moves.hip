@@ -42,11 +42,13 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* s_sum, uint
 }
 
 // ----------------------------------------------------------------------- keep
-// One launch: a workgroup for lengths and pages, the others move rows.  A chain of
-// latencies (offsets, path, slots, rows) bounds it; a workgroup goes through it once for
-// several layers and heads, so that all of them are on the card at a time.
-// 128 trees of up to 61 in 4 layers of 8 heads of 128: 15-18 us, with a workgroup a layer and head 36;
-// the bytes alone 4.4.  4 requests in one layer: 4.6.
+// One launch: a workgroup for lengths and pages, the others move rows.  A workgroup goes through
+// the chain of latencies (offsets, path, slots, rows) once for several layers and heads, so that
+// all of them are on the card at a time.
+// 128 trees of up to 61 in 4 layers of 8 heads of 128: 15-18 us, with a workgroup a layer and head 36.
+// A token's values are 2 bytes of a row of each value page, so what moves is not the 21 MB of the
+// elements (4.4 us) but their lines: 18 MB read and 24 written, 9 us at a copy's rate.  The rest is
+// the chain, as in 4 requests in one layer: 4.6.
 struct KeepArgs {
   const int32_t *path, *kept, *ctx, *cu, *slots, *free_head;
   int32_t *free_list, *table, *lens, *counts;
@@ -77,7 +79,6 @@ struct Kept {
 __device__ __forceinline__ uint32_t rows_that_stay(const KeepArgs& a, uint32_t first, uint32_t count, uint32_t kept,
                                                    uint32_t left, Kept* s_kept) {
   const uint32_t t = threadIdx.x, lane = t & 63, n = t % 16;
-  if (a.tokens == 0) return 0;
   // Four rows a thread at a time, their loads beside one another (row 0's where there is none).
   auto look = [&](const Kept (&it)[4], const uint32_t (&j)[4], bool (&gone)[4]) {
     uint32_t place[4], from[4], slot[4];
@@ -144,6 +145,35 @@ __device__ __forceinline__ uint32_t rows_that_stay(const KeepArgs& a, uint32_t f
   return s_kept[t].rows;  // (the next round's write is of the same thread)
 }
 
+// Some row of the step has no slot: only then may a path have to be cut, so a step without one (the
+// rule) pays for one look at its slots, 16 bytes a thread.  (8 prompts of 8000 tokens: 16 us with it, 43
+// with rows_that_stay; 8192 requests: 50 and 220.)
+__device__ __forceinline__ bool slots_missing(const KeepArgs& a) {
+  const uint32_t t = threadIdx.x;
+  const uint32_t own = t < a.tokens ? (uint32_t)a.slots[t] : 0;
+  const uint32_t end = a.requests ? (uint32_t)min(max(a.cu[a.requests], 0), (int)a.tokens) : 0;
+  bool missing = t < end && !a.pool.holds(own);
+  uint32_t from = 256;
+  if (reinterpret_cast<uintptr_t>(a.slots) % 16 == 0) {
+    for (; from + 4 <= end; from += 4 * 256 * 8) {
+      u32x4 v[8];
+#pragma unroll
+      for (uint32_t n = 0; n < 8; ++n) {
+        const uint32_t i = from + 4 * (256 * n + t);
+        v[n] = reinterpret_cast<const u32x4*>(a.slots)[i + 4 <= end ? i / 4 : 0];
+      }
+#pragma unroll
+      for (uint32_t n = 0; n < 8; ++n)
+        if (from + 4 * (256 * n + t) + 4 <= end)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) missing |= !a.pool.holds(v[n][e]);
+    }
+    from = end > 256 ? end / 4 * 4 : 256;  // the last few
+  }
+  for (uint32_t i = from + t; i < end; i += 256) missing |= !a.pool.holds((uint32_t)a.slots[i]);
+  return __syncthreads_or(missing);
+}
+
 // Lengths, and the pages past them, by one workgroup: the list's order is the requests'.
 // A column past the kept tokens begins at or behind the cached ones' end, so a new token
 // lies first in it and its slot names the page.  One that the plan gave no slot (a bad link,
@@ -152,6 +182,9 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum, K
   const uint32_t log = a.pool.log_block, round = a.pool.block() - 1;
   const uint32_t head = min((uint32_t)max(*a.free_head, 0), a.free_len);
   uint32_t total = 0;
+  // rounds of 256 requests in which a path may be cut
+  uint32_t cuts = slots_missing(a) ? ~0u : 0u;
+  static_assert(kMaxRequests <= 32 * 256, "a bit a round");
   // where 256 threads do not hold all requests, twice over them: how many pages, then which
   for (int pass = a.requests <= 256; pass < 2; ++pass) {
     uint32_t done = 0;
@@ -164,7 +197,11 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum, K
         ctx = (uint32_t)max(a.ctx[b], 0);
         kept = kept_of(a, b, first, count, &held);
       }
-      kept = rows_that_stay(a, first, count, kept, a.requests - b0, s_kept);
+      if (cuts >> b0 / 256 & 1) {
+        const uint32_t most = kept;
+        kept = rows_that_stay(a, first, count, kept, a.requests - b0, s_kept);
+        if (pass == 0 && !__syncthreads_or(kept < most)) cuts &= ~(1u << b0 / 256);
+      }
       if (b < a.requests) {
         now = (uint32_t)min((uint64_t)ctx + kept, (uint64_t)0x7FFFFFFF);
         from = min((uint32_t)(((uint64_t)now + round) >> log), a.width);
@@ -205,83 +242,94 @@ __device__ __forceinline__ void keep_pages(const KeepArgs& a, uint32_t* s_sum, K
 // A workgroup moves the kept rows of one request in some heads of the layers, 16 at a
 // time: all of them are read before any is written.  Index i_j >= j rises with j, so a
 // row that a later step reads lies behind every place that this one writes.  Slots are
-// looked up in the plan's list and not in the table, whose columns change at the same time.
-// s_end: of two steps in turn, the first row that does not stay.
-__device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, uint32_t* s_src, uint32_t* s_dst, uint32_t* s_end) {
+// looked up in the plan's list and not in the table, whose columns change at the same time,
+// 64 rows at a time; of them wave 0 leaves the slots and a bit for each 16 that something of
+// moves (kEnds: a row does not stay), in one of two sets of LDS in turn.
+constexpr uint32_t kLook = 64, kEnds = 1u << 4;
+struct Moves {
+  uint32_t src[kLook], dst[kLook], what;
+};
+__device__ __forceinline__ void keep_rows(const KeepArgs& a, uint32_t unit, Moves* s_moves) {
   const uint32_t t = threadIdx.x, dim = a.pool.dim, log = a.pool.log_block, in_page = a.pool.block() - 1;
   const uint32_t b = unit / a.parts, part = unit - b * a.parts;
   const uint32_t lh0 = part * a.each, lh1 = min(lh0 + a.each, a.pool.layers * a.pool.heads);
   uint32_t first, count;
   request_rows(a.cu, b, a.tokens, &first, &count);
-  int32_t ahead = t < min(count, kKeepRows) ? a.path[first + t] : 0;
+  int32_t ahead = t < min(count, kLook) ? a.path[first + t] : 0;
   bool held;
   const uint32_t kept = kept_of(a, b, first, count, &held);
-  bool ends = false;
-  for (uint32_t j0 = 0; j0 < kept && !ends; j0 += kKeepRows) {
-    const uint32_t rows = min(kept - j0, kKeepRows);
-    uint32_t* end = s_end + j0 / kKeepRows % 2;
-    bool moves = false;
-    if (t < 64) {
+  uint32_t what = 0;
+  for (uint32_t j0 = 0; j0 < kept && !(what & kEnds); j0 += kLook) {
+    Moves& s = s_moves[j0 / kLook % 2];
+    if (t < kLook) {
+      const uint32_t j = j0 + t;
       uint32_t src = ~0u, dst = ~0u;
-      bool stay = true;
-      if (t < rows) {
-        const uint32_t j = j0 + t, i = (uint32_t)(j0 ? a.path[first + j] : ahead);
+      bool moves = false, stays = true;
+      if (j < kept) {
+        const uint32_t i = (uint32_t)(j0 ? a.path[first + j] : ahead);
         moves = i > j && i < count;
         dst = (uint32_t)a.slots[first + j];
         if (moves) src = (uint32_t)a.slots[first + i];
-        stay = a.pool.holds(dst) && (!moves || a.pool.holds(src));
+        stays = a.pool.holds(dst) && (!moves || a.pool.holds(src));
       }
-      const uint64_t gone = __ballot(!stay);
-      const uint32_t least = gone ? (uint32_t)__builtin_ctzll(gone) : rows;
-      moves = moves && t < least;
-      if (t < rows) {
-        s_src[t] = moves ? src : ~0u;
-        s_dst[t] = dst;
-      }
-      if (t == 0) *end = least;
-    }
-    const bool any = __syncthreads_or(moves);
-    ends = *end < rows;
-    if (!any) continue;
-    const uint32_t vr = t % kKeepRows, v_src = vr < rows ? s_src[vr] : ~0u, v_dst = v_src != ~0u ? s_dst[vr] : 0;
-    for (uint32_t lh = lh0; lh < lh1; ++lh) {
-      const uint32_t layer = lh / a.pool.heads, head = lh - layer * a.pool.heads;
-      // value elements, a value row's side by side; 16-byte pieces of key rows, a row's side by side
-      const uint16_t* vs = a.pool.vc + a.pool.page(layer, v_src != ~0u ? v_src >> log : 0, head) + (v_src & in_page);
-      uint16_t* vd = a.pool.vc + a.pool.page(layer, v_dst >> log, head) + (v_dst & in_page);
-      for (uint32_t d0 = 0; d0 < dim; d0 += 128) {
-        const uint32_t dims = min(dim - d0, 128u);
-        u32x4 k;
-        uint16_t v[8];
-        const uint32_t r = t / (dims / 8), d = d0 + 8 * (t % (dims / 8));
-        const bool k_on = r < rows && s_src[r] != ~0u;
-        if (k_on)
-          k = *reinterpret_cast<const u32x4*>(a.pool.kc + a.pool.page(layer, s_src[r] >> log, head) + (s_src[r] & in_page) * dim + d);
+      const uint64_t gone = __ballot(!stays);
+      moves = moves && !(gone & ((2ull << t) - 1));  // neither the row nor one before it is gone
+      const uint64_t all = __ballot(moves);
+      s.src[t] = moves ? src : ~0u;
+      s.dst[t] = dst;
+      if (t == 0) {
+        uint32_t bits = gone ? kEnds : 0;
 #pragma unroll
-        for (uint32_t n = 0; n < 8; ++n) {
-          const uint32_t e = d0 + t / kKeepRows + 16 * n;
-          if (v_src != ~0u && e < d0 + dims) v[n] = vs[(uint64_t)e << log];
-        }
-        __syncthreads();
-        if (k_on)
-          *reinterpret_cast<u32x4*>(a.pool.kc + a.pool.page(layer, s_dst[r] >> log, head) + (s_dst[r] & in_page) * dim + d) = k;
-#pragma unroll
-        for (uint32_t n = 0; n < 8; ++n) {
-          const uint32_t e = d0 + t / kKeepRows + 16 * n;
-          if (v_src != ~0u && e < d0 + dims) vd[(uint64_t)e << log] = v[n];
-        }
+        for (uint32_t g = 0; g < kLook / kKeepRows; ++g) bits |= (all >> (kKeepRows * g) & 0xFFFFu) ? 1u << g : 0u;
+        s.what = bits;
       }
     }
-    __syncthreads();  // what was written is behind what the next step reads; s_src is reused
+    __syncthreads();
+    what = __builtin_amdgcn_readfirstlane(s.what);
+    for (uint32_t g = 0; g < kLook / kKeepRows; ++g) {
+      if (!(what >> g & 1)) continue;
+      const uint32_t *s_src = s.src + kKeepRows * g, *s_dst = s.dst + kKeepRows * g;
+      const uint32_t vr = t % kKeepRows, v_src = s_src[vr], v_dst = v_src != ~0u ? s_dst[vr] : 0;
+      for (uint32_t lh = lh0; lh < lh1; ++lh) {
+        const uint32_t layer = lh / a.pool.heads, head = lh - layer * a.pool.heads;
+        // value elements, a value row's side by side; 16-byte pieces of key rows, a row's side by side
+        const uint16_t* vs = a.pool.vc + a.pool.page(layer, v_src != ~0u ? v_src >> log : 0, head) + (v_src & in_page);
+        uint16_t* vd = a.pool.vc + a.pool.page(layer, v_dst >> log, head) + (v_dst & in_page);
+        for (uint32_t d0 = 0; d0 < dim; d0 += 128) {
+          const uint32_t dims = min(dim - d0, 128u);
+          u32x4 k;
+          uint16_t v[8];
+          const uint32_t r = t / (dims / 8), d = d0 + 8 * (t % (dims / 8));
+          const bool k_on = r < kKeepRows && s_src[r] != ~0u;
+          if (k_on)
+            k = *reinterpret_cast<const u32x4*>(a.pool.kc + a.pool.page(layer, s_src[r] >> log, head) + (s_src[r] & in_page) * dim + d);
+#pragma unroll
+          for (uint32_t n = 0; n < 8; ++n) {
+            const uint32_t e = d0 + t / kKeepRows + 16 * n;
+            if (v_src != ~0u && e < d0 + dims) v[n] = vs[(uint64_t)e << log];
+          }
+          __syncthreads();
+          if (k_on)
+            *reinterpret_cast<u32x4*>(a.pool.kc + a.pool.page(layer, s_dst[r] >> log, head) + (s_dst[r] & in_page) * dim + d) = k;
+#pragma unroll
+          for (uint32_t n = 0; n < 8; ++n) {
+            const uint32_t e = d0 + t / kKeepRows + 16 * n;
+            if (v_src != ~0u && e < d0 + dims) vd[(uint64_t)e << log] = v[n];
+          }
+        }
+      }
+      __syncthreads();  // what was written is behind what the next step reads
+    }
   }
 }
 
 // (eight workgroups a CU, 64 registers: with 123 registers and four of them the trees take 20.6 us)
 __global__ __launch_bounds__(256, 8) void k_page_keep(KeepArgs a) {
-  __shared__ uint32_t s_sum[4], s_src[kKeepRows], s_dst[kKeepRows], s_end[2];
+  __shared__ uint32_t s_sum[4];
   __shared__ Kept s_kept[256];
+  __shared__ Moves s_moves[2];
   if (blockIdx.x == 0) keep_pages(a, s_sum, s_kept);
-  else keep_rows(a, blockIdx.x - 1, s_src, s_dst, s_end);
+  else keep_rows(a, blockIdx.x - 1, s_moves);
 }
 
 // ----------------------------------------------------------------------- fork
