@@ -854,8 +854,10 @@ def dgt_chunk_attention(q, k_cache, v_cache, block_table, ctx_lens, cu, scale=No
                         stream=None):
     """Causal attention of the new tokens q [tokens, heads, dim] over each request's cached tokens and
     its new ones (already stored): dgt_tree_attention without a mask, made for prompts and parts of
-    prompts.  scale defaults to dim ** -0.5.  Rows past cu[-1] of `out` are not written.  ws: a workspace
-    to keep between calls (any contents); without one each call makes its own."""
+    prompts (up to 16 new tokens a request dgt_tree_attention is faster, from 128 on this one).  scale
+    defaults to dim ** -0.5.  Rows past cu[-1] of `out` are not written, and none are where cu falls and
+    names more rows than there are.  ws: a workspace to keep between calls (any contents; 68, 136 or
+    270 MB, by the heads' length); without one each call makes its own."""
     import torch
     i32 = torch.int32
     try:
@@ -1136,7 +1138,8 @@ def dgt_page_free_workspace(blocks) -> int:
 
 def dgt_page_free(rows, lens, free_blocks, free_head, block_table, shares, block_size, counts=None, ws=None,
                   stream=None):
-    """The requests in `rows` (int32, rows of block_table) end: their pages lose a holder, and those that
+    """The requests in `rows` (int32, rows of block_table) end: the pages of their lengths (those of a step's
+    new tokens go back with dgt_page_keep, kept 0, first) lose a holder, and those that
     no other request holds (shares) go back into free_blocks, in front of its head; their lengths become 0.
     ws: a workspace to keep between calls (alloc_workspace); without one each call makes its own.  Returns
     counts int32[2]: the list's new head, the pages that went back."""

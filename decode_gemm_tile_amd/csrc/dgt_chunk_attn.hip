@@ -540,8 +540,8 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_chunk_attention(ChunkArgs a) 
     // needed the sum of both: a product that waits for the unit keeps the other wave's
     // instructions back.)
     //
-    // 3 prompts of 8190 tokens, 32 heads over 8 of 128, bf16: 797-837 us on several cards, 973-1021
-    // TFLOP/s (in turns 861 where it is 820; the products alone 467).  The matrix units are busy for 46% of the cycles, at 1.8 to 2 GHz of 2.4:
+    // 3 prompts of 8190 tokens, 32 heads over 8 of 128, bf16: 795-855 us on several cards, 952-1024
+    // TFLOP/s (in turns 861 where it is 820; the products alone 467).  The matrix units are busy for 46-49% of the cycles, at 1.8 to 2 GHz of 2.4:
     // the clock gives way to power (3 x 4096 tokens: 950 TFLOP/s, with zeros for keys and values 1125).
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = floatx16{};

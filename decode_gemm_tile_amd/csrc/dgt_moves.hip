@@ -146,8 +146,8 @@ __device__ __forceinline__ uint32_t rows_that_stay(const KeepArgs& a, uint32_t f
 }
 
 // Some row of the step has no slot: only then may a path have to be cut, so a step without one (the
-// rule) pays for one look at its slots, 16 bytes a thread.  (8 prompts of 8000 tokens: 16 us with it, 43
-// with rows_that_stay; 8192 requests: 50 and 220.)
+// rule) pays for one look at its slots, 16 bytes a thread.  (8 prompts of 8000 tokens: 10 us with it, 43
+// with rows_that_stay; 1000 requests of 8: 10.5 and 34.)
 __device__ __forceinline__ bool slots_missing(const KeepArgs& a) {
   const uint32_t t = threadIdx.x;
   const uint32_t own = t < a.tokens ? (uint32_t)a.slots[t] : 0;

@@ -24,9 +24,9 @@ namespace {
 // workgroup chooses.  Where a chain was refused the weights are max(p - q, 0), p needs
 // the whole row's sum first, and one more launch forms them.
 //
-// Measured: 96 chains of up to 7, 128000 tokens, bf16: 101 us (order 5, rows 38, last rows 32,
-// refused ones 30); 64 trees of up to 27, fp32: 82 (5, 71, 20); 5 chains of up to 5, 32000, fp32:
-// 35 (4, 12, 21).  Chains of latencies bound all of them (in the trees 160 MB of 380 are read,
+// Measured: 96 chains of up to 7, 128000 tokens, bf16: 106 us (order 5, rows 45, last rows 28,
+// refused ones 30); 64 trees of up to 27, fp32: 72-86 (5, 67, 21); 5 chains of up to 5, 32000, fp32:
+// 37 (4, 15, 21).  Chains of latencies bound all of them (in the trees 160 MB of 380 are read,
 // and the paths' rows are 77).  fp64 exponentials stand eight side by side, as one alone waits
 // for itself.
 struct VerifyArgs {
@@ -666,7 +666,10 @@ __device__ __forceinline__ End finish_path(const VerifyArgs& a, uint32_t b, cons
 }
 
 // Up to this many segments every workgroup adds up a whole row itself sooner than a launch
-// more would give its sum.
+// more would give its sum.  The call, so and with the launch, for chains of up to 5 with draft
+// probabilities, us: 24 requests at 2 segments 40 and 50, at 4 42 and 50, at 6 48 and 53, at 8 49 and
+// 51, at 12 55 and 52, at 16 56 and 53; 96 requests at 4 51 and 58, at 6 58 and 58, at 8 66 and 63, at
+// 12 81 and 65; one request at 8 36 and 33.
 constexpr uint32_t kFew = 8;
 
 // Weights of a path's last row, a workgroup a segment; where they are p without the refused

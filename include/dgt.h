@@ -394,7 +394,17 @@ int dgt_rope_store(const void* d_q, const void* d_k, const void* d_v, uint32_t s
  * keys: what dgt_tree_attention computes without a mask, with its layouts and the
  * same values up to rounding, made for many new tokens a request: tiles of rows end at
  * their own last key, and long ones are split over the keys.
- *   d_ws: dgt_chunk_attention_workspace(...) bytes, any contents.
+ * Which of the two (bf16, 32 query heads on 8 of 128): up to 16 new tokens a request
+ * dgt_tree_attention takes less (32 requests behind 4000 tokens: one token 105 us, here 166;
+ * 16 tokens 107, here 152), from 128 on this one (4000 of one prompt: 177 us, there 491); between
+ * them it depends on the batch.  A step that mixes pieces of prompts with single tokens is best cut
+ * where they differ most: 500 tokens behind 2000 and 32 single ones behind 4000 take 130 us there
+ * and 192 here, 2000 tokens of a prompt beside them 260 and 189.
+ *   d_ws: dgt_chunk_attention_workspace(...) bytes, any contents.  It has room for the parts of
+ *          split tiles whatever the lengths are, and little of its size hangs on the arguments:
+ *          68 MB for heads of up to 64 elements, 136 up to 128, 270 up to 256.  One serves all
+ *          layers and steps of a stream.
+ * Offsets whose rows are more than `tokens` (they fall somewhere) are not computed: nothing is written.
  * Three launches; the order of all sums is fixed by the lengths and shapes.
  * Errors: E_ARG, E_SHAPE, E_BUFSIZE, E_UNSUPPORTED, E_HIP. */
 size_t dgt_chunk_attention_workspace(uint32_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim,
@@ -492,8 +502,9 @@ int dgt_page_fork(const int32_t* d_src, const int32_t* d_dst, uint32_t forks, in
                   uint32_t heads, uint32_t dim, uint32_t blocks, uint32_t block, void* d_k_cache,
                   void* d_v_cache, int32_t* d_counts, void* stream);
 
-/* End of requests: the pages of rows d_rows lose a holder, and those that nobody else holds
- * go back to the list, in the order of their ids.  Their lengths become 0, their columns
+/* End of requests: the pages of rows d_rows, as far as their lengths go (pages that a plan took
+ * for a step go back with dgt_page_keep, d_kept 0, first), lose a holder, and those that nobody else
+ * holds go back to the list, in the order of their ids.  Their lengths become 0, their columns
  * of the table -1.  Rows out of range or named before are passed over.
  *   d_counts: int32[2]: the list's new head, the pages that went back.
  *   d_ws: dgt_page_free_workspace(blocks) bytes, zero-filled before its first use; every
